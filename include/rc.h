@@ -384,6 +384,139 @@ rc_status rc_profile_end(void* handle, rc_profile* out);
 
 rc_status rc_cache_destroy(void* handle);
 
+/* ------------------------------------------------------------------------
+ * Paged-cache operators: many streams in one pool of pages.
+ *
+ * The ring of rc_step holds one stream. A server of many streams, or of
+ * several continuations of one, keeps their keys and values in pages of one
+ * pool instead, lists each stream's pages in a table and shares pages between
+ * streams. These calls need no handle: the pool, the tables and every tensor
+ * are the caller's; each call's scratch is a workspace of the caller's, so two
+ * calls on two streams, or two captured graphs, are independent as long as
+ * their workspaces are.
+ *
+ * Passages: RoPE over (t, h, w), the append of roped keys and values and the
+ * block-causal attention over them are those of rc_step (Causal-Forcing
+ * walkthrough, section 3); sink frames and window of frames are LingBot's
+ * sink_size and local_attn_size. The pages describe no paged cache: its
+ * layout is this library's own.
+ *
+ * Conventions beside those above
+ *   - Element types: RC_BF16 and RC_F16, and RC_F32 for rc_rope_axes only; one type per call.
+ *   - Strides are in elements and multiples of 16 bytes, at least 0 where only
+ *     read by plain loads (x of rc_rope_axes; q, k, v of rc_paged_append), else at least head_dim; the last dimension (head_dim) is
+ *     contiguous; every tensor starts on a 16-byte boundary.
+ *   - Lengths, tables and positions are int32 device arrays, read when the
+ *     kernels run: a captured call sees their values of each replay.
+ *   - What such an array holds out of range (a position outside its rotation
+ *     table, a page that is none, a length beyond the table) is brought into
+ *     range or left out as each call says, never followed, and sets *status
+ *     (a device word of the caller's, 0 before; NULL: not reported) to
+ *     RC_ERANGE; a wait that gives up sets it to RC_ETIMEOUT.
+ *   - Calls launch on `stream`, which must belong to the current device, as
+ *     must every pointer.
+ * ------------------------------------------------------------------------ */
+typedef enum rc_dtype { RC_BF16 = 0, RC_F16 = 1, RC_F32 = 2 } rc_dtype;
+
+/* Which two elements of a head a pair turns: (2m, 2m + 1) or (m, m + head_dim / 2). */
+typedef enum rc_pairing { RC_PAIR_ADJACENT = 0, RC_PAIR_HALVES = 1 } rc_pairing;
+
+/* Rotary positions over 1 to 3 axes (time, height, width, in any order): the
+ * first pairs[0] of the head_dim / 2 pairs turn by the token's position on axis
+ * 0, the next pairs[1] by axis 1, ... Their sum is head_dim / 2. */
+typedef struct rc_rope {
+  const int32_t* pos;     /* [n_tok][n_axes] */
+  const float* table[3];  /* axis a: [n_pos[a]][pairs[a]][2] (cos, sin); 8-byte aligned */
+  int32_t n_pos[3];
+  int32_t pairs[3];
+  int32_t n_axes;         /* 0: no rotation (rc_paged_append only) */
+  int32_t pairing;        /* rc_pairing */
+} rc_rope;
+
+/* [n_tok][heads][head_dim] */
+typedef struct rc_rows {
+  void* data;
+  int64_t tok_stride, head_stride;
+  int32_t heads;          /* 0: absent */
+} rc_rows;
+
+/* A pool of pages and the batch of sequences that lives in it. Token i of
+ * sequence b is row i % page_size of page page_table[b * table_stride + i /
+ * page_size]. The batch's queries are packed: those of sequence b are rows
+ * cu_q[b] .. cu_q[b + 1] - 1, its last tokens, so query row r is at position
+ * kv_len[b] - (cu_q[b + 1] - r). Rows from cu_q[n_seqs] on are left as they are. */
+typedef struct rc_paged {
+  void* k_pages;          /* [n_pages][kv_heads][page_size][head_dim] by strides */
+  void* v_pages;
+  int64_t k_stride[3];    /* of pages, heads, rows */
+  int64_t v_stride[3];
+  int32_t n_pages;
+  int32_t page_size;      /* 16, 32, 64 or 128 */
+  int32_t kv_heads;
+  int32_t head_dim;       /* 64 or 128 */
+  int32_t dtype;          /* RC_BF16 or RC_F16 */
+  int32_t n_seqs;
+  const int32_t* cu_q;    /* [n_seqs + 1], ascending from 0 */
+  const int32_t* kv_len;  /* [n_seqs] tokens in the pages, this call's among them */
+  const int32_t* page_table;
+  int64_t table_stride;
+  int32_t max_pages;      /* entries of a table row; max_pages * page_size <= 2^30 */
+} rc_paged;
+
+/* y = x turned by its positions, or back (inverse != 0: the transpose, which
+ * is the gradient with respect to x). Up to two tensors (queries and keys) in
+ * one launch: x[1].heads = 0 for one. y may be x with x's strides, else must not
+ * overlap it. Positions out of their table are clamped to it. */
+rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, int inverse, const rc_rows x[2],
+                       const rc_rows y[2], int32_t* status, void* stream);
+
+/* Appends a batch's new tokens: writes the turned keys and the values into
+ * their page rows and the turned queries to q_out (q, q_out: heads = 0 for
+ * none; q_out may be q). Without rotation (rope NULL or n_axes 0) all three are copied. A
+ * token whose place is none (position below 0 or past the table row, an entry outside
+ * [0, n_pages)) is kept out of the pool. Two tokens of one call with the same
+ * place: one of them is kept. */
+rc_status rc_paged_append(const rc_paged* p, const rc_rope* rope, int n_tok, const rc_rows* q, const rc_rows* k,
+                          const rc_rows* v, const rc_rows* q_out, int32_t* status, void* stream);
+
+/* What a query sees. With f = position / frame_seqlen it sees the keys of its
+ * sequence in frames <= f (its own frame whole; frame_seqlen 1 is causal
+ * attention token by token, one beyond every length is full attention). With
+ * window_frames > 0 only the last window_frames of them, its own included, and the first
+ * sink_frames frames. Entries of pages that no query of the call sees are not
+ * read and may hold anything.
+ *
+ * A prefix (prefix_len > 0) is one more run of keys that every query of the
+ * batch sees whole, held once in the pages prefix_table lists, and multiplied
+ * with all the batch's queries at once. Frames, window and positions count
+ * from the sequences' own tokens. */
+typedef struct rc_paged_mask {
+  int32_t frame_seqlen, sink_frames, window_frames;
+  int32_t max_q;                /* no sequence has more queries (a hint where it may be more; see below) */
+  float scale;                  /* of q . k; 0: 1 / sqrt(head_dim) */
+  int32_t prefix_len;
+  const int32_t* prefix_table;  /* [prefix_pages] */
+  int32_t prefix_pages;         /* at least prefix_len / page_size, rounded up */
+} rc_paged_mask;
+
+/* Bytes of workspace rc_paged_attention needs (256-byte aligned, contents not
+ * kept or read from call to call). It depends on the device only by its SM count. */
+rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n_tok, int q_heads, size_t* bytes);
+
+/* out = softmax(scale q k^T + mask) v over the batch's pages. Query head h
+ * reads key head h / (q_heads / kv_heads). A query that sees no key gets
+ * zeros and lse -inf. Keys that no query of its tile sees (behind a sequence, before its
+ * windows, rows not written yet) do not reach the result whatever their bits;
+ * a key that some query sees must be finite, or the NaN it makes can reach the
+ * queries of the same sequence that are computed with it.
+ *   lse: NULL or [q_heads][n_tok] fp32, natural log.
+ * max_q * (q_heads / kv_heads) <= 16 takes the kernel for few rows; it
+ * computes no more than that many, so max_q must not be below the longest
+ * (queries beyond are left out, with RC_ERANGE in *status). */
+rc_status rc_paged_attention(const rc_paged* p, const rc_paged_mask* mask, int n_tok, const rc_rows* q,
+                             const rc_rows* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream);
+
 /* Message for the calling thread's last failed call ("" if none). */
 const char* rc_last_error(void);
 

@@ -17,6 +17,8 @@ LIB_PATH = os.path.join(HERE, "librc.so")
 RC_OK, RC_EINVAL, RC_ESTATE, RC_ECUDA, RC_ERANGE, RC_ETIMEOUT, RC_ENOMEM = range(7)
 RC_NONE, RC_SLIDING, RC_ROLLING_SINK, RC_INFINITY_ROPE, RC_DEEP_FORCING, RC_RELAX_FORCING, RC_MEMROPE = range(7)
 RC_REINDEX_FLUSH, RC_REINDEX_CUT, RC_REINDEX_SINK = 1, 2, 4
+RC_BF16, RC_F16, RC_F32 = range(3)
+RC_PAIR_ADJACENT, RC_PAIR_HALVES = range(2)
 RC_MAX_SLOTS = 256
 RC_MAX_CHUNK_FRAMES = 16
 
@@ -79,11 +81,35 @@ class rc_profile(ctypes.Structure):
                 ("bytes", ctypes.c_double * _NK)]
 
 
+class rc_rope(ctypes.Structure):
+    _fields_ = [("pos", ctypes.c_void_p), ("table", ctypes.c_void_p * 3), ("n_pos", ctypes.c_int32 * 3),
+                ("pairs", ctypes.c_int32 * 3), ("n_axes", ctypes.c_int32), ("pairing", ctypes.c_int32)]
+
+
+class rc_rows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("tok_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("heads", ctypes.c_int32)]
+
+
+class rc_paged(ctypes.Structure):
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_stride", ctypes.c_int64 * 3),
+                ("v_stride", ctypes.c_int64 * 3), ("n_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("n_seqs", ctypes.c_int32), ("cu_q", ctypes.c_void_p), ("kv_len", ctypes.c_void_p),
+                ("page_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64), ("max_pages", ctypes.c_int32)]
+
+
+class rc_paged_mask(ctypes.Structure):
+    _fields_ = [("frame_seqlen", ctypes.c_int32), ("sink_frames", ctypes.c_int32),
+                ("window_frames", ctypes.c_int32), ("max_q", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("prefix_len", ctypes.c_int32), ("prefix_table", ctypes.c_void_p), ("prefix_pages", ctypes.c_int32)]
+
+
 EXPORTS = ["rc_config_init", "rc_cache_bytes", "rc_cache_create", "rc_step", "rc_step_noalloc",
            "rc_select_topc", "rc_reindex", "rc_comp_tokens", "rc_pool_scores",
            "rc_get_state", "rc_device_status", "rc_rope_table", "rc_cache_layout",
            "rc_watchdog_selftest", "rc_profile_begin", "rc_profile_end", "rc_cache_destroy",
-           "rc_last_error"]
+           "rc_rope_axes", "rc_paged_append", "rc_paged_workspace", "rc_paged_attention", "rc_last_error"]
 
 _lib = None
 
@@ -113,6 +139,11 @@ def lib() -> ctypes.CDLL:
         L.rc_profile_begin.argtypes = [vp, i]
         L.rc_profile_end.argtypes = [vp, ctypes.POINTER(rc_profile)]
         L.rc_cache_destroy.argtypes = [vp]
+        pr, pp, pm, prope = (ctypes.POINTER(t) for t in (rc_rows, rc_paged, rc_paged_mask, rc_rope))
+        L.rc_rope_axes.argtypes = [prope, i, i, i, i, pr, pr, vp, vp]
+        L.rc_paged_append.argtypes = [pp, prope, i, pr, pr, pr, pr, vp, vp]
+        L.rc_paged_workspace.argtypes = [pp, pm, i, i, ctypes.POINTER(sz)]
+        L.rc_paged_attention.argtypes = [pp, pm, i, pr, pr, vp, vp, sz, vp, vp]
         L.rc_last_error.argtypes = []
         L.rc_last_error.restype = ctypes.c_char_p
         for name in EXPORTS[:-1]:
@@ -224,6 +255,28 @@ def rc_profile_end(handle) -> dict:
     check(lib().rc_profile_end(handle, ctypes.byref(p)))
     return {n: dict(launches=p.launches[i], timed=p.timed[i], ms=p.ms[i], flops=p.flops[i],
                     bytes=p.bytes[i]) for i, n in enumerate(RC_KERNEL_NAMES)}
+
+
+def rc_rope_axes(rope: rc_rope, dtype, n_tok, head_dim, inverse, x, y, status=0, stream=0) -> None:
+    """x, y: (rc_rows * 2) arrays."""
+    check(lib().rc_rope_axes(rope, dtype, n_tok, head_dim, inverse, x, y, status or None, stream or None))
+
+
+def rc_paged_append(paged: rc_paged, rope: Optional[rc_rope], n_tok, q: rc_rows, k: rc_rows, v: rc_rows,
+                    q_out: rc_rows, status=0, stream=0) -> None:
+    check(lib().rc_paged_append(paged, rope, n_tok, q, k, v, q_out, status or None, stream or None))
+
+
+def rc_paged_workspace(paged: rc_paged, mask: rc_paged_mask, n_tok, q_heads) -> int:
+    n = ctypes.c_size_t()
+    check(lib().rc_paged_workspace(paged, mask, n_tok, q_heads, ctypes.byref(n)))
+    return n.value
+
+
+def rc_paged_attention(paged: rc_paged, mask: rc_paged_mask, n_tok, q: rc_rows, out: rc_rows, lse, workspace,
+                       nbytes, status=0, stream=0) -> None:
+    check(lib().rc_paged_attention(paged, mask, n_tok, q, out, lse or None, workspace or None, nbytes,
+                                   status or None, stream or None))
 
 
 def rc_cache_destroy(handle) -> None:

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 OUT = os.path.join(HERE, "librc.so")
 SOURCES = ["engine.cpp", "api.cu", "rope_kernels.cu", "attn_fwd.cu", "score_kernel.cu", "topc_kernel.cu",
            "rf_kernels.cu",
-           "noalloc.cu"]
+           "noalloc.cu", "paged_api.cu", "paged_rope.cu", "paged_decode.cu", "paged_attn.cu", "paged_combine.cu"]
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
 

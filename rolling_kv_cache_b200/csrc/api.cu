@@ -260,6 +260,10 @@ rc_status check_device(const Cache* c) {
 
 }  // namespace
 
+namespace rc {
+rc_status SetLastError(rc_status st, const char* message) { return set_err(st, message); }
+}  // namespace rc
+
 extern "C" {
 
 const char* rc_last_error(void) { return g_err.c_str(); }

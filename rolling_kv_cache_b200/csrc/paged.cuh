@@ -1,0 +1,110 @@
+// Kernel parameter blocks and launchers of the paged-cache operators: rotary
+// positions over several axes, the append that rotates keys into the pages,
+// and attention over pages. Metadata of a call travels by value; lengths,
+// page tables and positions are device arrays, so that a captured call sees
+// their values of each replay.
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "../../include/rc.h"
+#include "kernels.cuh"
+
+namespace rc {
+
+// Most sequences one attention call takes: their tile counts are scanned in shared memory.
+constexpr int kMaxSeqs = 4096;
+
+struct AxisTables {
+  const int32_t* pos;      // [n_tok][n_axes]
+  const float2* table[3];  // [n_pos][pairs] (cos, sin)
+  int n_pos[3];
+  int pairs[3];
+  int n_axes;
+};
+
+struct RowsView {
+  uint8_t* data;
+  long long tok_stride, head_stride;  // bytes
+  int heads;
+};
+
+// Rotary positions of up to two tensors of rows (queries and keys).
+struct RopeAxesParams {
+  AxisTables ax;
+  RowsView x[2], y[2];
+  int* status;
+  int n_tok, splits;
+  float sign;  // of the sine: -1 turns back (the transpose)
+};
+
+struct PageView {
+  uint8_t* data;
+  long long page_stride, head_stride, row_stride;  // bytes
+};
+
+struct BatchView {
+  const int32_t* cu_q;        // [n_seqs + 1]
+  const int32_t* kv_len;      // [n_seqs]
+  const int32_t* page_table;  // [n_seqs][table_stride]
+  long long table_stride;
+  int n_seqs, max_pages, n_pages;
+  int page_log2;
+};
+
+struct PagedAppendParams {
+  AxisTables ax;
+  RowsView q, k, v, q_out;
+  PageView kp, vp;
+  BatchView b;
+  int* status;
+  int n_tok, splits;
+};
+
+// The mask: with f = position / frame, a query sees the keys of frames <= its
+// own, and under a window (> 0 frames) only the last `window` of those frames
+// and the first sink_tok tokens.
+struct MaskView {
+  int frame, sink_tok, window;
+};
+
+// Attention over pages: one call's inputs and outputs.
+struct alignas(64) PagedAttnParams {
+  CUtensorMap tm_q;    // prefill only: q as (d, q_heads, n_tok), box {64, G, 128 / G}
+  CUtensorMap tm_k;    // pages as (d, page, heads, n_pages), box {64, box_rows, 1, 1}
+  CUtensorMap tm_v;
+  BatchView b;
+  RowsView q, out;     // byte strides
+  MaskView mask;
+  float* lse;          // [q_heads][n_tok] or null
+  int* status;
+  float* part_o;       // [2 * n_ctas][rows][d] fp32: parts of units cut between CTAs, each divided by its sum
+  float* part_lse;     // [2 * n_ctas][rows], log2-sum-exp of each part
+  int4* rec;           // [n_ctas] what of its range a CTA left in parts (PartRecord)
+  // result over the shared prefix to merge at the last write: fp32 [n_tok][q_heads][d] and [q_heads][n_tok] log2
+  const float* prev_o;
+  const float* prev_lse;
+  // or, when this call is the pass over a prefix: where that result goes (then out and lse are unused)
+  float* pre_o;
+  float* pre_lse;
+  int prefix_len;      // prefix pass: every query of the batch sees keys [0, prefix_len) of table row 0
+  int n_tok, Hk, G;
+  int box_rows;        // rows of a page per TMA box
+  float scale_log2;    // log2(e) * scale
+  int n_ctas;
+};
+
+// part_o / part_lse rows of one unit in the two attention kernels
+constexpr int kDecodeRows = 16;
+constexpr int kPrefillRows = 256;
+
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
+cudaError_t launch_paged_combine(const PagedAttnParams& p, bool bf16, int head_dim, bool decode, cudaStream_t s);
+
+cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, int head_dim, bool halves, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, int dtype, int head_dim, bool halves, cudaStream_t s);
+
+}  // namespace rc

@@ -1,0 +1,362 @@
+// C entries of the paged-cache operators (include/rc.h): argument checks,
+// TMA descriptors, workspace layout and launches. Host code.
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <climits>
+#include <cmath>
+#include <cstring>
+#include <exception>
+#include <mutex>
+#include <string>
+
+#include "paged.cuh"
+
+namespace rc {
+rc_status SetLastError(rc_status st, const char* message);  // api.cu
+}
+
+namespace {
+
+using rc::SetLastError;
+
+rc_status invalid(const char* m) { return SetLastError(RC_EINVAL, m); }
+
+rc_status cuda_failed(cudaError_t e, const char* what) {
+  return SetLastError(RC_ECUDA, (std::string(what) + ": " + cudaGetErrorString(e)).c_str());
+}
+
+// Runs an entry's body; nothing it throws crosses the C ABI.
+template <typename Fn>
+rc_status guarded(Fn f) {
+  try {
+    return f();
+  } catch (const std::exception& e) {
+    return SetLastError(RC_ENOMEM, e.what());
+  } catch (...) {
+    return SetLastError(RC_ENOMEM, "unknown exception");
+  }
+}
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
+
+int elem_size(int dtype) { return dtype == RC_F32 ? 4 : 2; }
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// `distinct`: rows that are written, or copied by TMA: every stride over more than one entry is at least a row.
+rc_status check_rows(const rc_rows& r, int n_tok, int d, int size, bool distinct, const char* what) {
+  const std::string name(what);
+  if (r.heads < 0 || r.heads > 16384) return invalid((name + ": heads out of range").c_str());
+  if (r.heads == 0 || n_tok == 0) return RC_OK;
+  if (!r.data) return invalid((name + ": null tensor").c_str());
+  if (!aligned16(r.data) || r.tok_stride * size % 16 || r.head_stride * size % 16)
+    return invalid((name + ": start and strides must be multiples of 16 bytes").c_str());
+  const int64_t most = (int64_t)1 << 40;
+  if (r.tok_stride < 0 || r.head_stride < 0 || r.tok_stride > most || r.head_stride > most)
+    return invalid((name + ": stride out of range").c_str());
+  if (distinct && ((n_tok > 1 && r.tok_stride < d) || (r.heads > 1 && r.head_stride < d)))
+    return invalid((name + ": the rows overlap").c_str());
+  return RC_OK;
+}
+
+rc::RowsView view(const rc_rows& r, int size) {
+  return rc::RowsView{static_cast<uint8_t*>(r.data), r.tok_stride * size, r.head_stride * size, r.heads};
+}
+
+rc_status make_axes(const rc_rope* rope, int n_tok, int head_dim, rc::AxisTables* ax) {
+  std::memset(ax, 0, sizeof(*ax));
+  if (!rope || rope->n_axes == 0) return RC_OK;
+  if (rope->n_axes < 0 || rope->n_axes > 3) return invalid("rope: n_axes must be 1 to 3");
+  if (rope->pairing != RC_PAIR_ADJACENT && rope->pairing != RC_PAIR_HALVES) return invalid("rope: unknown pairing");
+  if (n_tok > 0 && (!rope->pos || reinterpret_cast<uintptr_t>(rope->pos) % 4)) return invalid("rope: null or misaligned positions");
+  int sum = 0;
+  for (int a = 0; a < rope->n_axes; ++a) {
+    if (rope->pairs[a] < 0 || rope->pairs[a] > head_dim / 2) return invalid("rope: pairs out of range");
+    if (rope->n_pos[a] < 1) return invalid("rope: an empty table");
+    if (rope->pairs[a] > 0 && !rope->table[a]) return invalid("rope: null table");
+    if (reinterpret_cast<uintptr_t>(rope->table[a]) % 8)
+      return invalid("rope: misaligned table");
+    sum += rope->pairs[a];
+    ax->table[a] = reinterpret_cast<const float2*>(rope->table[a]);
+    ax->n_pos[a] = rope->n_pos[a];
+    ax->pairs[a] = rope->pairs[a];
+  }
+  if (sum != head_dim / 2) return invalid("rope: pairs must sum to head_dim / 2");
+  ax->pos = rope->pos;
+  ax->n_axes = rope->n_axes;
+  return RC_OK;
+}
+
+// The pool and the batch; *b receives the kernels' view.
+rc_status check_paged(const rc_paged* p, int n_tok, rc::BatchView* b) {
+  if (!p) return invalid("null argument");
+  if (p->dtype != RC_BF16 && p->dtype != RC_F16) return invalid("pages are bf16 or fp16");
+  if (p->head_dim != 64 && p->head_dim != 128) return invalid("head_dim must be 64 or 128");
+  if (p->page_size != 16 && p->page_size != 32 && p->page_size != 64 && p->page_size != 128)
+    return invalid("page_size must be 16, 32, 64 or 128");
+  if (p->kv_heads < 1 || p->kv_heads > 1024) return invalid("kv_heads must be in [1, 1024]");
+  if (p->n_pages < 1) return invalid("an empty pool");
+  if (!p->k_pages || !p->v_pages || !aligned16(p->k_pages) || !aligned16(p->v_pages))
+    return invalid("the pages must be 16-byte aligned");
+  const int entries[3] = {p->n_pages, p->kv_heads, p->page_size};
+  for (const int64_t* st : {p->k_stride, p->v_stride})
+    for (int i = 0; i < 3; ++i)
+      if (entries[i] > 1 && (st[i] < p->head_dim || st[i] % 8 || st[i] >= ((int64_t)1 << 38)))
+        return invalid("page strides must be multiples of 16 bytes, of at least a row");
+  if (n_tok < 0 || n_tok > (1 << 30)) return invalid("n_tok out of range");
+  if (p->n_seqs < 0 || p->n_seqs > rc::kMaxSeqs) return invalid("n_seqs must be in [0, 4096]");
+  if (p->n_seqs > 0 && (!p->cu_q || !p->kv_len)) return invalid("null cu_q or kv_len");
+  if (p->max_pages < 0) return invalid("max_pages must not be negative");
+  if ((int64_t)p->max_pages * p->page_size > (1 << 30))
+    return SetLastError(RC_ERANGE, "max_pages * page_size exceeds 2^30");
+  if (p->n_seqs > 0 && p->max_pages > 0 && !p->page_table) return invalid("null page_table");
+  if (p->table_stride < 0 || (p->n_seqs > 1 && p->table_stride < p->max_pages && p->table_stride != 0))
+    return invalid("table_stride below max_pages");
+  int lg = 4;
+  while ((1 << lg) < p->page_size) ++lg;
+  *b = rc::BatchView{p->cu_q, p->kv_len, p->page_table, p->table_stride, p->n_seqs, p->max_pages, p->n_pages, lg};
+  return RC_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+  });
+  return fn;
+}
+
+// A map over `rank` dimensions, innermost first; strides in elements of dimensions 1..rank - 1. A dimension of one
+// entry may come with any stride: it gets one that the encoder takes.
+rc_status encode(CUtensorMap* map, void* base, int dtype, int rank, const int64_t* dims, const int64_t* strides,
+                 const int* box) {
+  auto fn = encode_fn();
+  if (!fn) return SetLastError(RC_ECUDA, "cuTensorMapEncodeTiled is unavailable");
+  cuuint64_t d[5], st[4];
+  cuuint32_t bx[5], es[5];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = (cuuint64_t)dims[i];
+    bx[i] = (cuuint32_t)box[i];
+    es[i] = 1;
+    if (i > 0) st[i - 1] = (cuuint64_t)(dims[i] > 1 ? strides[i - 1] : dims[0]) * 2;
+  }
+  const CUresult r = fn(map, dtype == RC_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+                        rank, base, d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return SetLastError(RC_ECUDA, ("cuTensorMapEncodeTiled failed: " + std::to_string(r)).c_str());
+  return RC_OK;
+}
+
+cudaError_t sm_count(int* n) {
+  static rc::PerDevice cache;
+  return cache.get(n, [](int dev, int* x) { return cudaDeviceGetAttribute(x, cudaDevAttrMultiProcessorCount, dev); });
+}
+
+// Where the parts of an attention call lie in its workspace.
+struct Work {
+  bool decode, prefix;
+  int n_ctas, group;
+  size_t part_o, part_lse, rec, pre_o, pre_lse, total;
+};
+
+rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_heads, Work* w) {
+  rc::BatchView b;
+  if (rc_status st = check_paged(p, n_tok, &b)) return st;
+  if (!m) return invalid("null mask");
+  if (q_heads < 1 || q_heads % p->kv_heads) return invalid("q_heads must be a multiple of kv_heads");
+  w->group = q_heads / p->kv_heads;
+  if (w->group > 128) return invalid("q_heads / kv_heads must be at most 128");
+  if (m->frame_seqlen < 1 || m->frame_seqlen > (1 << 30)) return invalid("frame_seqlen must be in [1, 2^30]");
+  if (m->sink_frames < 0 || m->window_frames < 0) return invalid("sink_frames and window_frames must not be negative");
+  if (m->sink_frames > 0 && m->window_frames == 0) return invalid("sink_frames need a window");
+  if (m->max_q < 0) return invalid("max_q must not be negative");
+  if (!(m->scale >= 0.f) || !std::isfinite(m->scale)) return invalid("scale must be finite and not negative");
+  if (m->prefix_len < 0 || m->prefix_pages < 0) return invalid("prefix_len must not be negative");
+  if (m->prefix_len > 0 &&
+      (!m->prefix_table || (int64_t)m->prefix_pages * p->page_size < m->prefix_len || m->prefix_len > (1 << 30)))
+    return invalid("prefix_table must list the pages of prefix_len tokens");
+  w->decode = (int64_t)std::max(1, m->max_q) * w->group <= rc::kDecodeRows;
+  w->prefix = m->prefix_len > 0;
+  // positions of the stream-K split are 32-bit: tiles of every unit, summed
+  const int64_t tiles = (int64_t)std::max(p->max_pages, m->prefix_pages) * p->page_size / 64 + 1;
+  const int64_t pairs = (int64_t)n_tok / std::max(1, 2 * (128 / w->group)) + p->n_seqs + 1;
+  if ((w->decode ? tiles * p->n_seqs : tiles * pairs) * p->kv_heads >= INT_MAX)
+    return SetLastError(RC_ERANGE, "the batch has too many key tiles for one call");
+  int sms = 0;
+  if (cudaError_t e = sm_count(&sms)) return cuda_failed(e, "device attribute");
+  w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
+  const size_t rows = (size_t)2 * w->n_ctas * (w->decode && !w->prefix ? rc::kDecodeRows : rc::kPrefillRows);
+  size_t o = 0;
+  w->part_o = o;
+  o += align_up(rows * p->head_dim * 4);
+  w->part_lse = o;
+  o += align_up(rows * 4);
+  w->rec = o;
+  o += align_up((size_t)w->n_ctas * sizeof(int4));
+  w->pre_o = o;
+  if (w->prefix) o += align_up((size_t)n_tok * q_heads * p->head_dim * 4);
+  w->pre_lse = o;
+  if (w->prefix) o += align_up((size_t)n_tok * q_heads * 4);
+  w->total = o;
+  return RC_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, int inverse, const rc_rows x[2],
+                       const rc_rows y[2], int32_t* status, void* stream) {
+  return guarded([&]() -> rc_status {
+    if (!rope || !x || !y) return invalid("null argument");
+    if (dtype != RC_BF16 && dtype != RC_F16 && dtype != RC_F32) return invalid("unknown dtype");
+    if (head_dim != 64 && head_dim != 128) return invalid("head_dim must be 64 or 128");
+    if (n_tok < 0 || n_tok > (1 << 30)) return invalid("n_tok out of range");
+    rc::RopeAxesParams p{};
+    if (rope->n_axes == 0) return invalid("rope: n_axes must be 1 to 3");
+    if (rc_status st = make_axes(rope, n_tok, head_dim, &p.ax)) return st;
+    const int size = elem_size(dtype);
+    for (int i = 0; i < 2; ++i) {
+      if (rc_status st = check_rows(x[i], n_tok, head_dim, size, false, "x")) return st;
+      if (rc_status st = check_rows(y[i], n_tok, head_dim, size, true, "y")) return st;
+      if (x[i].heads != y[i].heads) return invalid("x and y differ in heads");
+      p.x[i] = view(x[i], size);
+      p.y[i] = view(y[i], size);
+    }
+    p.status = status;
+    p.n_tok = n_tok;
+    p.sign = inverse ? -1.f : 1.f;
+    if (cudaError_t e = rc::launch_rope_axes(p, dtype, head_dim, rope->pairing == RC_PAIR_HALVES,
+                                             static_cast<cudaStream_t>(stream)))
+      return cuda_failed(e, "rope launch");
+    return RC_OK;
+  });
+}
+
+rc_status rc_paged_append(const rc_paged* pg, const rc_rope* rope, int n_tok, const rc_rows* q, const rc_rows* k,
+                          const rc_rows* v, const rc_rows* q_out, int32_t* status, void* stream) {
+  return guarded([&]() -> rc_status {
+    rc::PagedAppendParams p{};
+    if (rc_status st = check_paged(pg, n_tok, &p.b)) return st;
+    if (!q || !k || !v || !q_out) return invalid("null argument");
+    if (rc_status st = make_axes(rope, n_tok, pg->head_dim, &p.ax)) return st;
+    if (rc_status st = check_rows(*q, n_tok, pg->head_dim, 2, false, "q")) return st;
+    if (rc_status st = check_rows(*q_out, n_tok, pg->head_dim, 2, true, "q_out")) return st;
+    if (rc_status st = check_rows(*k, n_tok, pg->head_dim, 2, false, "k")) return st;
+    if (rc_status st = check_rows(*v, n_tok, pg->head_dim, 2, false, "v")) return st;
+    if (q->heads != q_out->heads) return invalid("q and q_out differ in heads");
+    if (k->heads != pg->kv_heads || v->heads != pg->kv_heads) return invalid("k and v must have the pool's heads");
+    p.q = view(*q, 2);
+    p.q_out = view(*q_out, 2);
+    p.k = view(*k, 2);
+    p.v = view(*v, 2);
+    p.kp = rc::PageView{static_cast<uint8_t*>(pg->k_pages), pg->k_stride[0] * 2, pg->k_stride[1] * 2, pg->k_stride[2] * 2};
+    p.vp = rc::PageView{static_cast<uint8_t*>(pg->v_pages), pg->v_stride[0] * 2, pg->v_stride[1] * 2, pg->v_stride[2] * 2};
+    p.status = status;
+    p.n_tok = n_tok;
+    const bool halves = p.ax.n_axes > 0 && rope->pairing == RC_PAIR_HALVES;
+    if (cudaError_t e = rc::launch_paged_append(p, pg->dtype, pg->head_dim, halves, static_cast<cudaStream_t>(stream)))
+      return cuda_failed(e, "append launch");
+    return RC_OK;
+  });
+}
+
+rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n_tok, int q_heads, size_t* bytes) {
+  return guarded([&]() -> rc_status {
+    if (!bytes) return invalid("null argument");
+    Work w;
+    if (rc_status st = plan_work(p, mask, n_tok, q_heads, &w)) return st;
+    *bytes = w.total;
+    return RC_OK;
+  });
+}
+
+rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_tok, const rc_rows* q,
+                             const rc_rows* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* status,
+                             void* stream) {
+  return guarded([&]() -> rc_status {
+    if (!q || !out) return invalid("null argument");
+    Work w;
+    if (rc_status st = plan_work(pg, m, n_tok, q->heads, &w)) return st;
+    const int d = pg->head_dim;
+    if (rc_status st = check_rows(*q, n_tok, d, 2, true, "q")) return st;
+    if (rc_status st = check_rows(*out, n_tok, d, 2, true, "out")) return st;
+    if (q->heads != out->heads) return invalid("q and out differ in heads");
+    if (n_tok == 0 || pg->n_seqs == 0) return RC_OK;
+    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+      return invalid("the workspace must be 256-byte aligned");
+    if (workspace_bytes < w.total) return SetLastError(RC_ENOMEM, "workspace smaller than rc_paged_workspace()");
+    const bool bf16 = pg->dtype == RC_BF16;
+    rc::PagedAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (rc_status st = check_paged(pg, n_tok, &p.b)) return st;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.q = view(*q, 2);
+    p.out = view(*out, 2);
+    p.mask.frame = m->frame_seqlen;
+    p.mask.sink_tok = (int)std::min<int64_t>((int64_t)m->sink_frames * m->frame_seqlen, 1 << 30);
+    p.mask.window = m->window_frames;
+    p.lse = lse;
+    p.status = status;
+    p.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    p.rec = reinterpret_cast<int4*>(ws + w.rec);
+    p.n_tok = n_tok;
+    p.Hk = pg->kv_heads;
+    p.G = w.group;
+    p.n_ctas = w.n_ctas;
+    const double scale = m->scale > 0.f ? (double)m->scale : 1.0 / std::sqrt((double)d);
+    p.scale_log2 = (float)(1.4426950408889634 * scale);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+
+    auto maps = [&](int box_rows) -> rc_status {
+      p.box_rows = box_rows;
+      const int64_t dims[4] = {d, pg->page_size, pg->kv_heads, pg->n_pages};
+      const int box[4] = {64, box_rows, 1, 1};
+      const int64_t ks[3] = {pg->k_stride[2], pg->k_stride[1], pg->k_stride[0]};
+      const int64_t vs[3] = {pg->v_stride[2], pg->v_stride[1], pg->v_stride[0]};
+      if (rc_status st = encode(&p.tm_k, pg->k_pages, pg->dtype, 4, dims, ks, box)) return st;
+      return encode(&p.tm_v, pg->v_pages, pg->dtype, 4, dims, vs, box);
+    };
+    auto prefill = [&](const rc::PagedAttnParams& x) -> rc_status {
+      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "paged attention launch");
+      if (cudaError_t e = rc::launch_paged_combine(x, bf16, d, false, s)) return cuda_failed(e, "combine launch");
+      return RC_OK;
+    };
+    if (w.prefix || !w.decode) {
+      const int64_t dims[3] = {d, q->heads, n_tok};
+      const int64_t st3[2] = {q->head_stride, q->tok_stride};
+      const int box[3] = {64, w.group, 128 / w.group};
+      if (rc_status st = encode(&p.tm_q, q->data, pg->dtype, 3, dims, st3, box)) return st;
+      if (rc_status st = maps(pg->page_size)) return st;
+    }
+    if (w.prefix) {
+      rc::PagedAttnParams x = p;  // every query of the batch against the prefix's pages
+      x.b.page_table = m->prefix_table;
+      x.b.max_pages = m->prefix_pages;
+      x.b.table_stride = 0;
+      x.prefix_len = m->prefix_len;
+      x.mask = rc::MaskView{1 << 30, 0, 0};
+      x.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
+      x.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+      if (rc_status st = prefill(x)) return st;
+      p.prev_o = x.pre_o;
+      p.prev_lse = x.pre_lse;
+    }
+    if (!w.decode) return prefill(p);
+    if (rc_status st = maps(std::min(pg->page_size, 64))) return st;
+    if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, s)) return cuda_failed(e, "paged attention launch");
+    if (cudaError_t e = rc::launch_paged_combine(p, bf16, d, true, s)) return cuda_failed(e, "combine launch");
+    return RC_OK;
+  });
+}
+
+}  // extern "C"

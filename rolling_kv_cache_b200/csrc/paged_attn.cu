@@ -1,0 +1,680 @@
+// Attention over pages for many query rows per key head (tcgen05 + TMEM + TMA):
+// prompts, chunks of video frames, and a batch's queries against a shared
+// prefix.
+//
+//   o = sum_j exp(x_j) v_j / sum_j exp(x_j),  x_j = scale q . k_j,
+// over the keys the mask leaves, one pass, running maximum and sum. Bound by the tensor cores and
+// the exponentials: 4 * head_dim operations and one exponential a pair.
+//
+// A unit of work is a pair of 128-row query tiles (Q0, Q1) of one key head,
+// sharing every K/V tile. A tile's rows are (query, query head of the key
+// head) pairs, query-major: 128 / G whole queries of G heads each, brought by one TMA box per
+// 64 dims, so that shared key heads are read once for all their query heads.
+//   warps 0-7   softmax of Q0 and epilogue: 32 query rows (TMEM lanes) x
+//               64 keys per warp
+//   warps 8-15  softmax of Q1, epilogue
+//   warp 16     TMA producer: Q0/Q1 once per unit, K and V tiles (128 keys, a
+//               box per page and 64 dims) into separate 2-stage rings
+//   warp 17     TMEM allocator; one thread issues every tcgen05.mma
+// TMEM (512 columns): S0 [0,128), S1 [128,256), O0 [256,256+d), O1 [384,384+d).
+// P_i (16-bit) overwrites columns [0,32) and [64,96) of S_i and is the A operand of
+// O_i += P_i V. MMA issue order per KV tile j: PV0(j), S0(j+1), PV1(j), S1(j+1),
+// so that while one softmax group turns S into P the tensor core runs the
+// other group's two products.
+//
+// Units differ in length (ragged batches, causal and window masks), so their
+// tiles, in (sequence, key head, pair) order, are cut into equal ranges, one per CTA;
+// every CTA finds its own range from the lengths on the device. A unit cut between CTAs
+// leaves its parts for the combine kernel.
+//
+// Keys that no query of the pair sees (behind the sequence, before its windows)
+// are masked in S, and their V rows are zeroed in shared memory before the
+// product, so that what their bits hold stays out; pages that are none are
+// filled with zeros by an out-of-range copy and masked.
+//
+// Every wait is bounded (2 s) and reports RC_ETIMEOUT through the status
+// word; no trap.
+#include "exp2_cubic.cuh"
+#include "paged_common.cuh"
+
+namespace rc {
+
+namespace {
+
+constexpr int kTileRows = 128;
+constexpr uint32_t kSubTileBytes = 128 * 64 * 2;  // 128 rows x 64 dims = one 128-byte-swizzle box
+constexpr int kSoftmaxWarps = 16;
+constexpr int kProducerWarp = 16;
+constexpr int kMmaWarp = 17;
+constexpr int kPreThreads = 18 * 32;
+constexpr float kRescaleLog2 = 8.0f;
+
+template <int D>
+struct PreLayout {
+  static constexpr int kSub = D / 64;
+  static constexpr uint32_t kTile = kSubTileBytes * kSub;
+  static constexpr uint32_t kQ = 0;              // Q0, Q1
+  static constexpr uint32_t kK = 2 * kTile;      // 2 stages
+  static constexpr uint32_t kV = 4 * kTile;      // 2 stages
+  static constexpr uint32_t kPre = 6 * kTile;    // tiles of the sequences, summed
+  static constexpr uint32_t kBytes = kPre + (kMaxSeqs + 1) * 4;
+  static constexpr uint32_t kDynSmem = kBytes + 1024;
+};
+
+// KV tiles [kv_lo, kv_hi) of one pair of query tiles of key head h of
+// sequence b. slot >= 0: the job covers part of its unit and leaves
+// (O / l, log2-sum-exp) in that slot; slot < 0: it writes the output.
+struct Job {
+  int b, h, q0;      // q0: row of q of the pair's first query
+  int tokens, at0;   // queries of the pair, position of the first
+  int L, kv_lo, kv_hi, slot;
+  bool has1, head, tail;  // head: begins inside the unit; tail: ends inside it
+  int place;              // h * pairs + pair
+  TileSpan<kTileRows> sp;
+};
+
+// The batch as the kernel sees it: the sequences, or, in the pass over a
+// shared prefix, one sequence of every query that sees the prefix whole (the
+// host sets a frame beyond every position and no window).
+__device__ __forceinline__ Seq pre_seq(const PagedAttnParams& p, int b) {
+  if (p.pre_o) {
+    Seq s;
+    const int n = __ldg(p.b.cu_q + p.b.n_seqs);
+    s.q0 = 0;
+    s.n = min(max(n, 0), p.n_tok);
+    s.L = p.prefix_len;
+    s.bad = s.n != n;
+    return s;
+  }
+  return load_seq(p.b, p.n_tok, b);
+}
+
+__device__ __forceinline__ void pair_span(const PagedAttnParams& p, const Seq& s, int pair, int tpt, Job& j) {
+  const int i0 = pair * 2 * tpt;
+  j.tokens = min(2 * tpt, s.n - i0);
+  j.at0 = (p.pre_o ? 0 : s.L - s.n) + i0;
+  j.sp.init(p.mask, j.at0, j.at0 + j.tokens - 1, s.L);
+}
+
+// Where a CTA's range begins.
+struct Start {
+  int b, h, pair, off;
+};
+
+struct PairWalk {
+  const PagedAttnParams* p;
+  int n_seqs, tpt, pos, end;
+  int b, h, pair, off, pairs;
+  Seq s;
+
+  __device__ void load() {
+    s = pre_seq(*p, b);
+    pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
+  }
+  __device__ void init(const PagedAttnParams& prm, const Start& st, int pos_, int end_) {
+    p = &prm;
+    n_seqs = prm.pre_o ? 1 : prm.b.n_seqs;
+    tpt = kTileRows / prm.G;
+    pos = pos_;
+    end = end_;
+    b = st.b;
+    h = st.h;
+    pair = st.pair;
+    off = st.off;
+    if (pos < end) load();
+  }
+  __device__ bool next(Job& j) {
+    if (pos >= end) return false;
+    while (pair >= pairs) {
+      pair = 0;
+      if (pairs == 0 || ++h == p->Hk) {
+        h = 0;
+        if (++b >= n_seqs) return false;
+        load();
+      }
+    }
+    pair_span(*p, s, pair, tpt, j);
+    const int total = max(j.sp.n, 1);
+    const int len = min(total - off, end - pos);
+    j.b = b;
+    j.h = h;
+    j.q0 = s.q0 + pair * 2 * tpt;
+    j.L = s.L;
+    j.kv_lo = off;
+    j.kv_hi = min(off + len, j.sp.n);
+    j.has1 = j.tokens > tpt;
+    j.head = off > 0;
+    j.tail = off + len < total;
+    j.slot = j.head ? 2 * (int)blockIdx.x : (j.tail ? 2 * (int)blockIdx.x + 1 : -1);
+    j.place = h * pairs + pair;
+    pos += len;
+    off = 0;
+    ++pair;
+    return true;
+  }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __grid_constant__ PagedAttnParams p) {
+  using L = PreLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bar_q, bar_qe, bar_kf[2], bar_vf[2], bar_ke[2], bar_ve[2], bar_s[2], bar_p[2], bar_o[2],
+      bar_fin, bar_pair[8];
+  __shared__ float swap_buf[2][2][2][kTileRows];  // [group][exchange parity][column half][row]
+  __shared__ uint32_t readable[4];                // bit i: page i of the tile is one; tile g at g % 4
+  __shared__ int warp_sums[18];
+  __shared__ Start start_sh;
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_sh;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t base_u32 = (ptx::smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* base = smem_raw + (base_u32 - ptx::smem_u32(smem_raw));
+
+  if (threadIdx.x == 0) {
+    ptx::mbar_init(&bar_q, 1);
+    ptx::mbar_init(&bar_qe, 1);
+    for (int i = 0; i < 2; ++i) {
+      ptx::mbar_init(&bar_kf[i], 1);
+      ptx::mbar_init(&bar_vf[i], 1);
+      ptx::mbar_init(&bar_ke[i], 1);
+      ptx::mbar_init(&bar_ve[i], 1);
+      ptx::mbar_init(&bar_s[i], 1);
+      ptx::mbar_init(&bar_p[i], 256);
+      ptx::mbar_init(&bar_o[i], 1);
+    }
+    ptx::mbar_init(&bar_fin, 1);
+    for (int i = 0; i < 8; ++i) ptx::mbar_init(&bar_pair[i], 64);
+    abort_sh = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc(&tmem_base_sh, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::grid_launch_dependents();
+  // key tiles of each sequence (one key head), a warp a sequence; their sums
+  // give this CTA its range of the batch's tiles
+  int* pre = reinterpret_cast<int*>(base + L::kPre);
+  const int n_seqs = p.pre_o ? 1 : p.b.n_seqs;
+  const int tpt = kTileRows / p.G;
+  for (int b = warp; b < n_seqs; b += kPreThreads / 32) {
+    const Seq s = pre_seq(p, b);
+    const int pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
+    int sum = 0;
+    for (int q = lane; q < pairs; q += 32) {
+      Job j;
+      pair_span(p, s, q, tpt, j);
+      sum += max(j.sp.n, 1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) pre[b] = sum;
+  }
+  __syncthreads();
+  block_prefix<kPreThreads>(pre, n_seqs, warp_sums, [&](int b) { return pre[b]; });
+  const int W = p.Hk * pre[n_seqs];
+  const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
+  const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
+  if (warp == 0 && pos < end) {
+    int lo = 0, hi = n_seqs - 1;
+    while (lo < hi) {  // the largest b with Hk * pre[b] <= pos
+      const int mid = (lo + hi + 1) >> 1;
+      if (p.Hk * pre[mid] <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    const int w = pre[lo + 1] - pre[lo];
+    const int rem = pos - p.Hk * pre[lo], h = rem / w;
+    int left = rem - h * w;
+    const Seq s = pre_seq(p, lo);
+    const int pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
+    for (int q0 = 0; q0 < pairs; q0 += 32) {
+      int t = 0;
+      if (q0 + lane < pairs) {
+        Job j;
+        pair_span(p, s, q0 + lane, tpt, j);
+        t = max(j.sp.n, 1);
+      }
+      int inc = t;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (left >= inc - t && left < inc) start_sh = Start{lo, h, q0 + lane, left - (inc - t)};
+      const int sum = __shfl_sync(0xffffffffu, inc, 31);
+      if (left < sum) break;
+      left -= sum;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort = &abort_sh;
+  int dummy_abort = 0;
+  volatile int* noabort = reinterpret_cast<volatile int*>(&dummy_abort);
+  PairWalk wk_mem;
+  wk_mem.init(p, start_sh, pos, end);
+  // the walk's state lives in local memory (read once per unit), keeping
+  // registers for the per-tile work
+  PairWalk* volatile wk_ptr = &wk_mem;
+  PairWalk& walk = *wk_ptr;
+  Job jb;
+
+  if (warp == kProducerWarp) {
+    // ---------------------------------------------------------- producer
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&p.tm_q);
+      ptx::tma_prefetch_desc(&p.tm_k);
+      ptx::tma_prefetch_desc(&p.tm_v);
+    }
+    int nq = 0, g = 0;
+    PartRecord rec = make_int4(0, 0, -1, 0);
+    // K/V tiles are read by every pair of their head: keep them in L2; Q is read once
+    const uint64_t pol_q = ptx::l2_policy(false), pol_kv = ptx::l2_policy(true);
+    const int boxes = kTileRows >> p.b.page_log2;
+    const int box_bytes = 128 << p.b.page_log2;
+    bool ok = true, v_missing = false;
+    while (ok && walk.next(jb)) {
+      if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      if (jb.head) {
+        rec.x = 1;
+        rec.y = !jb.tail;
+      } else if (jb.tail) {
+        rec.z = jb.b;
+        rec.w = jb.place;
+      }
+      if (jb.kv_lo >= jb.kv_hi) continue;
+      ok = nq == 0 || ptx::mbar_wait(&bar_qe, (nq - 1) & 1, abort, p.status, RC_ETIMEOUT);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        const int nt = jb.has1 ? 2 : 1;
+        ptx::mbar_arrive_expect_tx(&bar_q, nt * L::kSub * tpt * p.G * 128);
+        for (int i = 0; i < nt; ++i)
+          for (int k = 0; k < L::kSub; ++k)
+            ptx::tma_load_3d_hint(&p.tm_q, &bar_q, base + L::kQ + i * L::kTile + k * kSubTileBytes, 64 * k,
+                                  jb.h * p.G, jb.q0 + i * tpt, pol_q);
+      }
+      ++nq;
+      for (int j = jb.kv_lo; j < jb.kv_hi; ++j, ++g) {
+        const int st = g & 1;
+        const uint32_t free_par = ((g >> 1) - 1) & 1;
+        const int k0 = jb.sp.key(j) + (lane << p.b.page_log2);
+        bool want = false;
+        int page = -1;
+        if (lane < boxes) {
+          want = k0 < jb.sp.hi_max &&
+                 (k0 + (1 << p.b.page_log2) > jb.sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
+          if (want) page = __ldg(p.b.page_table + jb.b * p.b.table_stride + (k0 >> p.b.page_log2));
+        }
+        const bool good = page >= 0 && page < p.b.n_pages;
+        if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        const uint32_t pages = __ballot_sync(0xffffffffu, good);
+        const int pg = good ? page : p.b.n_pages;  // a page that is none: read out of bounds on purpose, zeros
+        ok = g < 2 || ptx::mbar_wait(&bar_ke[st], free_par, abort, p.status, RC_ETIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        if (lane == 0) {
+          // S of tile g - 2 is complete, issued after the P of tile g - 3: the
+          // softmax is past tile g - 4, whose word this was
+          readable[g & 3] = pages;
+          ptx::mbar_arrive_expect_tx(&bar_kf[st], L::kTile);
+        }
+        __syncwarp();
+        if (lane < boxes)
+          for (int k = 0; k < L::kSub; ++k)
+            ptx::tma_load_4d_hint(&p.tm_k, &bar_kf[st],
+                                  base + L::kK + st * L::kTile + k * kSubTileBytes + lane * box_bytes, 64 * k, 0, jb.h,
+                                  pg, pol_kv);
+        ok = g < 2 || ptx::mbar_wait(&bar_ve[st], free_par, abort, p.status, RC_ETIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) {
+          ++g;  // its K is in flight, its V is not
+          v_missing = true;
+          break;
+        }
+        if (lane == 0) ptx::mbar_arrive_expect_tx(&bar_vf[st], L::kTile);
+        __syncwarp();
+        if (lane < boxes)
+          for (int k = 0; k < L::kSub; ++k)
+            ptx::tma_load_4d_hint(&p.tm_v, &bar_vf[st],
+                                  base + L::kV + st * L::kTile + k * kSubTileBytes + lane * box_bytes, 64 * k, 0, jb.h,
+                                  pg, pol_kv);
+      }
+    }
+    if (lane == 0) {
+      p.rec[blockIdx.x] = rec;
+      // never leave a copy in flight: wait (bounded, ignoring abort) for the last ones
+      if (nq) ptx::mbar_wait(&bar_q, (nq - 1) & 1, noabort, p.status, RC_ETIMEOUT);
+      for (int k = max(0, g - 2); k < g; ++k) {
+        ptx::mbar_wait(&bar_kf[k & 1], (k >> 1) & 1, noabort, p.status, RC_ETIMEOUT);
+        if (!(v_missing && k + 1 == g)) ptx::mbar_wait(&bar_vf[k & 1], (k >> 1) & 1, noabort, p.status, RC_ETIMEOUT);
+      }
+    }
+  } else if (warp == kMmaWarp && lane == 0) {
+    // ---------------------------------------------------------- MMA issuer
+    constexpr uint32_t idesc_s = ptx::idesc_f16(BF16, 128, 128, 0, 0);
+    constexpr uint32_t idesc_o = ptx::idesc_f16(BF16, 128, D, 0, 1);
+    const uint32_t sQ = base_u32 + L::kQ;
+    auto issue_s = [&](int i, int st) {
+      const uint32_t sQi = sQ + i * L::kTile;
+      const uint32_t sK = base_u32 + L::kK + st * L::kTile;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks) {
+        const uint32_t off = (ks >> 2) * kSubTileBytes + (ks & 3) * 32;
+        ptx::mma_ss(tmem + i * 128, ptx::sdesc_sw128(sQi + off, 16, 1024), ptx::sdesc_sw128(sK + off, 16, 1024),
+                    idesc_s, ks > 0);
+      }
+      ptx::mma_commit(&bar_s[i]);
+    };
+    // O_i += P_i V; committed for the epilogue after a job's last PV only (a
+    // softmax that rescales O at tile j has waited for S_i(j), issued after PV_i(j-1))
+    auto issue_pv = [&](int i, int st, bool acc, bool last) {
+      const uint32_t sV = base_u32 + L::kV + st * L::kTile;
+      // P of keys [16 ks, 16 ks + 16): column (ks / 4) * 64 + (ks % 4) * 8 of S_i
+#pragma unroll
+      for (int ks = 0; ks < kTileRows / 16; ++ks)
+        ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
+                    ptx::sdesc_sw128(sV + ks * 2048, kSubTileBytes, 1024), idesc_o, acc || ks > 0);
+      if (last) ptx::mma_commit(&bar_o[i]);
+    };
+    int nq = 0, g = 0, gp[2] = {0, 0};
+    bool ok = true;
+    while (ok && walk.next(jb)) {
+      const int n = jb.kv_hi - jb.kv_lo;
+      if (n <= 0) continue;
+      const bool two = jb.has1;
+      if (!ptx::mbar_wait(&bar_q, nq & 1, abort, p.status, RC_ETIMEOUT)) break;
+      ++nq;
+      if (!ptx::mbar_wait(&bar_kf[g & 1], (g >> 1) & 1, abort, p.status, RC_ETIMEOUT)) break;
+      ptx::tc_fence_after();
+      issue_s(0, g & 1);
+      if (two) issue_s(1, g & 1);
+      ptx::mma_commit(&bar_ke[g & 1]);
+      if (n == 1) ptx::mma_commit(&bar_qe);
+      for (int j = 0; j < n; ++j, ++g) {
+        const int st = g & 1, st1 = (g + 1) & 1;
+        const bool more = j + 1 < n;
+        if (!ptx::mbar_wait(&bar_p[0], gp[0] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        if (!ptx::mbar_wait(&bar_vf[st], (g >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        ptx::tc_fence_after();
+        issue_pv(0, st, j > 0, !more);
+        ++gp[0];
+        if (!two) ptx::mma_commit(&bar_ve[st]);
+        if (more) {
+          if (!ptx::mbar_wait(&bar_kf[st1], ((g + 1) >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          ptx::tc_fence_after();
+          issue_s(0, st1);
+          if (!two) {
+            ptx::mma_commit(&bar_ke[st1]);
+            if (j + 2 == n) ptx::mma_commit(&bar_qe);
+          }
+        }
+        if (two) {
+          if (!ptx::mbar_wait(&bar_p[1], gp[1] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          ptx::tc_fence_after();
+          issue_pv(1, st, j > 0, !more);
+          ++gp[1];
+          ptx::mma_commit(&bar_ve[st]);
+          if (more) {
+            issue_s(1, st1);
+            ptx::mma_commit(&bar_ke[st1]);
+            if (j + 2 == n) ptx::mma_commit(&bar_qe);
+          }
+        }
+      }
+    }
+    ptx::mma_commit(&bar_fin);
+    ptx::mbar_wait(&bar_fin, 0, noabort, p.status, RC_ETIMEOUT);
+  } else if (warp < kSoftmaxWarps) {
+    // ---------------------------------------------------------- softmax
+    // group g = warp / 8 owns query tile g. Warp w reads TMEM lane quarter
+    // w % 4 (32 rows) and column half ch = (w / 4) % 2: keys [64 ch, 64 ch + 64)
+    // of S and output columns [ch D/2, ch D/2 + D/2) of O. The two warps of a
+    // row block (partners) swap their partial row maxima every tile and their
+    // partial row sums once per unit through shared memory and a 64-thread
+    // mbarrier.
+    const int grp = warp >> 3;
+    const int ch = (warp >> 2) & 1;
+    const int wq = warp & 3;
+    const int row = wq * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>(wq * 32) << 16;
+    const uint32_t tS = tmem + lane_off + grp * 128 + ch * 64;
+    const uint32_t tO = tmem + lane_off + 256 + grp * 128 + ch * (D / 2);
+    uint64_t* pbar = &bar_pair[grp * 4 + wq];
+    const float c = p.scale_log2;
+    const float thresh = kRescaleLog2 / c;
+    const int qi = grp * tpt + row / p.G;         // this row's query within the pair
+    const bool row_in = row < tpt * p.G;
+    const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
+    int gs = 0;  // this group's tiles so far (phase of bar_s / bar_p)
+    int gt = 0;  // the CTA's tiles so far (stage of K and V)
+    int nj = 0;  // this group's jobs so far (phase of bar_o: one commit per job)
+    int nx = 0;  // partner exchanges so far (phase of pbar, slot of swap_buf)
+    // writes v, returns the partner's value (bounded wait)
+    auto swap = [&](float v, float& other) -> bool {
+      float(*buf)[128] = swap_buf[grp][nx & 1];
+      buf[ch][row] = v;
+      ptx::mbar_arrive(pbar);
+      if (!ptx::mbar_wait(pbar, nx & 1, abort, p.status, RC_ETIMEOUT)) return false;
+      ++nx;
+      other = buf[ch ^ 1][row];
+      return true;
+    };
+    while (walk.next(jb)) {
+      if (*abort) break;
+      if (grp == 1 && !jb.has1) {
+        gt += max(0, jb.kv_hi - jb.kv_lo);
+        continue;
+      }
+      const bool live = row_in && qi < jb.tokens;
+      // rows of no query take the widest mask, so that they never slow their warp
+      RowMask rm{jb.sp.lo_min, jb.sp.hi_max};
+      if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
+      float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
+      bool ok = true;
+      int done = 0;
+      for (int j = jb.kv_lo; j < jb.kv_hi; ++j) {
+        if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        ptx::tc_fence_after();
+        const int t0 = jb.sp.key(j), h0 = t0 + ch * 64;  // this warp's keys: [h0, h0 + 64)
+        const uint32_t pages = readable[gt & 3];
+        // pages of this half that are there, as a bit per page
+        const int lg = p.b.page_log2;
+        const uint32_t all_pages = lg >= 6 ? 1u : (1u << (64 >> lg)) - 1;
+        const uint32_t half_pages = (pages >> ((ch * 64) >> lg)) & all_pages;
+        const bool full = __all_sync(0xffffffffu, h0 + 64 <= rm.hi && (h0 >= rm.lo || h0 + 64 <= sink) &&
+                                                      half_pages == all_pages);
+        uint32_t va = 0xffffffffu, vb = 0xffffffffu;  // visible keys, a bit each
+        if (!full) {
+          auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
+          unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
+          if (half_pages != all_pages) {
+            unsigned long long pm = 0;
+            for (int k = 0; k < 64; k += min(64, 1 << lg))
+              if ((half_pages >> (k >> lg)) & 1) pm |= below(min(64, 1 << lg)) << k;
+            v &= pm;
+          }
+          va = (uint32_t)v;
+          vb = (uint32_t)(v >> 32);
+        }
+        // V rows that no query of the pair sees: zero, before group 0's P lets the product start
+        if (grp == 0 && !(t0 + kTileRows <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || t0 + kTileRows <= sink))) {
+          const int st = gt & 1;
+          if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          const int vr = (int)threadIdx.x >> 1, key = t0 + vr;
+          if (!(key < jb.sp.hi_max && (key >= jb.sp.lo_min || key < sink))) {
+            uint8_t* dst = base + L::kV + st * L::kTile + vr * 128 + (threadIdx.x & 1) * 64;
+#pragma unroll
+            for (int k = 0; k < L::kSub; ++k)
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(dst + k * kSubTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          ptx::fence_proxy_async_smem();
+        }
+        uint32_t ra[32], rb[32];
+        ptx::tmem_ld32(tS, ra);
+        ptx::tmem_ld32(tS + 32, rb);
+        ptx::tmem_ld_wait();
+        float mx = -INFINITY;
+        if (full) {
+#pragma unroll
+          for (int k = 0; k < 32; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[k]), __uint_as_float(rb[k]));
+        } else {
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            mx = ptx::fmax3(mx, (va >> k) & 1u ? __uint_as_float(ra[k]) : -INFINITY,
+                            (vb >> k) & 1u ? __uint_as_float(rb[k]) : -INFINITY);
+        }
+        float mo;
+        if (!swap(mx, mo)) { ok = false; break; }
+        const float m_new = ptx::fmax3(m, mx, mo);
+        const bool need = m_new > m + thresh;       // also true for the first visible tile
+        const bool real = need && m != -INFINITY;   // O already holds weighted values
+        if (__any_sync(0xffffffffu, real)) {
+          // PV of the previous tile is complete: it was issued before this
+          // tile's S, which the wait above saw complete
+          const float alpha = real ? ptx::ex2((m - m_new) * c) : 1.f;
+#pragma unroll
+          for (int cc = 0; cc < D / 64; ++cc) {
+            uint32_t o[32];
+            ptx::tmem_ld32(tO + cc * 32, o);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+            ptx::tmem_st32(tO + cc * 32, o);
+          }
+          ptx::tmem_st_wait();
+          l *= alpha;
+        }
+        if (need) m = m_new;
+        const float mc = (m == -INFINITY ? 0.f : m) * c;
+        // P = 2^(s c - m c) as packed 16-bit pairs over the first 32 columns of
+        // this half of S (already read): keys h0 + 2i, h0 + 2i + 1 -> column i.
+        // P is rounded to the values' type, the product's operand: off by at most
+        // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it
+        float sum = 0.f;
+        auto emit = [&](const uint32_t (&r)[32], uint32_t vis, int k0) {
+          uint32_t pk[16];
+          if (full) {
+            const float2 c2 = make_float2(c, c), nmc2 = make_float2(-mc, -mc);
+            float2 s2 = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float2 x =
+                  ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nmc2);
+              float2 e;
+              if ((k & 7) < kCubicPairs) {
+                e = exp2_cubic2(x);
+              } else {
+                e.x = ptx::ex2(x.x);
+                e.y = ptx::ex2(x.y);
+              }
+              s2 = ptx::fadd2(s2, e);
+              pk[k] = ptx::pack16x2<BF16>(e.x, e.y);
+            }
+            sum += s2.x + s2.y;
+          } else {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float a = (vis >> (2 * k)) & 1u ? ptx::ex2(fmaf(__uint_as_float(r[2 * k]), c, -mc)) : 0.f;
+              const float b =
+                  (vis >> (2 * k + 1)) & 1u ? ptx::ex2(fmaf(__uint_as_float(r[2 * k + 1]), c, -mc)) : 0.f;
+              sum += a + b;
+              pk[k] = ptx::pack16x2<BF16>(a, b);
+            }
+          }
+          ptx::tmem_st16(tS + k0 / 2, pk);
+        };
+        // S is read again rather than kept in registers across the exchange
+        ptx::tmem_ld32(tS, ra);
+        ptx::tmem_ld_wait();
+        emit(ra, va, 0);
+        ptx::tmem_ld32(tS + 32, rb);
+        ptx::tmem_ld_wait();
+        emit(rb, vb, 32);
+        ptx::tmem_st_wait();
+        l += sum;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar_p[grp]);
+        ++gs;
+        ++gt;
+        ++done;
+      }
+      // epilogue: O / l, merged with the prefix's result where there is one, to
+      // the output, or to this CTA's partial slot (fp32, log2-sum-exp); each
+      // warp writes its D/2 columns
+      float l_other = 0.f;
+      if (ok && !swap(l, l_other)) ok = false;
+      const float lt = l + l_other;
+      const bool have_o =
+          ok && done > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
+      if (done > 0) ++nj;
+      ptx::tc_fence_after();
+      // a row that sees nothing has lt = 0: zeros and -inf; a NaN sum stays NaN
+      const float inv_l = lt == 0.f ? 0.f : 1.f / lt;
+      const float lse2 = lt == 0.f ? -INFINITY : m * c + log2f(lt);
+#pragma unroll
+      for (int cc = 0; cc < D / 64; ++cc) {
+        uint32_t o[32];
+        if (have_o) {
+          ptx::tmem_ld32(tO + cc * 32, o);
+          ptx::tmem_ld_wait();
+        }
+        if (!live) continue;
+        const int col = ch * (D / 2) + cc * 32;
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          float acc[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = have_o && lt != 0.f ? __uint_as_float(o[8 * v + k]) * inv_l : 0.f;
+          if (jb.slot < 0) {
+            const int tok = jb.q0 + qi, head = jb.h * p.G + row % p.G;
+            float lse = lse2;
+            if (p.prev_o) merge_prev<D>(p, tok, head, col + 8 * v, acc, lse);
+            store_row<D, BF16>(p, tok, head, col + 8 * v, acc, lse);
+          } else {
+            const size_t at = (size_t)jb.slot * kPrefillRows + grp * kTileRows + row;
+            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col + 8 * v);
+            dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+            dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+            if (col + 8 * v == 0) p.part_lse[at] = lse2;
+          }
+        }
+      }
+      if (!ok) break;
+    }
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, bool BF16>
+cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
+  static PerDevice attr_set;
+  int done = 0;
+  cudaError_t e = attr_set.get(&done, [](int, int* x) {
+    *x = 1;
+    return cudaFuncSetAttribute(paged_prefill_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)PreLayout<D>::kDynSmem);
+  });
+  if (e != cudaSuccess) return e;
+  paged_prefill_kernel<D, BF16><<<p.n_ctas, kPreThreads, PreLayout<D>::kDynSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {
+  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
+  return bf16 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
+}
+
+}  // namespace rc

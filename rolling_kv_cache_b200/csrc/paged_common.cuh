@@ -1,0 +1,136 @@
+// Pieces the paged attention kernels share: the mask of a query, the key
+// tiles a range of queries walks, and the stream-K split of a ragged batch.
+#pragma once
+
+#include "paged.cuh"
+#include "ptx.cuh"
+
+namespace rc {
+
+// Keys [lo, hi) and, under a window, [0, sink_tok) within hi.
+struct RowMask {
+  int lo, hi;
+};
+
+// at: the query's position (negative: it sees nothing); L: tokens in the pages.
+__device__ __forceinline__ RowMask row_mask(const MaskView& m, int at, int L) {
+  if (at < 0) return RowMask{0, 0};
+  const int f = at / m.frame;
+  const int lo = m.window > 0 && f >= m.window ? (f - m.window + 1) * m.frame : 0;
+  return RowMask{lo, min(L, (f + 1) * m.frame)};
+}
+
+// The key tiles (TK keys each, tile k = keys [k TK, k TK + TK)) that queries
+// at positions [first, last] walk: those of the sinks, then those from the
+// first window start to the last query's end.
+template <int TK>
+struct TileSpan {
+  int n_sink, from, n;
+  int lo_min, hi_max;  // union of what the queries see: [0, sinks) and [lo_min, hi_max)
+  __device__ __forceinline__ void init(const MaskView& m, int first, int last, int L) {
+    hi_max = row_mask(m, last, L).hi;
+    lo_min = row_mask(m, max(first, 0), L).lo;
+    const int n_end = (hi_max + TK - 1) / TK;
+    n_sink = 0;
+    from = 0;
+    if (m.window > 0) {
+      n_sink = min((m.sink_tok + TK - 1) / TK, n_end);
+      from = max(n_sink, lo_min / TK);
+    }
+    n = n_sink + max(0, n_end - from);
+  }
+  __device__ __forceinline__ int key(int j) const { return (j < n_sink ? j : from + j - n_sink) * TK; }
+};
+
+// One sequence of the batch, with whatever the device arrays hold brought
+// into range: rows [q0, q0 + n) of q, L tokens in the pages. `bad` says that
+// something was out of range.
+struct Seq {
+  int q0, n, L;
+  bool bad;
+};
+
+__device__ __forceinline__ Seq load_seq(const BatchView& v, int n_tok, int b) {
+  const int a = __ldg(v.cu_q + b), e = __ldg(v.cu_q + b + 1), l = __ldg(v.kv_len + b);
+  Seq s;
+  s.q0 = min(max(a, 0), n_tok);
+  s.n = min(max(e - s.q0, 0), n_tok - s.q0);
+  s.L = min(max(l, 0), v.max_pages << v.page_log2);
+  s.bad = s.q0 != a || e - a != s.n || s.L != l;
+  return s;
+}
+
+// What a CTA's stream-K range left in the partial rows. Slot 2c holds the
+// part of the unit its range begins inside (x: 1 if there is one, y: 1 if
+// that unit ends in the range); slot 2c + 1 the first part of a unit that
+// begins in the range and goes on in the next CTA's (z: its sequence, or -1;
+// w: its place within the sequence, kernel-defined).
+using PartRecord = int4;
+
+// Exclusive prefix sums of f(0..n-1) into pre[0..n] (shared memory), by all
+// threads of the block.
+template <int THREADS, typename Fn>
+__device__ __forceinline__ void block_prefix(int* pre, int n, int* warp_sums, Fn f) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int per = (n + THREADS - 1) / THREADS;
+  const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
+  int sum = 0;
+  for (int i = i0; i < i1; ++i) {
+    const int w = f(i);
+    pre[i] = sum;
+    sum += w;
+  }
+  int inc = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += t;
+  }
+  if (lane == 31) warp_sums[warp] = inc;
+  __syncthreads();
+  int base = inc - sum;
+  for (int w = 0; w < warp; ++w) base += warp_sums[w];
+  for (int i = i0; i < i1; ++i) pre[i] += base;
+  if (i0 < i1 && i1 == n) pre[n] = base + sum;
+  if (n == 0 && tid == 0) pre[0] = 0;
+  __syncthreads();
+}
+
+// Merges 8 columns of a row (divided by its sum; lse2 its log2-sum-exp) with
+// the same row's result over the shared prefix.
+template <int D>
+__device__ __forceinline__ void merge_prev(const PagedAttnParams& p, int tok, int head, int col, float (&acc)[8],
+                                           float& lse2) {
+  const float pl = p.prev_lse[(size_t)head * p.n_tok + tok];
+  const float m = fmaxf(lse2, pl);
+  if (m == -INFINITY) return;  // neither side saw a key
+  const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.Hk * p.G + head) * D + col);
+  const float4 a = src[0], b = src[1];
+  const float w = exp2f(lse2 - m), wp = exp2f(pl - m), inv = 1.f / (w + wp);
+  const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = (acc[k] * w + x[k] * wp) * inv;
+  lse2 = m + log2f(w + wp);
+}
+
+// The last write of 8 columns of a row: the output, or the prefix pass's fp32 result.
+template <int D, bool BF16>
+__device__ __forceinline__ void store_row(const PagedAttnParams& p, int tok, int head, int col, const float (&acc)[8],
+                                          float lse2) {
+  if (p.pre_o) {
+    float4* dst = reinterpret_cast<float4*>(p.pre_o + ((size_t)tok * p.Hk * p.G + head) * D + col);
+    dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+    if (col == 0) p.pre_lse[(size_t)head * p.n_tok + tok] = lse2;
+    return;
+  }
+  uint4 u;
+  u.x = ptx::pack16x2<BF16>(acc[0], acc[1]);
+  u.y = ptx::pack16x2<BF16>(acc[2], acc[3]);
+  u.z = ptx::pack16x2<BF16>(acc[4], acc[5]);
+  u.w = ptx::pack16x2<BF16>(acc[6], acc[7]);
+  *reinterpret_cast<uint4*>(p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + col * 2) = u;
+  if (p.lse && col == 0) p.lse[(size_t)head * p.n_tok + tok] = lse2 * 0.69314718055994531f;
+}
+
+}  // namespace rc

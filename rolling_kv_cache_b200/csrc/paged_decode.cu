@@ -1,0 +1,429 @@
+// Attention over pages for few query rows per key head (rows = queries of a
+// sequence x query heads of a key head <= 16): single tokens, short drafts.
+//
+//   o = sum_j exp(x_j) v_j / sum_j exp(x_j),  x_j = scale q . k_j,
+// over the keys the mask leaves, in one pass with the running maximum and
+// sum. Every key and value is read once for all the rows of its key head, so
+// the bound is HBM: 2 * keys * head_dim * 2 bytes per (sequence, key head).
+//
+// The units (sequence, key head) are cut into 64-key tiles, and the tiles of
+// the whole batch, in order, into one range per CTA (one CTA per SM), equal to
+// a tile: a ragged batch and a single long sequence keep every SM reading
+// alike. Each CTA finds its range from the lengths on the device. A unit cut
+// between CTAs leaves parts for the combine kernel.
+//
+// One warp issues TMA copies of the tiles' pages (a box per page and 64 dims,
+// 128-byte swizzle) into a ring of 160 KB, running ahead across units, so
+// that about that much of HBM reads is in flight per SM. Two groups of four warps
+// take alternate tiles; a warp owns 16 keys of its tile: S = Q K^T and O += P V
+// by warp-level 16 x 8 x 16 matrix steps on ldmatrix fragments (the 16 rows
+// are the padded query rows; with so few rows a tcgen05 tile of 128 would be
+// nearly all padding), with its own running maximum, sum and O, so that no warp waits
+// for another within a unit. At a unit's end the eight warps' results meet
+// in shared memory in a fixed order.
+//
+// Rows of a tile that no query of the unit sees (behind the sequence, before
+// the window, on a page that is not one) get weight 0 and their V fragments
+// are zeroed, so whatever their bits hold, NaN included, stays out.
+#include "paged_common.cuh"
+
+namespace rc {
+
+namespace {
+
+constexpr int kTK = 64;                       // keys per tile
+constexpr int kConsumers = 8;                 // warps
+constexpr int kDecThreads = (kConsumers + 1) * 32;
+constexpr int kRingBytes = 160 * 1024;
+constexpr float kDecRescaleLog2 = 8.f;
+
+template <int D>
+struct DecLayout {
+  static constexpr int kSub = D / 64;
+  static constexpr uint32_t kPlane = kTK * 128;          // 64 keys x 64 dims
+  static constexpr uint32_t kTile = kPlane * kSub;       // K or V of a tile
+  static constexpr uint32_t kStage = 2 * kTile;
+  static constexpr int kStages = kRingBytes / kStage;    // 5 at d = 128, 10 at d = 64
+  static constexpr int kOPad = D + 8;                    // row stride of a merge buffer: spreads rows over banks
+  static constexpr uint32_t kMerge = kRingBytes;         // 4 buffers [16][kOPad] fp32
+  static constexpr uint32_t kPre = kMerge + 4 * 16 * kOPad * 4;
+  static constexpr uint32_t kBytes = kPre + (kMaxSeqs + 1) * 4;
+  static constexpr uint32_t kDynSmem = kBytes + 1024;
+};
+
+struct DecUnit {
+  int b, h, lo, hi, total;  // tiles [lo, hi) of the unit's `total`
+};
+
+// Walks the units of positions [pos, end): position Hk * pre[b] + h * w + t is
+// tile t of head h of sequence b, w = pre[b + 1] - pre[b].
+struct DecWalk {
+  const int* pre;
+  int Hk, pos, end, b;
+  __device__ __forceinline__ void init(const int* pre_, int n, int Hk_, int pos_, int end_) {
+    pre = pre_;
+    Hk = Hk_;
+    pos = pos_;
+    end = end_;
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {  // the largest b with Hk * pre[b] <= pos
+      const int mid = (lo + hi + 1) >> 1;
+      if (Hk * pre[mid] <= pos) lo = mid;
+      else hi = mid - 1;
+    }
+    b = lo;
+  }
+  __device__ __forceinline__ bool next(DecUnit& u) {
+    if (pos >= end) return false;
+    while (Hk * pre[b + 1] <= pos) ++b;
+    const int w = pre[b + 1] - pre[b], rem = pos - Hk * pre[b];
+    u.b = b;
+    u.h = rem / w;
+    u.lo = rem - u.h * w;
+    u.total = w;
+    u.hi = min(w, u.lo + end - pos);
+    pos += u.hi - u.lo;
+    return true;
+  }
+};
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
+  using L = DecLayout<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint64_t bar_full[L::kStages], bar_empty[L::kStages];
+  __shared__ uint32_t readable[L::kStages];  // bit i: page i of the stage's tile is one
+  __shared__ float wm[2][kConsumers][16], wl[2][kConsumers][16];
+  __shared__ int warp_sums[kConsumers + 1];
+  __shared__ int abort_sh;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* base = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
+  const uint32_t base_u32 = ptx::smem_u32(base);
+  int* pre = reinterpret_cast<int*>(base + L::kPre);
+  if (tid == 0) {
+    for (int i = 0; i < L::kStages; ++i) {
+      ptx::mbar_init(&bar_full[i], 1);
+      ptx::mbar_init(&bar_empty[i], 4);
+    }
+    abort_sh = 0;
+    ptx::fence_mbar_init();
+  }
+  ptx::grid_launch_dependents();
+  // tiles of each sequence, and this CTA's range of the batch's
+  block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
+    const Seq s = load_seq(p.b, p.n_tok, b);
+    if (s.n == 0) return 0;
+    TileSpan<kTK> sp;
+    sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+    return max(sp.n, 1);
+  });
+  const int W = p.Hk * pre[p.b.n_seqs];
+  const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
+  const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
+  volatile int* abort = &abort_sh;
+  DecWalk walk;
+  walk.init(pre, p.b.n_seqs, p.Hk, pos, end);
+  DecUnit u;
+
+  if (warp == kConsumers) {
+    // ------------------------------------------------------------ producer
+    if (lane == 0) {
+      ptx::tma_prefetch_desc(&p.tm_k);
+      ptx::tma_prefetch_desc(&p.tm_v);
+    }
+    const uint64_t pol = ptx::l2_policy(false);
+    // boxes of a tile: page lanes (keys [i * box, i * box + box)), each with kSub planes of K and of V
+    const int boxes = kTK / p.box_rows;
+    const int in_page = (1 << p.b.page_log2) - 1;
+    int g = 0;
+    bool ok = true;
+    int4 rec = make_int4(0, 0, -1, 0);
+    while (ok && walk.next(u)) {
+      const Seq s = load_seq(p.b, p.n_tok, u.b);
+      TileSpan<kTK> sp;
+      sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+      if (lane == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      if (u.lo > 0) {
+        rec.x = 1;
+        rec.y = u.hi == u.total;
+      } else if (u.hi < u.total) {
+        rec.z = u.b;
+        rec.w = u.h;
+      }
+      const int n = min(u.hi, sp.n);
+      for (int j = u.lo; j < n; ++j, ++g) {
+        const int t0 = sp.key(j);
+        int page = -1;
+        bool want = false;
+        const int k0 = t0 + lane * p.box_rows;
+        if (lane < boxes) {
+          want = k0 < sp.hi_max && (k0 + p.box_rows > sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
+          if (want) page = __ldg(p.b.page_table + u.b * p.b.table_stride + (k0 >> p.b.page_log2));
+        }
+        const bool good = page >= 0 && page < p.b.n_pages;
+        if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        const uint32_t pages = __ballot_sync(0xffffffffu, good);
+        const int st = g % L::kStages;
+        if (g >= L::kStages) {
+          ok = ptx::mbar_wait(&bar_empty[st], (g / L::kStages - 1) & 1, abort, p.status, RC_ETIMEOUT);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+        }
+        if (lane == 0) {
+          readable[st] = pages;
+          ptx::mbar_arrive_expect_tx(&bar_full[st], L::kStage);
+        }
+        __syncwarp();
+        if (lane < boxes) {
+          // a page that is none is read out of bounds on purpose: the copy fills zeros
+          const int pg = good ? page : p.b.n_pages, row = good ? (k0 & in_page) : 0;
+          uint8_t* dst = base + st * L::kStage + lane * p.box_rows * 128;
+#pragma unroll
+          for (int i = 0; i < L::kSub; ++i) {
+            ptx::tma_load_4d_hint(&p.tm_k, &bar_full[st], dst + i * L::kPlane, 64 * i, row, u.h, pg, pol);
+            ptx::tma_load_4d_hint(&p.tm_v, &bar_full[st], dst + L::kTile + i * L::kPlane, 64 * i, row, u.h, pg, pol);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (lane == 0) {
+      p.rec[blockIdx.x] = rec;
+      // leave no copy in flight (bounded, whether or not the others gave up)
+      int dummy = 0;
+      for (int k = max(0, g - L::kStages); k < g; ++k)
+        ptx::mbar_wait(&bar_full[k % L::kStages], (k / L::kStages) & 1, &dummy, p.status, RC_ETIMEOUT);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int grp = warp >> 2, kw = (warp & 3) * 16;  // this warp's keys of its group's tiles
+  const int r0 = lane >> 2, r1 = r0 + 8, cq = (lane & 3) * 2;
+  const float c = p.scale_log2, thresh = kDecRescaleLog2 / c;
+  int g = 0, nu = 0;
+  bool alive = true;  // a warp whose wait gave up still meets the others at the merges' barriers
+  while (walk.next(u)) {
+    const Seq s = load_seq(p.b, p.n_tok, u.b);
+    TileSpan<kTK> sp;
+    sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+    const int nq = min(s.n, 16 / p.G), R = nq * p.G;
+    if (nq < s.n && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+    const int i0 = r0 / p.G, i1 = r1 / p.G;
+    const RowMask m0 = row_mask(p.mask, s.L - s.n + i0, s.L), m1 = row_mask(p.mask, s.L - s.n + i1, s.L);
+    const RowMask first = row_mask(p.mask, s.L - s.n, s.L), last = row_mask(p.mask, s.L - 1, s.L);
+    // Q fragments: rows r0 and r1, zero behind the last row
+    uint32_t qf[D / 16][4];
+    {
+      const uint8_t* q0 = p.q.data + (s.q0 + i0) * p.q.tok_stride + (u.h * p.G + r0 - i0 * p.G) * p.q.head_stride;
+      const uint8_t* q1 = p.q.data + (s.q0 + i1) * p.q.tok_stride + (u.h * p.G + r1 - i1 * p.G) * p.q.head_stride;
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const int off = (k * 16 + cq) * 2;
+        qf[k][0] = r0 < R ? __ldg(reinterpret_cast<const uint32_t*>(q0 + off)) : 0u;
+        qf[k][1] = r1 < R ? __ldg(reinterpret_cast<const uint32_t*>(q1 + off)) : 0u;
+        qf[k][2] = r0 < R ? __ldg(reinterpret_cast<const uint32_t*>(q0 + off + 16)) : 0u;
+        qf[k][3] = r1 < R ? __ldg(reinterpret_cast<const uint32_t*>(q1 + off + 16)) : 0u;
+      }
+    }
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
+    float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    const int n = min(u.hi, sp.n);
+    for (int j = u.lo; j < n && alive; ++j, ++g) {
+      if ((g & 1) != grp) continue;
+      const int st = g % L::kStages;
+      alive = ptx::mbar_wait(&bar_full[st], (g / L::kStages) & 1, abort, p.status, RC_ETIMEOUT);
+      alive = __all_sync(0xffffffffu, alive);
+      if (!alive) break;
+      const int t0 = sp.key(j), w0 = t0 + kw;
+      const uint32_t sK = base_u32 + st * L::kStage, sV = sK + L::kTile;
+      float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+      {
+        const int row = kw + (lane >> 4) * 8 + (lane & 7);
+        const uint32_t a = sK + row * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t kf[4];
+          ptx::ldsm4(kf, a + (k >> 2) * L::kPlane + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+          ptx::mma16816<BF16>(x[0], qf[k], kf[0], kf[1]);
+          ptx::mma16816<BF16>(x[1], qf[k], kf[2], kf[3]);
+        }
+      }
+      // keep: bit pairs of this lane's 4 keys (w0 + cq, +1, +8, +9) that some row sees
+      const uint32_t pages = readable[st];
+      const bool whole = w0 + 16 <= first.hi && (w0 >= last.lo || (p.mask.window > 0 && w0 + 16 <= p.mask.sink_tok)) &&
+                         ((pages >> (kw / p.box_rows)) & 1u);
+      uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
+      if (!whole) {
+        const bool page_ok = (pages >> (kw / p.box_rows)) & 1u;  // a warp's 16 keys lie in one page
+        const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
+        uint32_t kb[2] = {0u, 0u};
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int key = w0 + i * 8 + cq + e;
+            const bool v0 = page_ok && key < m0.hi && (key >= m0.lo || key < sink);
+            const bool v1 = page_ok && key < m1.hi && (key >= m1.lo || key < sink);
+            if (!v0) x[i][e] = -INFINITY;
+            if (!v1) x[i][2 + e] = -INFINITY;
+            if (page_ok && key < sp.hi_max && (key >= sp.lo_min || key < sink)) kb[i] |= 0xffffu << (16 * e);
+          }
+        keep0 = kb[0];
+        keep1 = kb[1];
+      }
+      float t_0 = ptx::fmax3(fmaxf(x[0][0], x[0][1]), x[1][0], x[1][1]);
+      float t_1 = ptx::fmax3(fmaxf(x[0][2], x[0][3]), x[1][2], x[1][3]);
+#pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        t_0 = fmaxf(t_0, __shfl_xor_sync(0xffffffffu, t_0, d));
+        t_1 = fmaxf(t_1, __shfl_xor_sync(0xffffffffu, t_1, d));
+      }
+      // the maximum moves only when it grows by more than 2^8: numerator and
+      // denominator share the stale one, and P stays below 256
+      const bool n0 = t_0 > mx0 + thresh, n1 = t_1 > mx1 + thresh;
+      if (__any_sync(0xffffffffu, n0 || n1)) {
+        const float a0 = n0 ? ptx::ex2((mx0 - t_0) * c) : 1.f, a1 = n1 ? ptx::ex2((mx1 - t_1) * c) : 1.f;
+        if (n0) mx0 = t_0;
+        if (n1) mx1 = t_1;
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+          o[i][0] *= a0;
+          o[i][1] *= a0;
+          o[i][2] *= a1;
+          o[i][3] *= a1;
+        }
+      }
+      const float b0 = mx0 == -INFINITY ? 0.f : mx0 * c, b1 = mx1 == -INFINITY ? 0.f : mx1 * c;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        x[i][0] = ptx::ex2(fmaf(x[i][0], c, -b0));
+        x[i][1] = ptx::ex2(fmaf(x[i][1], c, -b0));
+        x[i][2] = ptx::ex2(fmaf(x[i][2], c, -b1));
+        x[i][3] = ptx::ex2(fmaf(x[i][3], c, -b1));
+      }
+      l0 += (x[0][0] + x[0][1]) + (x[1][0] + x[1][1]);
+      l1 += (x[0][2] + x[0][3]) + (x[1][2] + x[1][3]);
+      // P is rounded to the values' type, the matrix step's operand: off by at
+      // most 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sums l are not
+      const uint32_t pf[4] = {ptx::pack16x2<BF16>(x[0][0], x[0][1]), ptx::pack16x2<BF16>(x[0][2], x[0][3]),
+                              ptx::pack16x2<BF16>(x[1][0], x[1][1]), ptx::pack16x2<BF16>(x[1][2], x[1][3])};
+      {
+        const int row = kw + (lane & 15);
+        const uint32_t a = sV + row * 128;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          uint32_t vf[4];
+          ptx::ldsm4_t(vf, a + (k >> 2) * L::kPlane + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) << 4));
+          ptx::mma16816<BF16>(o[2 * k], pf, vf[0] & keep0, vf[1] & keep1);
+          ptx::mma16816<BF16>(o[2 * k + 1], pf, vf[2] & keep0, vf[3] & keep1);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bar_empty[st]);
+    }
+    // ------------------------------------------------- merge of the 8 warps
+#pragma unroll
+    for (int d = 1; d < 4; d <<= 1) {
+      l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+      l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    float(*um)[16] = wm[nu & 1];
+    float(*ul)[16] = wl[nu & 1];
+    ++nu;
+    if ((lane & 3) == 0) {
+      um[warp][r0] = mx0;
+      um[warp][r1] = mx1;
+      ul[warp][r0] = l0;
+      ul[warp][r1] = l1;
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    float* buf = reinterpret_cast<float*>(base + L::kMerge) + (warp & 3) * 16 * L::kOPad;
+    float g0 = -INFINITY, g1 = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kConsumers; ++w) {
+      g0 = fmaxf(g0, um[w][r0]);
+      g1 = fmaxf(g1, um[w][r1]);
+    }
+    const float f0 = mx0 == -INFINITY ? 0.f : ptx::ex2((mx0 - g0) * c);
+    const float f1 = mx1 == -INFINITY ? 0.f : ptx::ex2((mx1 - g1) * c);
+    if (warp >= 4) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        if (r0 < R) *reinterpret_cast<float2*>(buf + r0 * L::kOPad + i * 8 + cq) = make_float2(o[i][0] * f0, o[i][1] * f0);
+        if (r1 < R) *reinterpret_cast<float2*>(buf + r1 * L::kOPad + i * 8 + cq) = make_float2(o[i][2] * f1, o[i][3] * f1);
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    if (warp < 4) {
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {
+        if (r0 < R) {
+          float2* d = reinterpret_cast<float2*>(buf + r0 * L::kOPad + i * 8 + cq);
+          *d = make_float2(fmaf(o[i][0], f0, d->x), fmaf(o[i][1], f0, d->y));
+        }
+        if (r1 < R) {
+          float2* d = reinterpret_cast<float2*>(buf + r1 * L::kOPad + i * 8 + cq);
+          *d = make_float2(fmaf(o[i][2], f1, d->x), fmaf(o[i][3], f1, d->y));
+        }
+      }
+    }
+    asm volatile("bar.sync 1, 256;" ::: "memory");
+    const int row = tid / (D / 8), col = (tid % (D / 8)) * 8;
+    if (row < R) {
+      const float* b = reinterpret_cast<const float*>(base + L::kMerge) + row * L::kOPad + col;
+      float acc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        acc[k] = (b[k] + b[16 * L::kOPad + k]) + (b[32 * L::kOPad + k] + b[48 * L::kOPad + k]);
+      float gm = -INFINITY, l = 0.f;
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) gm = fmaxf(gm, um[w][row]);
+#pragma unroll
+      for (int w = 0; w < kConsumers; ++w) l += um[w][row] == -INFINITY ? 0.f : ul[w][row] * ptx::ex2((um[w][row] - gm) * c);
+      // a row that sees nothing has l = 0: zeros and -inf; a NaN sum stays NaN
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      float lse2 = l == 0.f ? -INFINITY : gm * c + log2f(l);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] *= inv;
+      if (u.lo > 0 || u.hi < u.total) {
+        const size_t at = (size_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * kDecodeRows + row;
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (col == 0) p.part_lse[at] = lse2;
+      } else {
+        const int i = row / p.G, head = u.h * p.G + row - i * p.G, tok = s.q0 + i;
+        if (p.prev_o) merge_prev<D>(p, tok, head, col, acc, lse2);
+        store_row<D, BF16>(p, tok, head, col, acc, lse2);
+      }
+    }
+  }
+}
+
+}  // namespace
+
+template <int D, bool BF16>
+static cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
+  static PerDevice attr_set;
+  int done = 0;
+  cudaError_t e = attr_set.get(&done, [](int, int* x) {
+    *x = 1;
+    return cudaFuncSetAttribute(paged_decode_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)DecLayout<D>::kDynSmem);
+  });
+  if (e != cudaSuccess) return e;
+  paged_decode_kernel<D, BF16><<<p.n_ctas, kDecThreads, DecLayout<D>::kDynSmem, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {
+  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
+  return bf16 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
+}
+
+}  // namespace rc
