@@ -161,7 +161,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   __shared__ uint64_t bar_q, bar_qe, bar_kf[2], bar_vf[2], bar_ke[2], bar_ve[2], bar_s[2], bar_p[2], bar_o[2],
       bar_fin, bar_pair[8];
   __shared__ float swap_buf[2][2][2][kTileRows];  // [group][exchange parity][column half][row]
-  __shared__ uint32_t readable[4];                // bit i: page i of the tile is one; tile g at g % 4
+  // what the softmax has to know of tile g, at g % 4: its first key, its pages
+  // that are there (a bit each), whether every query sees all of it, whether some V
+  // rows are seen by none
+  __shared__ int4 tile_info[4];
   __shared__ int warp_sums[18];
   __shared__ Start start_sh;
   __shared__ uint32_t tmem_base_sh;
@@ -273,76 +276,88 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     PartRecord rec = make_int4(0, 0, -1, 0);
     // K/V tiles are read by every pair of their head: keep them in L2; Q is read once
     const uint64_t pol_q = ptx::l2_policy(false), pol_kv = ptx::l2_policy(true);
+    // a tile is `boxes` pages; a lane copies one page's 64 dims of K, then of V
     const int boxes = kTileRows >> p.b.page_log2;
-    const int box_bytes = 128 << p.b.page_log2;
-    bool ok = true, v_missing = false;
-    while (ok && walk.next(jb)) {
-      if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-      if (jb.head) {
-        rec.x = 1;
-        rec.y = !jb.tail;
-      } else if (jb.tail) {
-        rec.z = jb.b;
-        rec.w = jb.place;
-      }
-      if (jb.kv_lo >= jb.kv_hi) continue;
-      ok = nq == 0 || ptx::mbar_wait(&bar_qe, (nq - 1) & 1, abort, p.status, RC_ETIMEOUT);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) break;
-      if (lane == 0) {
-        const int nt = jb.has1 ? 2 : 1;
-        ptx::mbar_arrive_expect_tx(&bar_q, nt * L::kSub * tpt * p.G * 128);
-        for (int i = 0; i < nt; ++i)
-          for (int k = 0; k < L::kSub; ++k)
-            ptx::tma_load_3d_hint(&p.tm_q, &bar_q, base + L::kQ + i * L::kTile + k * kSubTileBytes, 64 * k,
-                                  jb.h * p.G, jb.q0 + i * tpt, pol_q);
-      }
-      ++nq;
-      for (int j = jb.kv_lo; j < jb.kv_hi; ++j, ++g) {
-        const int st = g & 1;
-        const uint32_t free_par = ((g >> 1) - 1) & 1;
-        const int k0 = jb.sp.key(j) + (lane << p.b.page_log2);
-        bool want = false;
-        int page = -1;
-        if (lane < boxes) {
-          want = k0 < jb.sp.hi_max &&
-                 (k0 + (1 << p.b.page_log2) > jb.sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
-          if (want) page = __ldg(p.b.page_table + jb.b * p.b.table_stride + (k0 >> p.b.page_log2));
+    const int box = lane & (boxes - 1), plane = lane / boxes;
+    const bool copies = plane < L::kSub;
+    const uint32_t dst0 = plane * kSubTileBytes + (box << p.b.page_log2) * 128;
+    int j = 0, n = 0, page = -1;
+    bool ok = true, v_missing = false, want = false, fresh = false;
+    // the next tile, with the load of its page entry under way; fresh: it is its unit's first
+    auto advance = [&]() -> bool {
+      fresh = false;
+      for (++j; j >= n;) {
+        if (!walk.next(jb)) return false;
+        if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        if (jb.head) {
+          rec.x = 1;
+          rec.y = !jb.tail;
+        } else if (jb.tail) {
+          rec.z = jb.b;
+          rec.w = jb.place;
         }
-        const bool good = page >= 0 && page < p.b.n_pages;
-        if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-        const uint32_t pages = __ballot_sync(0xffffffffu, good);
-        const int pg = good ? page : p.b.n_pages;  // a page that is none: read out of bounds on purpose, zeros
-        ok = g < 2 || ptx::mbar_wait(&bar_ke[st], free_par, abort, p.status, RC_ETIMEOUT);
+        j = jb.kv_lo;
+        n = jb.kv_hi;
+        fresh = true;
+      }
+      const int k0 = jb.sp.key(j) + (box << p.b.page_log2);
+      want = k0 < jb.sp.hi_max &&
+             (k0 + (1 << p.b.page_log2) > jb.sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
+      page = want ? __ldg(p.b.page_table + jb.b * p.b.table_stride + (k0 >> p.b.page_log2)) : -1;
+      return true;
+    };
+    for (bool more = advance(); more; ++g) {
+      const int st = g & 1;
+      const uint32_t free_par = ((g >> 1) - 1) & 1;
+      const bool good = page >= 0 && page < p.b.n_pages;
+      if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      const uint32_t pages = __ballot_sync(0xffffffffu, good);
+      const int pg = good ? page : p.b.n_pages;  // a page that is none: read out of bounds on purpose, zeros
+      const int h = jb.h, t0 = jb.sp.key(j), t1 = t0 + kTileRows;
+      const bool in_sink = p.mask.window > 0 && t1 <= p.mask.sink_tok;
+      const int4 info =
+          make_int4(t0, (int)pages,
+                    t1 <= jb.sp.hi_min && (t0 >= jb.sp.lo_max || in_sink) && __all_sync(0xffffffffu, good),
+                    !(t1 <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || in_sink)));
+      if (fresh) {
+        ok = nq == 0 || ptx::mbar_wait(&bar_qe, (nq - 1) & 1, abort, p.status, RC_ETIMEOUT);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         if (lane == 0) {
-          // S of tile g - 2 is complete, issued after the P of tile g - 3: the
-          // softmax is past tile g - 4, whose word this was
-          readable[g & 3] = pages;
-          ptx::mbar_arrive_expect_tx(&bar_kf[st], L::kTile);
+          const int nt = jb.has1 ? 2 : 1;
+          ptx::mbar_arrive_expect_tx(&bar_q, nt * L::kSub * tpt * p.G * 128);
+          for (int i = 0; i < nt; ++i)
+            for (int k = 0; k < L::kSub; ++k)
+              ptx::tma_load_3d_hint(&p.tm_q, &bar_q, base + L::kQ + i * L::kTile + k * kSubTileBytes, 64 * k,
+                                    h * p.G, jb.q0 + i * tpt, pol_q);
         }
-        __syncwarp();
-        if (lane < boxes)
-          for (int k = 0; k < L::kSub; ++k)
-            ptx::tma_load_4d_hint(&p.tm_k, &bar_kf[st],
-                                  base + L::kK + st * L::kTile + k * kSubTileBytes + lane * box_bytes, 64 * k, 0, jb.h,
-                                  pg, pol_kv);
-        ok = g < 2 || ptx::mbar_wait(&bar_ve[st], free_par, abort, p.status, RC_ETIMEOUT);
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) {
-          ++g;  // its K is in flight, its V is not
-          v_missing = true;
-          break;
-        }
-        if (lane == 0) ptx::mbar_arrive_expect_tx(&bar_vf[st], L::kTile);
-        __syncwarp();
-        if (lane < boxes)
-          for (int k = 0; k < L::kSub; ++k)
-            ptx::tma_load_4d_hint(&p.tm_v, &bar_vf[st],
-                                  base + L::kV + st * L::kTile + k * kSubTileBytes + lane * box_bytes, 64 * k, 0, jb.h,
-                                  pg, pol_kv);
+        ++nq;
       }
+      ok = g < 2 || ptx::mbar_wait(&bar_ke[st], free_par, abort, p.status, RC_ETIMEOUT);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (lane == 0) {
+        // S of tile g - 2 is complete, issued after the P of tile g - 3: the
+        // softmax is past tile g - 4, whose word this was
+        tile_info[g & 3] = info;
+        ptx::mbar_arrive_expect_tx(&bar_kf[st], L::kTile);
+      }
+      __syncwarp();
+      if (copies)
+        ptx::tma_load_4d_hint(&p.tm_k, &bar_kf[st], base + L::kK + st * L::kTile + dst0, 64 * plane, 0, h, pg, pol_kv);
+      more = advance();
+      ok = g < 2 || ptx::mbar_wait(&bar_ve[st], free_par, abort, p.status, RC_ETIMEOUT);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) {
+        ++g;  // its K is in flight, its V is not
+        v_missing = true;
+        break;
+      }
+      if (lane == 0) ptx::mbar_arrive_expect_tx(&bar_vf[st], L::kTile);
+      __syncwarp();
+      if (copies)
+        ptx::tma_load_4d_hint(&p.tm_v, &bar_vf[st], base + L::kV + st * L::kTile + dst0, 64 * plane, 0, h, pg, pol_kv);
+      __syncwarp();
     }
     if (lane == 0) {
       p.rec[blockIdx.x] = rec;
@@ -448,7 +463,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     const float thresh = kRescaleLog2 / c;
     const int qi = grp * tpt + row / p.G;         // this row's query within the pair
     const bool row_in = row < tpt * p.G;
-    const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
     int gs = 0;  // this group's tiles so far (phase of bar_s / bar_p)
     int gt = 0;  // the CTA's tiles so far (stage of K and V)
     int nj = 0;  // this group's jobs so far (phase of bar_o: one commit per job)
@@ -470,41 +484,37 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         continue;
       }
       const bool live = row_in && qi < jb.tokens;
-      // rows of no query take the widest mask, so that they never slow their warp
-      RowMask rm{jb.sp.lo_min, jb.sp.hi_max};
-      if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
       bool ok = true;
+      const int n_tiles = max(0, jb.kv_hi - jb.kv_lo);
       int done = 0;
-      for (int j = jb.kv_lo; j < jb.kv_hi; ++j) {
+      for (; done < n_tiles;) {
         if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         ptx::tc_fence_after();
-        const int t0 = jb.sp.key(j), h0 = t0 + ch * 64;  // this warp's keys: [h0, h0 + 64)
-        const uint32_t pages = readable[gt & 3];
-        // pages of this half that are there, as a bit per page
-        const int lg = p.b.page_log2;
-        const uint32_t all_pages = lg >= 6 ? 1u : (1u << (64 >> lg)) - 1;
-        const uint32_t half_pages = (pages >> ((ch * 64) >> lg)) & all_pages;
-        const bool full = __all_sync(0xffffffffu, h0 + 64 <= rm.hi && (h0 >= rm.lo || h0 + 64 <= sink) &&
-                                                      half_pages == all_pages);
-        uint32_t va = 0xffffffffu, vb = 0xffffffffu;  // visible keys, a bit each
+        const int4 info = tile_info[gt & 3];
+        const bool full = info.z != 0;
+        uint32_t va = 0xffffffffu, vb = 0xffffffffu;  // visible keys of this warp's half, a bit each
         if (!full) {
+          // rows of no query take the widest mask
+          const int h0 = info.x + ch * 64, lg = p.b.page_log2;
+          RowMask rm{jb.sp.lo_min, jb.sp.hi_max};
+          if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
+          const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
           auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
           unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
-          if (half_pages != all_pages) {
-            unsigned long long pm = 0;
-            for (int k = 0; k < 64; k += min(64, 1 << lg))
-              if ((half_pages >> (k >> lg)) & 1) pm |= below(min(64, 1 << lg)) << k;
-            v &= pm;
-          }
+          const uint32_t pages = (uint32_t)info.y >> ((ch * 64) >> lg);
+          const int step = min(64, 1 << lg);
+          for (int k = 0; k < 64; k += step)
+            if (!((pages >> (k >> lg)) & 1)) v &= ~(below(step) << k);
           va = (uint32_t)v;
           vb = (uint32_t)(v >> 32);
         }
         // V rows that no query of the pair sees: zero, before group 0's P lets the product start
-        if (grp == 0 && !(t0 + kTileRows <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || t0 + kTileRows <= sink))) {
+        if (grp == 0 && info.w) {
           const int st = gt & 1;
           if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
-          const int vr = (int)threadIdx.x >> 1, key = t0 + vr;
+          const int vr = (int)threadIdx.x >> 1, key = info.x + vr;
+          const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
           if (!(key < jb.sp.hi_max && (key >= jb.sp.lo_min || key < sink))) {
             uint8_t* dst = base + L::kV + st * L::kTile + vr * 128 + (threadIdx.x & 1) * 64;
 #pragma unroll

@@ -30,11 +30,13 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
   const int tid = threadIdx.x, c = blockIdx.x;
   if (tid == 0) last_sh = p.n_ctas - 1;
   ptx::grid_wait();
-  const PartRecord rec = p.rec[c];
-  if (rec.z < 0) return;
+  // records and parts come from L2 (ld.cg): this block's SM may have cached
+  // their addresses before the attention kernel wrote them
+  const PartRecord rec = __ldcg(p.rec + c);
+  if (rec.z < 0 || rec.z >= p.b.n_seqs) return;
   __syncthreads();
   for (int i = c + 1 + tid; i < p.n_ctas; i += kCombThreads) {
-    const PartRecord r = p.rec[i];
+    const PartRecord r = __ldcg(p.rec + i);
     if (r.y) atomicMin(&last_sh, i);
   }
   __syncthreads();
@@ -70,11 +72,11 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   if (grp < groups) {
     for (int i = grp; i < parts; i += groups) {
-      if (i > 0 && !p.rec[c + i].x) continue;  // a CTA whose range is empty
+      if (i > 0 && !__ldcg(&p.rec[c + i].x)) continue;  // a CTA whose range is empty
       const size_t at = (size_t)(2 * (c + i) + (i == 0)) * kUnitRows + row;
-      const float pl = p.part_lse[at];
+      const float pl = __ldcg(p.part_lse + at);
       const float4* src = reinterpret_cast<const float4*>(p.part_o + at * D + col);
-      const float4 a = src[0], b = src[1];
+      const float4 a = __ldcg(src), b = __ldcg(src + 1);
       if (pl == -INFINITY) continue;
       const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
       const float mn = fmaxf(m, pl), f = exp2f(m - mn), w = exp2f(pl - mn);

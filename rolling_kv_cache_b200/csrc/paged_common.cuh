@@ -26,10 +26,14 @@ __device__ __forceinline__ RowMask row_mask(const MaskView& m, int at, int L) {
 template <int TK>
 struct TileSpan {
   int n_sink, from, n;
-  int lo_min, hi_max;  // union of what the queries see: [0, sinks) and [lo_min, hi_max)
+  int lo_min, hi_max;  // some query sees: [lo_min, hi_max) and the sinks below hi_max
+  int lo_max, hi_min;  // every query sees: [lo_max, hi_min) and the sinks below hi_min
   __device__ __forceinline__ void init(const MaskView& m, int first, int last, int L) {
-    hi_max = row_mask(m, last, L).hi;
-    lo_min = row_mask(m, max(first, 0), L).lo;
+    const RowMask a = row_mask(m, first, L), b = row_mask(m, last, L);
+    lo_min = a.lo;
+    lo_max = b.lo;
+    hi_min = a.hi;
+    hi_max = b.hi;
     const int n_end = (hi_max + TK - 1) / TK;
     n_sink = 0;
     from = 0;

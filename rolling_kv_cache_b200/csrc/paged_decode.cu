@@ -132,60 +132,65 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       ptx::tma_prefetch_desc(&p.tm_v);
     }
     const uint64_t pol = ptx::l2_policy(false);
-    // boxes of a tile: page lanes (keys [i * box, i * box + box)), each with kSub planes of K and of V
+    // a tile is `boxes` runs of box_rows keys, each in one page; a lane copies
+    // one run's 64 dims of K or of V
     const int boxes = kTK / p.box_rows;
     const int in_page = (1 << p.b.page_log2) - 1;
-    int g = 0;
-    bool ok = true;
-    int4 rec = make_int4(0, 0, -1, 0);
-    while (ok && walk.next(u)) {
-      const Seq s = load_seq(p.b, p.n_tok, u.b);
-      TileSpan<kTK> sp;
-      sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-      if (lane == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-      if (u.lo > 0) {
-        rec.x = 1;
-        rec.y = u.hi == u.total;
-      } else if (u.hi < u.total) {
-        rec.z = u.b;
-        rec.w = u.h;
+    const int box = lane & (boxes - 1), part = lane / boxes;
+    const bool copies = part < 2 * L::kSub;
+    const bool is_v = part >= L::kSub;
+    const int plane = is_v ? part - L::kSub : part;
+    const uint32_t dst0 = (is_v ? L::kTile : 0) + plane * L::kPlane + box * p.box_rows * 128;
+    int g = 0, j = 0, n = 0, k0 = 0, page = -1;
+    bool want = false, ok = true;
+    PartRecord rec = make_int4(0, 0, -1, 0);
+    TileSpan<kTK> sp;
+    // the next tile, with the load of its page entry under way
+    auto advance = [&]() -> bool {
+      for (++j; j >= n;) {
+        if (!walk.next(u)) return false;
+        const Seq s = load_seq(p.b, p.n_tok, u.b);
+        sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+        if (lane == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        if (u.lo > 0) {
+          rec.x = 1;
+          rec.y = u.hi == u.total;
+        } else if (u.hi < u.total) {
+          rec.z = u.b;
+          rec.w = u.h;
+        }
+        j = u.lo;
+        n = min(u.hi, sp.n);
       }
-      const int n = min(u.hi, sp.n);
-      for (int j = u.lo; j < n; ++j, ++g) {
-        const int t0 = sp.key(j);
-        int page = -1;
-        bool want = false;
-        const int k0 = t0 + lane * p.box_rows;
-        if (lane < boxes) {
-          want = k0 < sp.hi_max && (k0 + p.box_rows > sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
-          if (want) page = __ldg(p.b.page_table + u.b * p.b.table_stride + (k0 >> p.b.page_log2));
-        }
-        const bool good = page >= 0 && page < p.b.n_pages;
-        if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-        const uint32_t pages = __ballot_sync(0xffffffffu, good);
-        const int st = g % L::kStages;
-        if (g >= L::kStages) {
-          ok = ptx::mbar_wait(&bar_empty[st], (g / L::kStages - 1) & 1, abort, p.status, RC_ETIMEOUT);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-        }
-        if (lane == 0) {
-          readable[st] = pages;
-          ptx::mbar_arrive_expect_tx(&bar_full[st], L::kStage);
-        }
-        __syncwarp();
-        if (lane < boxes) {
-          // a page that is none is read out of bounds on purpose: the copy fills zeros
-          const int pg = good ? page : p.b.n_pages, row = good ? (k0 & in_page) : 0;
-          uint8_t* dst = base + st * L::kStage + lane * p.box_rows * 128;
-#pragma unroll
-          for (int i = 0; i < L::kSub; ++i) {
-            ptx::tma_load_4d_hint(&p.tm_k, &bar_full[st], dst + i * L::kPlane, 64 * i, row, u.h, pg, pol);
-            ptx::tma_load_4d_hint(&p.tm_v, &bar_full[st], dst + L::kTile + i * L::kPlane, 64 * i, row, u.h, pg, pol);
-          }
-        }
-        __syncwarp();
+      k0 = sp.key(j) + box * p.box_rows;
+      want = k0 < sp.hi_max && (k0 + p.box_rows > sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
+      page = want ? __ldg(p.b.page_table + u.b * p.b.table_stride + (k0 >> p.b.page_log2)) : -1;
+      return true;
+    };
+    for (bool more = advance(); more; ++g) {
+      const int pg0 = page, row0 = k0 & in_page, h = u.h;
+      const bool wanted = want;
+      more = advance();
+      const bool good = pg0 >= 0 && pg0 < p.b.n_pages;
+      if (wanted && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      const uint32_t pages = __ballot_sync(0xffffffffu, good);
+      const int st = g % L::kStages;
+      if (g >= L::kStages) {
+        ok = ptx::mbar_wait(&bar_empty[st], (g / L::kStages - 1) & 1, abort, p.status, RC_ETIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
       }
+      if (lane == 0) {
+        readable[st] = pages;
+        ptx::mbar_arrive_expect_tx(&bar_full[st], L::kStage);
+      }
+      __syncwarp();
+      // a page that is none is read out of bounds on purpose: the copy fills zeros
+      uint8_t* dst = base + st * L::kStage + dst0;
+      const int row = good ? row0 : 0, pg = good ? pg0 : p.b.n_pages;
+      if (copies && !is_v) ptx::tma_load_4d_hint(&p.tm_k, &bar_full[st], dst, plane * 64, row, h, pg, pol);
+      if (copies && is_v) ptx::tma_load_4d_hint(&p.tm_v, &bar_full[st], dst, plane * 64, row, h, pg, pol);
+      __syncwarp();
     }
     if (lane == 0) {
       p.rec[blockIdx.x] = rec;
