@@ -73,7 +73,9 @@ struct MaskView {
 // Attention over pages: one call's inputs and outputs.
 struct alignas(64) PagedAttnParams {
   CUtensorMap tm_q;    // prefill only: q as (d, q_heads, n_tok), box {64, G, 128 / G}
-  CUtensorMap tm_k;    // pages as (d, page, heads, n_pages), box {64, box_rows, 1, 1}
+  // prefill: pages as (d, page, heads, n_pages), box {64, page, 1, 1}; decode: as
+  // (64, page, d / 64, heads, n_pages), box {64, box_rows, d / 64, 1, 1}
+  CUtensorMap tm_k;
   CUtensorMap tm_v;
   BatchView b;
   RowsView q, out;     // byte strides

@@ -317,14 +317,20 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
     p.scale_log2 = (float)(1.4426950408889634 * scale);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
 
-    auto maps = [&](int box_rows) -> rc_status {
+    auto maps = [&](bool planes, int box_rows) -> rc_status {
       p.box_rows = box_rows;
-      const int64_t dims[4] = {d, pg->page_size, pg->kv_heads, pg->n_pages};
-      const int box[4] = {64, box_rows, 1, 1};
-      const int64_t ks[3] = {pg->k_stride[2], pg->k_stride[1], pg->k_stride[0]};
-      const int64_t vs[3] = {pg->v_stride[2], pg->v_stride[1], pg->v_stride[0]};
-      if (rc_status st = encode(&p.tm_k, pg->k_pages, pg->dtype, 4, dims, ks, box)) return st;
-      return encode(&p.tm_v, pg->v_pages, pg->dtype, 4, dims, vs, box);
+      for (int i = 0; i < 2; ++i) {
+        const int64_t* st = i ? pg->v_stride : pg->k_stride;
+        CUtensorMap* map = i ? &p.tm_v : &p.tm_k;
+        void* base = i ? pg->v_pages : pg->k_pages;
+        const int64_t d4[4] = {d, pg->page_size, pg->kv_heads, pg->n_pages}, s4[3] = {st[2], st[1], st[0]};
+        const int64_t d5[5] = {64, pg->page_size, d / 64, pg->kv_heads, pg->n_pages}, s5[4] = {st[2], 64, st[1], st[0]};
+        const int b4[4] = {64, box_rows, 1, 1}, b5[5] = {64, box_rows, d / 64, 1, 1};
+        if (rc_status e = planes ? encode(map, base, pg->dtype, 5, d5, s5, b5)
+                                 : encode(map, base, pg->dtype, 4, d4, s4, b4))
+          return e;
+      }
+      return RC_OK;
     };
     auto prefill = [&](const rc::PagedAttnParams& x) -> rc_status {
       if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "paged attention launch");
@@ -336,7 +342,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       const int64_t st3[2] = {q->head_stride, q->tok_stride};
       const int box[3] = {64, w.group, 128 / w.group};
       if (rc_status st = encode(&p.tm_q, q->data, pg->dtype, 3, dims, st3, box)) return st;
-      if (rc_status st = maps(pg->page_size)) return st;
+      if (rc_status st = maps(false, pg->page_size)) return st;
     }
     if (w.prefix) {
       rc::PagedAttnParams x = p;  // every query of the batch against the prefix's pages
@@ -352,7 +358,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       p.prev_lse = x.pre_lse;
     }
     if (!w.decode) return prefill(p);
-    if (rc_status st = maps(std::min(pg->page_size, 64))) return st;
+    if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
     if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, s)) return cuda_failed(e, "paged attention launch");
     if (cudaError_t e = rc::launch_paged_combine(p, bf16, d, true, s)) return cuda_failed(e, "combine launch");
     return RC_OK;

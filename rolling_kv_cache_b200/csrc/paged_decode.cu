@@ -12,8 +12,8 @@
 // alike. Each CTA finds its range from the lengths on the device. A unit cut
 // between CTAs leaves parts for the combine kernel.
 //
-// One warp issues TMA copies of the tiles' pages (a box per page and 64 dims,
-// 128-byte swizzle) into a ring of 160 KB, running ahead across units, so
+// One warp issues TMA copies of the tiles' pages (a box per page, its 64-dim
+// planes one after the other, 128-byte swizzle) into a ring of 128 KB, running ahead across units, so
 // that about that much of HBM reads is in flight per SM. Two groups of four warps
 // take alternate tiles; a warp owns 16 keys of its tile: S = Q K^T and O += P V
 // by warp-level 16 x 8 x 16 matrix steps on ldmatrix fragments (the 16 rows
@@ -34,16 +34,21 @@ namespace {
 constexpr int kTK = 64;                       // keys per tile
 constexpr int kConsumers = 8;                 // warps
 constexpr int kDecThreads = (kConsumers + 1) * 32;
-constexpr int kRingBytes = 160 * 1024;
+constexpr int kRingBytes = 128 * 1024;
 constexpr float kDecRescaleLog2 = 8.f;
 
 template <int D>
 struct DecLayout {
   static constexpr int kSub = D / 64;
-  static constexpr uint32_t kPlane = kTK * 128;          // 64 keys x 64 dims
-  static constexpr uint32_t kTile = kPlane * kSub;       // K or V of a tile
+  static constexpr uint32_t kTile = kTK * 128 * kSub;    // K or V of a tile: [box][64-dim plane][box row][128 bytes]
   static constexpr uint32_t kStage = 2 * kTile;
-  static constexpr int kStages = kRingBytes / kStage;    // 5 at d = 128, 10 at d = 64
+  static constexpr int kStages = kRingBytes / kStage;    // 4 at d = 128, 8 at d = 64
+  // Tiles alternate between the two groups of warps, so an even number of
+  // stages gives each stage to one group. With an odd number a group that waits
+  // for its tile in a stage whose last tile, the other group's, has not
+  // landed would see the completed phase before that one, of the same parity,
+  // and go on with stale data.
+  static_assert(kStages % 2 == 0, "a stage belongs to one group of warps");
   static constexpr int kOPad = D + 8;                    // row stride of a merge buffer: spreads rows over banks
   static constexpr uint32_t kMerge = kRingBytes;         // 4 buffers [16][kOPad] fp32
   static constexpr uint32_t kPre = kMerge + 4 * 16 * kOPad * 4;
@@ -133,14 +138,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     const uint64_t pol = ptx::l2_policy(false);
     // a tile is `boxes` runs of box_rows keys, each in one page; a lane copies
-    // one run's 64 dims of K or of V
+    // one run of K or of V
     const int boxes = kTK / p.box_rows;
     const int in_page = (1 << p.b.page_log2) - 1;
-    const int box = lane & (boxes - 1), part = lane / boxes;
-    const bool copies = part < 2 * L::kSub;
-    const bool is_v = part >= L::kSub;
-    const int plane = is_v ? part - L::kSub : part;
-    const uint32_t dst0 = (is_v ? L::kTile : 0) + plane * L::kPlane + box * p.box_rows * 128;
+    const int box = lane & (boxes - 1);
+    const bool is_k = lane < boxes, is_v = !is_k && lane < 2 * boxes;
+    const uint32_t dst0 = (is_v ? L::kTile : 0) + box * p.box_rows * 128 * L::kSub;
     int g = 0, j = 0, n = 0, k0 = 0, page = -1;
     bool want = false, ok = true;
     PartRecord rec = make_int4(0, 0, -1, 0);
@@ -188,8 +191,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       // a page that is none is read out of bounds on purpose: the copy fills zeros
       uint8_t* dst = base + st * L::kStage + dst0;
       const int row = good ? row0 : 0, pg = good ? pg0 : p.b.n_pages;
-      if (copies && !is_v) ptx::tma_load_4d_hint(&p.tm_k, &bar_full[st], dst, plane * 64, row, h, pg, pol);
-      if (copies && is_v) ptx::tma_load_4d_hint(&p.tm_v, &bar_full[st], dst, plane * 64, row, h, pg, pol);
+      if (is_k) ptx::tma_load_5d_hint(&p.tm_k, &bar_full[st], dst, 0, row, 0, h, pg, pol);
+      if (is_v) ptx::tma_load_5d_hint(&p.tm_v, &bar_full[st], dst, 0, row, 0, h, pg, pol);
       __syncwarp();
     }
     if (lane == 0) {
@@ -205,6 +208,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   // -------------------------------------------------------------- consumers
   const int grp = warp >> 2, kw = (warp & 3) * 16;  // this warp's keys of its group's tiles
   const int r0 = lane >> 2, r1 = r0 + 8, cq = (lane & 3) * 2;
+  // the warp's 16 keys lie in one box: its start, their first row in it, and the box's plane stride
+  const uint32_t plane = p.box_rows * 128, box0 = (kw / p.box_rows) * plane * L::kSub;
+  const int krow0 = kw & (p.box_rows - 1);
   const float c = p.scale_log2, thresh = kDecRescaleLog2 / c;
   int g = 0, nu = 0;
   bool alive = true;  // a warp whose wait gave up still meets the others at the merges' barriers
@@ -246,12 +252,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       const uint32_t sK = base_u32 + st * L::kStage, sV = sK + L::kTile;
       float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       {
-        const int row = kw + (lane >> 4) * 8 + (lane & 7);
-        const uint32_t a = sK + row * 128;
+        const int row = krow0 + (lane >> 4) * 8 + (lane & 7);
+        const uint32_t a = sK + box0 + row * 128;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t kf[4];
-          ptx::ldsm4(kf, a + (k >> 2) * L::kPlane + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
+          ptx::ldsm4(kf, a + (k >> 2) * plane + ((((k & 3) * 2 + ((lane >> 3) & 1)) ^ (row & 7)) << 4));
           ptx::mma16816<BF16>(x[0], qf[k], kf[0], kf[1]);
           ptx::mma16816<BF16>(x[1], qf[k], kf[2], kf[3]);
         }
@@ -318,12 +324,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       const uint32_t pf[4] = {ptx::pack16x2<BF16>(x[0][0], x[0][1]), ptx::pack16x2<BF16>(x[0][2], x[0][3]),
                               ptx::pack16x2<BF16>(x[1][0], x[1][1]), ptx::pack16x2<BF16>(x[1][2], x[1][3])};
       {
-        const int row = kw + (lane & 15);
-        const uint32_t a = sV + row * 128;
+        const int row = krow0 + (lane & 15);
+        const uint32_t a = sV + box0 + row * 128;
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           uint32_t vf[4];
-          ptx::ldsm4_t(vf, a + (k >> 2) * L::kPlane + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) << 4));
+          ptx::ldsm4_t(vf, a + (k >> 2) * plane + ((((k & 3) * 2 + (lane >> 4)) ^ (row & 7)) << 4));
           ptx::mma16816<BF16>(o[2 * k], pf, vf[0] & keep0, vf[1] & keep1);
           ptx::mma16816<BF16>(o[2 * k + 1], pf, vf[2] & keep0, vf[3] & keep1);
         }
