@@ -22,14 +22,19 @@
 // so that while one softmax group turns S into P the tensor core runs the
 // other group's two products.
 //
-// Units differ in length (ragged batches, causal and window masks), so their
-// tiles, in (sequence, key head, pair) order, are cut into equal ranges, one per CTA;
-// every CTA finds its own range from the lengths on the device. A unit cut between CTAs
-// leaves its parts for the combine kernel.
+// Schedule, found by every CTA from the lengths on the device: units in
+// (sequence, key head, pair) order; CTA c of G first takes whole units c, c + G,
+// ... for as many rounds as leave no CTA above the average of the whole
+// batch's tiles (the pairs of a head then walk its K/V tiles together, which
+// come from DRAM once), and the tiles of the units left over, in order, are
+// cut into one range per CTA, sized so that every CTA's total is the
+// average (units differ in length: ragged batches, causal and window masks).
+// A unit cut between CTAs leaves its parts for the combine kernel.
 //
 // Keys that no query of the pair sees (behind the sequence, before its windows)
-// are masked in S, and their V rows are zeroed in shared memory before the
-// product, so that what their bits hold stays out; pages that are none are
+// are masked in S (-inf, written back to TMEM by a tile's softmax warps before
+// they use it, in boundary tiles only), and their V rows are zeroed in shared
+// memory before the product, so that what their bits hold stays out; pages that are none are
 // filled with zeros by an out-of-range copy and masked.
 //
 // Every wait is bounded (2 s) and reports RC_ETIMEOUT through the status
@@ -48,6 +53,7 @@ constexpr int kProducerWarp = 16;
 constexpr int kMmaWarp = 17;
 constexpr int kPreThreads = 18 * 32;
 constexpr float kRescaleLog2 = 8.0f;
+constexpr int kMaxRounds = 64;
 
 template <int D>
 struct PreLayout {
@@ -56,9 +62,14 @@ struct PreLayout {
   static constexpr uint32_t kQ = 0;              // Q0, Q1
   static constexpr uint32_t kK = 2 * kTile;      // 2 stages
   static constexpr uint32_t kV = 4 * kTile;      // 2 stages
-  static constexpr uint32_t kPre = 6 * kTile;    // tiles of the sequences, summed
-  static constexpr uint32_t kBytes = kPre + (kMaxSeqs + 1) * 4;
+  static constexpr uint32_t kBytes = 6 * kTile;
   static constexpr uint32_t kDynSmem = kBytes + 1024;
+  // the schedule's sums, gone before the first load: tiles and pairs of the
+  // sequences, and each CTA's tiles after each round
+  static constexpr uint32_t kTilesBefore = 0;
+  static constexpr uint32_t kPairsBefore = kTilesBefore + (kMaxSeqs + 1) * 4;
+  static constexpr uint32_t kLoads = kPairsBefore + (kMaxSeqs + 1) * 4;
+  static_assert(kLoads + kMaxRounds * kMaxPersistentCtas * 4 <= kBytes, "the schedule fits the tiles' memory");
 };
 
 // KV tiles [kv_lo, kv_hi) of one pair of query tiles of key head h of
@@ -96,34 +107,65 @@ __device__ __forceinline__ void pair_span(const PagedAttnParams& p, const Seq& s
   j.sp.init(p.mask, j.at0, j.at0 + j.tokens - 1, s.L);
 }
 
-// Where a CTA's range begins.
+// A unit, and a tile within it.
 struct Start {
   int b, h, pair, off;
 };
 
+// This CTA's work: `rounds` whole units from `whole` on, G apart, then the
+// tiles [pos, end) of the batch, which begin at `range`.
+struct Plan {
+  Start whole, range;
+  int rounds, pos, end;
+};
+
 struct PairWalk {
   const PagedAttnParams* p;
-  int n_seqs, tpt, pos, end;
+  int n_seqs, tpt, pos, end, rounds;
   int b, h, pair, off, pairs;
+  Start range;
   Seq s;
 
   __device__ void load() {
     s = pre_seq(*p, b);
     pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
   }
-  __device__ void init(const PagedAttnParams& prm, const Start& st, int pos_, int end_) {
-    p = &prm;
-    n_seqs = prm.pre_o ? 1 : prm.b.n_seqs;
-    tpt = kTileRows / prm.G;
-    pos = pos_;
-    end = end_;
+  __device__ void go(const Start& st) {
     b = st.b;
     h = st.h;
     pair = st.pair;
     off = st.off;
-    if (pos < end) load();
+    load();
   }
-  __device__ bool next(Job& j) {
+  __device__ void init(const PagedAttnParams& prm, const Plan& pl) {
+    p = &prm;
+    n_seqs = prm.pre_o ? 1 : prm.b.n_seqs;
+    tpt = kTileRows / prm.G;
+    pos = pl.pos;
+    end = pl.end;
+    rounds = pl.rounds;
+    range = pl.range;
+    if (rounds > 0) go(pl.whole);
+    else if (pos < end) go(range);
+  }
+  __device__ __noinline__ bool next(Job& j) {
+    if (rounds > 0) {
+      pair_span(*p, s, pair, tpt, j);
+      fill(j, 0, max(j.sp.n, 1));
+      if (--rounds > 0) {
+        int i = h * pairs + pair + (int)gridDim.x;
+        while (i >= p->Hk * pairs) {
+          i -= p->Hk * pairs;
+          ++b;
+          load();
+        }
+        h = i / pairs;
+        pair = i - h * pairs;
+      } else if (pos < end) {
+        go(range);
+      }
+      return true;
+    }
     if (pos >= end) return false;
     while (pair >= pairs) {
       pair = 0;
@@ -134,25 +176,216 @@ struct PairWalk {
       }
     }
     pair_span(*p, s, pair, tpt, j);
-    const int total = max(j.sp.n, 1);
-    const int len = min(total - off, end - pos);
-    j.b = b;
-    j.h = h;
-    j.q0 = s.q0 + pair * 2 * tpt;
-    j.L = s.L;
-    j.kv_lo = off;
-    j.kv_hi = min(off + len, j.sp.n);
-    j.has1 = j.tokens > tpt;
-    j.head = off > 0;
-    j.tail = off + len < total;
-    j.slot = j.head ? 2 * (int)blockIdx.x : (j.tail ? 2 * (int)blockIdx.x + 1 : -1);
-    j.place = h * pairs + pair;
+    const int len = min(max(j.sp.n, 1) - off, end - pos);
+    fill(j, off, len);
     pos += len;
     off = 0;
     ++pair;
     return true;
   }
+  __device__ void fill(Job& j, int lo, int len) const {
+    j.b = b;
+    j.h = h;
+    j.q0 = s.q0 + pair * 2 * tpt;
+    j.L = s.L;
+    j.kv_lo = lo;
+    j.kv_hi = min(lo + len, j.sp.n);
+    j.has1 = j.tokens > tpt;
+    j.head = lo > 0;
+    j.tail = lo + len < max(j.sp.n, 1);
+    j.slot = j.head ? 2 * (int)blockIdx.x : (j.tail ? 2 * (int)blockIdx.x + 1 : -1);
+    j.place = h * pairs + pair;
+  }
 };
+
+// The largest b < n with per * before[b] <= x.
+__device__ __forceinline__ int last_at_most(const int* before, int n, int per, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (per * before[mid] <= x) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// The schedule, by all threads; `mem` is scratch of the layout's kLoads + ... bytes.
+template <int D>
+__device__ __noinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem, int* warp_sums, int* most, int* sums,
+                                          Plan* plan) {
+  using L = PreLayout<D>;
+  int* tiles_before = reinterpret_cast<int*>(mem + L::kTilesBefore);
+  int* pairs_before = reinterpret_cast<int*>(mem + L::kPairsBefore);
+  int* loads = reinterpret_cast<int*>(mem + L::kLoads);  // [round][CTA]
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int n_seqs = p.pre_o ? 1 : p.b.n_seqs, tpt = kTileRows / p.G;
+  const int G = gridDim.x, c = blockIdx.x;
+  // tiles and pairs of each sequence (one key head), a warp a sequence
+  for (int b = warp; b < n_seqs; b += kPreThreads / 32) {
+    const Seq s = pre_seq(p, b);
+    const int pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
+    int sum = 0;
+    for (int q = lane; q < pairs; q += 32) {
+      Job j;
+      pair_span(p, s, q, tpt, j);
+      sum += max(j.sp.n, 1);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) {
+      tiles_before[b] = sum;
+      pairs_before[b] = pairs;
+    }
+  }
+  if (tid < kMaxRounds) most[tid] = 0;
+  if (tid < 2) sums[tid] = 0;
+  __syncthreads();
+  block_prefix<kPreThreads>(tiles_before, n_seqs, warp_sums, [&](int b) { return tiles_before[b]; });
+  block_prefix<kPreThreads>(pairs_before, n_seqs, warp_sums, [&](int b) { return pairs_before[b]; });
+  const int W = p.Hk * tiles_before[n_seqs], U = p.Hk * pairs_before[n_seqs];
+  const int r_max = min(U / G, kMaxRounds);
+  // each CTA's tiles after each round, and the most any has
+  if (tid < G) {
+    int load = 0, b = 0;
+    Seq s;
+    for (int r = 0; r < r_max; ++r) {
+      const int u = tid + r * G;
+      if (r == 0) b = last_at_most(pairs_before, n_seqs, p.Hk, u);
+      while (p.Hk * pairs_before[b + 1] <= u) ++b;
+      s = pre_seq(p, b);
+      Job j;
+      pair_span(p, s, (u - p.Hk * pairs_before[b]) % (pairs_before[b + 1] - pairs_before[b]), tpt, j);
+      load += max(j.sp.n, 1);
+      loads[r * G + tid] = load;
+      atomicMax(&most[r], load);
+    }
+  }
+  __syncthreads();
+  int rounds = 0;
+  while (rounds < r_max && most[rounds] <= W / G) ++rounds;
+  // range of this CTA: what brings it, and those before it, to the average
+  if (rounds > 0 && tid < G) {
+    const int load = loads[(rounds - 1) * G + tid];
+    atomicAdd(&sums[0], load);
+    if (tid < c) atomicAdd(&sums[1], load);
+  }
+  __syncthreads();
+  const int own = rounds > 0 ? loads[(rounds - 1) * G + c] : 0;
+  const int pos = (int)((long long)W * c / G) - sums[1] + sums[0];
+  const int end = (int)((long long)W * (c + 1) / G) - sums[1] - own + sums[0];
+  if (warp == 0) {
+    if (rounds > 0 && lane == 0) {
+      const int b = last_at_most(pairs_before, n_seqs, p.Hk, c);
+      const int pairs = pairs_before[b + 1] - pairs_before[b], i = c - p.Hk * pairs_before[b];
+      plan->whole = Start{b, i / pairs, i % pairs, 0};
+    }
+    if (pos < end) {
+      const int b = last_at_most(tiles_before, n_seqs, p.Hk, pos);
+      const int w = tiles_before[b + 1] - tiles_before[b];
+      const int rem = pos - p.Hk * tiles_before[b], h = rem / w;
+      int left = rem - h * w;
+      const Seq s = pre_seq(p, b);
+      const int pairs = pairs_before[b + 1] - pairs_before[b];
+      for (int q0 = 0; q0 < pairs; q0 += 32) {
+        int t = 0;
+        if (q0 + lane < pairs) {
+          Job j;
+          pair_span(p, s, q0 + lane, tpt, j);
+          t = max(j.sp.n, 1);
+        }
+        int inc = t;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int x = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += x;
+        }
+        if (left >= inc - t && left < inc) plan->range = Start{b, h, q0 + lane, left - (inc - t)};
+        const int sum = __shfl_sync(0xffffffffu, inc, 31);
+        if (left < sum) break;
+        left -= sum;
+      }
+    }
+    if (lane == 0) {
+      plan->rounds = rounds;
+      plan->pos = pos;
+      plan->end = end;
+    }
+  }
+}
+
+// What runs once in many tiles stays out of line, so that its registers are
+// not the tile loop's: the masking of a boundary tile, and a unit's last writes.
+
+// -inf over the scores of one row's 64 keys from h0 on (TMEM columns tS ..)
+// that the row does not see or whose page is none.
+__device__ __noinline__ void mask_scores(uint32_t tS, int h0, RowMask rm, int sink, uint32_t pages, int page_log2) {
+  auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
+  unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
+  const int step = min(64, 1 << page_log2);
+  for (int k = 0; k < 64; k += step)
+    if (!((pages >> (k >> page_log2)) & 1)) v &= ~(below(step) << k);
+#pragma unroll 1
+  for (int cc = 0; cc < 2; ++cc) {
+    const uint32_t vis = (uint32_t)(v >> (32 * cc));
+    uint32_t r[32];
+    ptx::tmem_ld32(tS + cc * 32, r);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 32; ++k) r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
+    ptx::tmem_st32(tS + cc * 32, r);
+  }
+  ptx::tmem_st_wait();
+}
+
+// Zeros the V rows of a tile (from key t0 on, one row to two threads) that no query of the pair sees.
+template <int D>
+__device__ __noinline__ void zero_values(uint8_t* v, int t0, int lo_min, int hi_max, int sink) {
+  const int row = (int)threadIdx.x >> 1, key = t0 + row;
+  if (!(key < hi_max && (key >= lo_min || key < sink))) {
+    uint8_t* dst = v + row * 128 + (threadIdx.x & 1) * 64;
+#pragma unroll
+    for (int k = 0; k < PreLayout<D>::kSub; ++k)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(dst + k * kSubTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+  }
+  ptx::fence_proxy_async_smem();
+}
+
+// A row's D / 2 columns from `col0` on: O (TMEM columns tO .., if have_o) times inv_l, to
+// the output, or, slot >= 0, to row `at` of the partial rows.
+template <int D, bool BF16>
+__device__ __noinline__ void write_row(const PagedAttnParams& p, uint32_t tO, bool have_o, bool live, int slot,
+                                       size_t at, int tok, int head, int col0, float inv_l, float lse2) {
+#pragma unroll 1
+  for (int cc = 0; cc < D / 2; cc += 16) {
+    uint32_t o[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) o[k] = 0u;
+    if (have_o) {
+      ptx::tmem_ld16(tO + cc, o);
+      ptx::tmem_ld_wait();
+    }
+    if (!live) continue;
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+      float acc[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = inv_l == 0.f ? 0.f : __uint_as_float(o[8 * v + k]) * inv_l;
+      const int col = col0 + cc + 8 * v;
+      if (slot < 0) {
+        float lse = lse2;
+        if (p.prev_o) merge_prev<D>(p, tok, head, col, acc, lse);
+        store_row<D, BF16>(p, tok, head, col, acc, lse);
+      } else {
+        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (col == 0) p.part_lse[at] = lse2;
+      }
+    }
+  }
+}
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __grid_constant__ PagedAttnParams p) {
@@ -165,8 +398,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   // that are there (a bit each), whether every query sees all of it, whether some V
   // rows are seen by none
   __shared__ int4 tile_info[4];
-  __shared__ int warp_sums[18];
-  __shared__ Start start_sh;
+  __shared__ int warp_sums[18], most[kMaxRounds], sums[2];
+  __shared__ Plan plan;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
 
@@ -196,69 +429,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     ptx::tmem_relinquish();
   }
   ptx::grid_launch_dependents();
-  // key tiles of each sequence (one key head), a warp a sequence; their sums
-  // give this CTA its range of the batch's tiles
-  int* pre = reinterpret_cast<int*>(base + L::kPre);
-  const int n_seqs = p.pre_o ? 1 : p.b.n_seqs;
-  const int tpt = kTileRows / p.G;
-  for (int b = warp; b < n_seqs; b += kPreThreads / 32) {
-    const Seq s = pre_seq(p, b);
-    const int pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
-    int sum = 0;
-    for (int q = lane; q < pairs; q += 32) {
-      Job j;
-      pair_span(p, s, q, tpt, j);
-      sum += max(j.sp.n, 1);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) pre[b] = sum;
-  }
-  __syncthreads();
-  block_prefix<kPreThreads>(pre, n_seqs, warp_sums, [&](int b) { return pre[b]; });
-  const int W = p.Hk * pre[n_seqs];
-  const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
-  const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
-  if (warp == 0 && pos < end) {
-    int lo = 0, hi = n_seqs - 1;
-    while (lo < hi) {  // the largest b with Hk * pre[b] <= pos
-      const int mid = (lo + hi + 1) >> 1;
-      if (p.Hk * pre[mid] <= pos) lo = mid;
-      else hi = mid - 1;
-    }
-    const int w = pre[lo + 1] - pre[lo];
-    const int rem = pos - p.Hk * pre[lo], h = rem / w;
-    int left = rem - h * w;
-    const Seq s = pre_seq(p, lo);
-    const int pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
-    for (int q0 = 0; q0 < pairs; q0 += 32) {
-      int t = 0;
-      if (q0 + lane < pairs) {
-        Job j;
-        pair_span(p, s, q0 + lane, tpt, j);
-        t = max(j.sp.n, 1);
-      }
-      int inc = t;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      if (left >= inc - t && left < inc) start_sh = Start{lo, h, q0 + lane, left - (inc - t)};
-      const int sum = __shfl_sync(0xffffffffu, inc, 31);
-      if (left < sum) break;
-      left -= sum;
-    }
-  }
+  make_plan<D>(p, base, warp_sums, most, sums, &plan);
+  ptx::fence_proxy_async_smem();  // the plan's scratch is where copies land
   ptx::tc_fence_before();
   __syncthreads();
   ptx::tc_fence_after();
   const uint32_t tmem = tmem_base_sh;
+  const int tpt = kTileRows / p.G;
   volatile int* abort = &abort_sh;
   int dummy_abort = 0;
   volatile int* noabort = reinterpret_cast<volatile int*>(&dummy_abort);
   PairWalk wk_mem;
-  wk_mem.init(p, start_sh, pos, end);
+  wk_mem.init(p, plan);
   // the walk's state lives in local memory (read once per unit), keeping
   // registers for the per-tile work
   PairWalk* volatile wk_ptr = &wk_mem;
@@ -487,58 +669,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
       bool ok = true;
       const int n_tiles = max(0, jb.kv_hi - jb.kv_lo);
-      int done = 0;
-      for (; done < n_tiles;) {
+      for (int left = n_tiles; left > 0; --left) {
         if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         ptx::tc_fence_after();
         const int4 info = tile_info[gt & 3];
-        const bool full = info.z != 0;
-        uint32_t va = 0xffffffffu, vb = 0xffffffffu;  // visible keys of this warp's half, a bit each
-        if (!full) {
-          // rows of no query take the widest mask
-          const int h0 = info.x + ch * 64, lg = p.b.page_log2;
+        if (!info.z) {
+          // some key of the tile is hidden from some row: those scores become
+          // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
+          // query take the widest mask
           RowMask rm{jb.sp.lo_min, jb.sp.hi_max};
           if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
-          const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
-          auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
-          unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
-          const uint32_t pages = (uint32_t)info.y >> ((ch * 64) >> lg);
-          const int step = min(64, 1 << lg);
-          for (int k = 0; k < 64; k += step)
-            if (!((pages >> (k >> lg)) & 1)) v &= ~(below(step) << k);
-          va = (uint32_t)v;
-          vb = (uint32_t)(v >> 32);
+          mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 ? p.mask.sink_tok : 0,
+                      (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
         }
         // V rows that no query of the pair sees: zero, before group 0's P lets the product start
         if (grp == 0 && info.w) {
           const int st = gt & 1;
           if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
-          const int vr = (int)threadIdx.x >> 1, key = info.x + vr;
-          const int sink = p.mask.window > 0 ? p.mask.sink_tok : 0;
-          if (!(key < jb.sp.hi_max && (key >= jb.sp.lo_min || key < sink))) {
-            uint8_t* dst = base + L::kV + st * L::kTile + vr * 128 + (threadIdx.x & 1) * 64;
-#pragma unroll
-            for (int k = 0; k < L::kSub; ++k)
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(dst + k * kSubTileBytes + i * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          ptx::fence_proxy_async_smem();
+          zero_values<D>(base + L::kV + st * L::kTile, info.x, jb.sp.lo_min, jb.sp.hi_max,
+                         p.mask.window > 0 ? p.mask.sink_tok : 0);
         }
-        uint32_t ra[32], rb[32];
-        ptx::tmem_ld32(tS, ra);
-        ptx::tmem_ld32(tS + 32, rb);
-        ptx::tmem_ld_wait();
+        // S in halves, read again for the exponentials: 32 scores at a time leave
+        // the loop's state in registers
+        uint32_t ra[32];
         float mx = -INFINITY;
-        if (full) {
+        ptx::tmem_ld32(tS, ra);
+        ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[k]), __uint_as_float(rb[k]));
-        } else {
+        for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+        ptx::tmem_ld32(tS + 32, ra);
+        ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 32; ++k)
-            mx = ptx::fmax3(mx, (va >> k) & 1u ? __uint_as_float(ra[k]) : -INFINITY,
-                            (vb >> k) & 1u ? __uint_as_float(rb[k]) : -INFINITY);
-        }
+        for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
         float mo;
         if (!swap(mx, mo)) { ok = false; break; }
         const float m_new = ptx::fmax3(m, mx, mo);
@@ -567,52 +729,39 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         // P is rounded to the values' type, the product's operand: off by at most
         // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it
         float sum = 0.f;
-        auto emit = [&](const uint32_t (&r)[32], uint32_t vis, int k0) {
+        auto emit = [&](const uint32_t (&r)[32], int k0) {
           uint32_t pk[16];
-          if (full) {
-            const float2 c2 = make_float2(c, c), nmc2 = make_float2(-mc, -mc);
-            float2 s2 = make_float2(0.f, 0.f);
+          const float2 c2 = make_float2(c, c), nmc2 = make_float2(-mc, -mc);
+          float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float2 x =
-                  ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nmc2);
-              float2 e;
-              if ((k & 7) < kCubicPairs) {
-                e = exp2_cubic2(x);
-              } else {
-                e.x = ptx::ex2(x.x);
-                e.y = ptx::ex2(x.y);
-              }
-              s2 = ptx::fadd2(s2, e);
-              pk[k] = ptx::pack16x2<BF16>(e.x, e.y);
+          for (int k = 0; k < 16; ++k) {
+            const float2 x =
+                ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nmc2);
+            float2 e;
+            if ((k & 7) < kCubicPairs) {
+              e = exp2_cubic2(x);
+            } else {
+              e.x = ptx::ex2(x.x);
+              e.y = ptx::ex2(x.y);
             }
-            sum += s2.x + s2.y;
-          } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float a = (vis >> (2 * k)) & 1u ? ptx::ex2(fmaf(__uint_as_float(r[2 * k]), c, -mc)) : 0.f;
-              const float b =
-                  (vis >> (2 * k + 1)) & 1u ? ptx::ex2(fmaf(__uint_as_float(r[2 * k + 1]), c, -mc)) : 0.f;
-              sum += a + b;
-              pk[k] = ptx::pack16x2<BF16>(a, b);
-            }
+            s2 = ptx::fadd2(s2, e);
+            pk[k] = ptx::pack16x2<BF16>(e.x, e.y);
           }
+          sum += s2.x + s2.y;
           ptx::tmem_st16(tS + k0 / 2, pk);
         };
-        // S is read again rather than kept in registers across the exchange
         ptx::tmem_ld32(tS, ra);
         ptx::tmem_ld_wait();
-        emit(ra, va, 0);
-        ptx::tmem_ld32(tS + 32, rb);
+        emit(ra, 0);
+        ptx::tmem_ld32(tS + 32, ra);
         ptx::tmem_ld_wait();
-        emit(rb, vb, 32);
+        emit(ra, 32);
         ptx::tmem_st_wait();
         l += sum;
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar_p[grp]);
         ++gs;
         ++gt;
-        ++done;
       }
       // epilogue: O / l, merged with the prefix's result where there is one, to
       // the output, or to this CTA's partial slot (fp32, log2-sum-exp); each
@@ -621,40 +770,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       if (ok && !swap(l, l_other)) ok = false;
       const float lt = l + l_other;
       const bool have_o =
-          ok && done > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
-      if (done > 0) ++nj;
+          ok && n_tiles > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
+      if (n_tiles > 0) ++nj;
       ptx::tc_fence_after();
-      // a row that sees nothing has lt = 0: zeros and -inf; a NaN sum stays NaN
-      const float inv_l = lt == 0.f ? 0.f : 1.f / lt;
-      const float lse2 = lt == 0.f ? -INFINITY : m * c + log2f(lt);
-#pragma unroll
-      for (int cc = 0; cc < D / 64; ++cc) {
-        uint32_t o[32];
-        if (have_o) {
-          ptx::tmem_ld32(tO + cc * 32, o);
-          ptx::tmem_ld_wait();
-        }
-        if (!live) continue;
-        const int col = ch * (D / 2) + cc * 32;
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-          float acc[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = have_o && lt != 0.f ? __uint_as_float(o[8 * v + k]) * inv_l : 0.f;
-          if (jb.slot < 0) {
-            const int tok = jb.q0 + qi, head = jb.h * p.G + row % p.G;
-            float lse = lse2;
-            if (p.prev_o) merge_prev<D>(p, tok, head, col + 8 * v, acc, lse);
-            store_row<D, BF16>(p, tok, head, col + 8 * v, acc, lse);
-          } else {
-            const size_t at = (size_t)jb.slot * kPrefillRows + grp * kTileRows + row;
-            float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col + 8 * v);
-            dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-            dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-            if (col + 8 * v == 0) p.part_lse[at] = lse2;
-          }
-        }
-      }
+      // a row that saw nothing kept m = -inf (the cubic turns its scores into
+      // 2^-126, not 0): zeros and -inf; a NaN sum stays NaN
+      const bool none = m == -INFINITY && lt == lt;
+      const float inv_l = none ? 0.f : 1.f / lt;
+      const float lse2 = none ? -INFINITY : m * c + log2f(lt);
+      write_row<D, BF16>(p, tO, have_o, live, jb.slot, (size_t)max(jb.slot, 0) * kPrefillRows + grp * kTileRows + row,
+                         jb.q0 + qi, jb.h * p.G + row % p.G, ch * (D / 2), have_o ? inv_l : 0.f, lse2);
       if (!ok) break;
     }
   }

@@ -15,7 +15,7 @@ struct RowMask {
 // at: the query's position (negative: it sees nothing); L: tokens in the pages.
 __device__ __forceinline__ RowMask row_mask(const MaskView& m, int at, int L) {
   if (at < 0) return RowMask{0, 0};
-  const int f = at / m.frame;
+  const int f = m.frame == 1 ? at : at / m.frame;
   const int lo = m.window > 0 && f >= m.window ? (f - m.window + 1) * m.frame : 0;
   return RowMask{lo, min(L, (f + 1) * m.frame)};
 }
