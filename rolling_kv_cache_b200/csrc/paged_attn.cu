@@ -107,6 +107,15 @@ __device__ __forceinline__ void pair_span(const PagedAttnParams& p, const Seq& s
   j.sp.init(p.mask, j.at0, j.at0 + j.tokens - 1, s.L);
 }
 
+// A unit as the softmax and MMA warps need it.
+struct JobInfo {
+  int tiles;              // its key tiles; -1: the last unit is past
+  int two;                // it has a second query tile
+  int tokens, q0, head0;  // queries, row of q of the first, query head of the tile's first row
+  int at0, L, slot, lo_min, hi_max;
+};
+constexpr int kJobRing = 4;
+
 // A unit, and a tile within it.
 struct Start {
   int b, h, pair, off;
@@ -126,18 +135,18 @@ struct PairWalk {
   Start range;
   Seq s;
 
-  __device__ void load() {
+  __device__ __forceinline__ void load() {
     s = pre_seq(*p, b);
     pairs = (s.n + 2 * tpt - 1) / (2 * tpt);
   }
-  __device__ void go(const Start& st) {
+  __device__ __forceinline__ void go(const Start& st) {
     b = st.b;
     h = st.h;
     pair = st.pair;
     off = st.off;
     load();
   }
-  __device__ void init(const PagedAttnParams& prm, const Plan& pl) {
+  __device__ __forceinline__ void init(const PagedAttnParams& prm, const Plan& pl) {
     p = &prm;
     n_seqs = prm.pre_o ? 1 : prm.b.n_seqs;
     tpt = kTileRows / prm.G;
@@ -148,7 +157,7 @@ struct PairWalk {
     if (rounds > 0) go(pl.whole);
     else if (pos < end) go(range);
   }
-  __device__ __noinline__ bool next(Job& j) {
+  __device__ __forceinline__ bool next(Job& j) {
     if (rounds > 0) {
       pair_span(*p, s, pair, tpt, j);
       fill(j, 0, max(j.sp.n, 1));
@@ -183,7 +192,7 @@ struct PairWalk {
     ++pair;
     return true;
   }
-  __device__ void fill(Job& j, int lo, int len) const {
+  __device__ __forceinline__ void fill(Job& j, int lo, int len) const {
     j.b = b;
     j.h = h;
     j.q0 = s.q0 + pair * 2 * tpt;
@@ -398,6 +407,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   // that are there (a bit each), whether every query sees all of it, whether some V
   // rows are seen by none
   __shared__ int4 tile_info[4];
+  // the units' descriptions, written by the producer (which alone walks the
+  // schedule: the walk's state in 18 warps' local memory would not fit L1)
+  __shared__ JobInfo jobs[kJobRing];
+  __shared__ uint64_t bar_jf[kJobRing], bar_je[kJobRing];
   __shared__ int warp_sums[18], most[kMaxRounds], sums[2];
   __shared__ Plan plan;
   __shared__ uint32_t tmem_base_sh;
@@ -421,6 +434,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     }
     ptx::mbar_init(&bar_fin, 1);
     for (int i = 0; i < 8; ++i) ptx::mbar_init(&bar_pair[i], 64);
+    for (int i = 0; i < kJobRing; ++i) {
+      ptx::mbar_init(&bar_jf[i], 1);
+      ptx::mbar_init(&bar_je[i], kSoftmaxWarps + 1);
+    }
     abort_sh = 0;
     ptx::fence_mbar_init();
   }
@@ -439,14 +456,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   volatile int* abort = &abort_sh;
   int dummy_abort = 0;
   volatile int* noabort = reinterpret_cast<volatile int*>(&dummy_abort);
-  PairWalk wk_mem;
-  wk_mem.init(p, plan);
-  // the walk's state lives in local memory (read once per unit), keeping
-  // registers for the per-tile work
-  PairWalk* volatile wk_ptr = &wk_mem;
-  PairWalk& walk = *wk_ptr;
-  Job jb;
-
   if (warp == kProducerWarp) {
     // ---------------------------------------------------------- producer
     if (lane == 0) {
@@ -454,8 +463,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       ptx::tma_prefetch_desc(&p.tm_k);
       ptx::tma_prefetch_desc(&p.tm_v);
     }
-    int nq = 0, g = 0;
+    int nq = 0, g = 0, nw = 0;
     PartRecord rec = make_int4(0, 0, -1, 0);
+    PairWalk walk;
+    walk.init(p, plan);
+    Job jb;
     // K/V tiles are read by every pair of their head: keep them in L2; Q is read once
     const uint64_t pol_q = ptx::l2_policy(false), pol_kv = ptx::l2_policy(true);
     // a tile is `boxes` pages; a lane copies one page's 64 dims of K, then of V
@@ -465,11 +477,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     const uint32_t dst0 = plane * kSubTileBytes + (box << p.b.page_log2) * 128;
     int j = 0, n = 0, page = -1;
     bool ok = true, v_missing = false, want = false, fresh = false;
+    // describes the next unit to the other warps; n < 0: there is none
+    auto publish = [&](int tiles) {
+      const int slot = nw % kJobRing;
+      if (nw >= kJobRing) {
+        ok = ptx::mbar_wait(&bar_je[slot], (nw / kJobRing - 1) & 1, abort, p.status, RC_ETIMEOUT);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+      }
+      if (lane == 0) {
+        jobs[slot] = JobInfo{tiles, jb.has1, jb.tokens, jb.q0, jb.h * p.G, jb.at0, jb.L, jb.slot, jb.sp.lo_min, jb.sp.hi_max};
+        ptx::mbar_arrive(&bar_jf[slot]);
+      }
+      ++nw;
+    };
     // the next tile, with the load of its page entry under way; fresh: it is its unit's first
     auto advance = [&]() -> bool {
       fresh = false;
       for (++j; j >= n;) {
-        if (!walk.next(jb)) return false;
+        if (!walk.next(jb)) {
+          publish(-1);
+          return false;
+        }
         if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
         if (jb.head) {
           rec.x = 1;
@@ -481,6 +510,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         j = jb.kv_lo;
         n = jb.kv_hi;
         fresh = true;
+        publish(max(0, n - j));
+        if (!ok) return false;
       }
       const int k0 = jb.sp.key(j) + (box << p.b.page_log2);
       want = k0 < jb.sp.hi_max &&
@@ -527,7 +558,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       __syncwarp();
       if (copies)
         ptx::tma_load_4d_hint(&p.tm_k, &bar_kf[st], base + L::kK + st * L::kTile + dst0, 64 * plane, 0, h, pg, pol_kv);
-      more = advance();
       ok = g < 2 || ptx::mbar_wait(&bar_ve[st], free_par, abort, p.status, RC_ETIMEOUT);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) {
@@ -540,6 +570,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       if (copies)
         ptx::tma_load_4d_hint(&p.tm_v, &bar_vf[st], base + L::kV + st * L::kTile + dst0, 64 * plane, 0, h, pg, pol_kv);
       __syncwarp();
+      // only with this tile's loads out: a unit is published once the fourth
+      // before it is done, which may be this tile's when the units between are empty
+      more = advance();
     }
     if (lane == 0) {
       p.rec[blockIdx.x] = rec;
@@ -579,10 +612,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     };
     int nq = 0, g = 0, gp[2] = {0, 0};
     bool ok = true;
-    while (ok && walk.next(jb)) {
-      const int n = jb.kv_hi - jb.kv_lo;
-      if (n <= 0) continue;
-      const bool two = jb.has1;
+    for (int nw = 0; ok; ++nw) {
+      const int slot = nw % kJobRing;
+      if (!ptx::mbar_wait(&bar_jf[slot], (nw / kJobRing) & 1, abort, p.status, RC_ETIMEOUT)) break;
+      const int n = jobs[slot].tiles;
+      const bool two = jobs[slot].two;
+      ptx::mbar_arrive(&bar_je[slot]);
+      if (n < 0) break;
+      if (n == 0) continue;
       if (!ptx::mbar_wait(&bar_q, nq & 1, abort, p.status, RC_ETIMEOUT)) break;
       ++nq;
       if (!ptx::mbar_wait(&bar_kf[g & 1], (g >> 1) & 1, abort, p.status, RC_ETIMEOUT)) break;
@@ -659,16 +696,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       other = buf[ch ^ 1][row];
       return true;
     };
-    while (walk.next(jb)) {
-      if (*abort) break;
-      if (grp == 1 && !jb.has1) {
-        gt += max(0, jb.kv_hi - jb.kv_lo);
+    for (int nw = 0;; ++nw) {
+      const int slot = nw % kJobRing;
+      if (!ptx::mbar_wait(&bar_jf[slot], (nw / kJobRing) & 1, abort, p.status, RC_ETIMEOUT)) break;
+      const JobInfo& jb = jobs[slot];
+      const int n_tiles = jb.tiles;
+      if (n_tiles < 0) break;
+      if (grp == 1 && !jb.two) {
+        gt += n_tiles;
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
         continue;
       }
       const bool live = row_in && qi < jb.tokens;
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
       bool ok = true;
-      const int n_tiles = max(0, jb.kv_hi - jb.kv_lo);
       for (int left = n_tiles; left > 0; --left) {
         if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         ptx::tc_fence_after();
@@ -677,7 +719,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           // some key of the tile is hidden from some row: those scores become
           // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
           // query take the widest mask
-          RowMask rm{jb.sp.lo_min, jb.sp.hi_max};
+          RowMask rm{jb.lo_min, jb.hi_max};
           if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
           mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 ? p.mask.sink_tok : 0,
                       (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
@@ -686,7 +728,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         if (grp == 0 && info.w) {
           const int st = gt & 1;
           if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
-          zero_values<D>(base + L::kV + st * L::kTile, info.x, jb.sp.lo_min, jb.sp.hi_max,
+          zero_values<D>(base + L::kV + st * L::kTile, info.x, jb.lo_min, jb.hi_max,
                          p.mask.window > 0 ? p.mask.sink_tok : 0);
         }
         // S in halves, read again for the exponentials: 32 scores at a time leave
@@ -779,7 +821,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       const float inv_l = none ? 0.f : 1.f / lt;
       const float lse2 = none ? -INFINITY : m * c + log2f(lt);
       write_row<D, BF16>(p, tO, have_o, live, jb.slot, (size_t)max(jb.slot, 0) * kPrefillRows + grp * kTileRows + row,
-                         jb.q0 + qi, jb.h * p.G + row % p.G, ch * (D / 2), have_o ? inv_l : 0.f, lse2);
+                         jb.q0 + qi, jb.head0 + row % p.G, ch * (D / 2), have_o ? inv_l : 0.f, lse2);
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
       if (!ok) break;
     }
   }
