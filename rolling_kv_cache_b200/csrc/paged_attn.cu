@@ -220,7 +220,7 @@ __device__ __forceinline__ int last_at_most(const int* before, int n, int per, i
 
 // The schedule, by all threads; `mem` is scratch of the layout's kLoads + ... bytes.
 template <int D>
-__device__ __noinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem, int* warp_sums, int* most, int* sums,
+__device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem, int* warp_sums, int* most, int* sums,
                                           Plan* plan) {
   using L = PreLayout<D>;
   int* tiles_before = reinterpret_cast<int*>(mem + L::kTilesBefore);
@@ -364,7 +364,7 @@ __device__ __noinline__ void zero_values(uint8_t* v, int t0, int lo_min, int hi_
 // A row's D / 2 columns from `col0` on: O (TMEM columns tO .., if have_o) times inv_l, to
 // the output, or, slot >= 0, to row `at` of the partial rows.
 template <int D, bool BF16>
-__device__ __noinline__ void write_row(const PagedAttnParams& p, uint32_t tO, bool have_o, bool live, int slot,
+__device__ __noinline__ void write_row(const RowOutput& p, uint32_t tO, bool have_o, bool live, int slot,
                                        size_t at, int tok, int head, int col0, float inv_l, float lse2) {
 #pragma unroll 1
   for (int cc = 0; cc < D / 2; cc += 16) {
@@ -407,6 +407,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   // that are there (a bit each), whether every query sees all of it, whether some V
   // rows are seen by none
   __shared__ int4 tile_info[4];
+  __shared__ RowOutput to_sh;  // for code out of line: a reference to the parameters would read them as global memory
   // the units' descriptions, written by the producer (which alone walks the
   // schedule: the walk's state in 18 warps' local memory would not fit L1)
   __shared__ JobInfo jobs[kJobRing];
@@ -439,6 +440,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       ptx::mbar_init(&bar_je[i], kSoftmaxWarps + 1);
     }
     abort_sh = 0;
+    to_sh = row_output(p);
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -820,7 +822,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       const bool none = m == -INFINITY && lt == lt;
       const float inv_l = none ? 0.f : 1.f / lt;
       const float lse2 = none ? -INFINITY : m * c + log2f(lt);
-      write_row<D, BF16>(p, tO, have_o, live, jb.slot, (size_t)max(jb.slot, 0) * kPrefillRows + grp * kTileRows + row,
+      write_row<D, BF16>(to_sh, tO, have_o, live, jb.slot, (size_t)max(jb.slot, 0) * kPrefillRows + grp * kTileRows + row,
                          jb.q0 + qi, jb.head0 + row % p.G, ch * (D / 2), have_o ? inv_l : 0.f, lse2);
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);

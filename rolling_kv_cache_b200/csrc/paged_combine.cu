@@ -124,8 +124,9 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
     h = rr % p.G;
     if (rr >= tpt * p.G || i >= s.n) return;
   }
-  if (p.prev_o) merge_prev<D>(p, s.q0 + i, head0 + h, col, acc, lse2);
-  store_row<D, BF16>(p, s.q0 + i, head0 + h, col, acc, lse2);
+  const RowOutput to = row_output(p);
+  if (to.prev_o) merge_prev<D>(to, s.q0 + i, head0 + h, col, acc, lse2);
+  store_row<D, BF16>(to, s.q0 + i, head0 + h, col, acc, lse2);
 }
 
 template <int D, bool BF16>

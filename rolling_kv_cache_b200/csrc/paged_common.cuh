@@ -100,15 +100,34 @@ __device__ __forceinline__ void block_prefix(int* pre, int n, int* warp_sums, Fn
   __syncthreads();
 }
 
+// Where a row's result goes, and what it is merged with (PagedAttnParams' fields).
+struct RowOutput {
+  uint8_t* out;
+  long long tok_stride, head_stride;  // bytes
+  float* lse;
+  const float* prev_o;
+  const float* prev_lse;
+  float* pre_o;
+  float* pre_lse;
+  float* part_o;
+  float* part_lse;
+  int n_tok, heads;
+};
+
+__device__ __forceinline__ RowOutput row_output(const PagedAttnParams& p) {
+  return RowOutput{p.out.data, p.out.tok_stride, p.out.head_stride, p.lse,    p.prev_o, p.prev_lse,
+                   p.pre_o,    p.pre_lse,        p.part_o,          p.part_lse, p.n_tok,  p.Hk * p.G};
+}
+
 // Merges 8 columns of a row (divided by its sum; lse2 its log2-sum-exp) with
 // the same row's result over the shared prefix.
 template <int D>
-__device__ __forceinline__ void merge_prev(const PagedAttnParams& p, int tok, int head, int col, float (&acc)[8],
+__device__ __forceinline__ void merge_prev(const RowOutput& p, int tok, int head, int col, float (&acc)[8],
                                            float& lse2) {
   const float pl = p.prev_lse[(size_t)head * p.n_tok + tok];
   const float m = fmaxf(lse2, pl);
   if (m == -INFINITY) return;  // neither side saw a key
-  const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.Hk * p.G + head) * D + col);
+  const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.heads + head) * D + col);
   const float4 a = src[0], b = src[1];
   const float w = exp2f(lse2 - m), wp = exp2f(pl - m), inv = 1.f / (w + wp);
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
@@ -119,10 +138,10 @@ __device__ __forceinline__ void merge_prev(const PagedAttnParams& p, int tok, in
 
 // The last write of 8 columns of a row: the output, or the prefix pass's fp32 result.
 template <int D, bool BF16>
-__device__ __forceinline__ void store_row(const PagedAttnParams& p, int tok, int head, int col, const float (&acc)[8],
+__device__ __forceinline__ void store_row(const RowOutput& p, int tok, int head, int col, const float (&acc)[8],
                                           float lse2) {
   if (p.pre_o) {
-    float4* dst = reinterpret_cast<float4*>(p.pre_o + ((size_t)tok * p.Hk * p.G + head) * D + col);
+    float4* dst = reinterpret_cast<float4*>(p.pre_o + ((size_t)tok * p.heads + head) * D + col);
     dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
     if (col == 0) p.pre_lse[(size_t)head * p.n_tok + tok] = lse2;
@@ -133,7 +152,7 @@ __device__ __forceinline__ void store_row(const PagedAttnParams& p, int tok, int
   u.y = ptx::pack16x2<BF16>(acc[2], acc[3]);
   u.z = ptx::pack16x2<BF16>(acc[4], acc[5]);
   u.w = ptx::pack16x2<BF16>(acc[6], acc[7]);
-  *reinterpret_cast<uint4*>(p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + col * 2) = u;
+  *reinterpret_cast<uint4*>(p.out + tok * p.tok_stride + head * p.head_stride + col * 2) = u;
   if (p.lse && col == 0) p.lse[(size_t)head * p.n_tok + tok] = lse2 * 0.69314718055994531f;
 }
 

@@ -409,8 +409,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         if (col == 0) p.part_lse[at] = lse2;
       } else {
         const int i = row / p.G, head = u.h * p.G + row - i * p.G, tok = s.q0 + i;
-        if (p.prev_o) merge_prev<D>(p, tok, head, col, acc, lse2);
-        store_row<D, BF16>(p, tok, head, col, acc, lse2);
+        const RowOutput to = row_output(p);
+        if (to.prev_o) merge_prev<D>(to, tok, head, col, acc, lse2);
+        store_row<D, BF16>(to, tok, head, col, acc, lse2);
       }
     }
   }
