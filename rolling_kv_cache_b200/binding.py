@@ -9,8 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-import struct
-from typing import Optional, Union
+from typing import Optional
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "librc.so")
@@ -106,18 +105,6 @@ class rc_paged_mask(ctypes.Structure):
                 ("prefix_len", ctypes.c_int32), ("prefix_table", ctypes.c_void_p), ("prefix_pages", ctypes.c_int32)]
 
 
-# The same four as packed bytes, fields in order: building a ctypes structure costs microseconds, which a
-# decoding step's call would notice. The functions below take either.
-PACK_ROPE = struct.Struct("@P3P3i3iii")
-PACK_ROWS = struct.Struct("@Pqqi4x")
-PACK_PAGED = struct.Struct("@PP3q3qiiiiiiPPPqi4x")
-PACK_MASK = struct.Struct("@iiiifiPi4x")
-
-
-def _arg(s):
-    return s if s is None or type(s) is bytes else ctypes.byref(s)
-
-
 EXPORTS = ["rc_config_init", "rc_cache_bytes", "rc_cache_create", "rc_step", "rc_step_noalloc",
            "rc_select_topc", "rc_reindex", "rc_comp_tokens", "rc_pool_scores",
            "rc_get_state", "rc_device_status", "rc_rope_table", "rc_cache_layout",
@@ -152,10 +139,11 @@ def lib() -> ctypes.CDLL:
         L.rc_profile_begin.argtypes = [vp, i]
         L.rc_profile_end.argtypes = [vp, ctypes.POINTER(rc_profile)]
         L.rc_cache_destroy.argtypes = [vp]
-        L.rc_rope_axes.argtypes = [vp, i, i, i, i, vp, vp, vp, vp]
-        L.rc_paged_append.argtypes = [vp, vp, i, vp, vp, vp, vp, vp, vp]
-        L.rc_paged_workspace.argtypes = [vp, vp, i, i, vp]
-        L.rc_paged_attention.argtypes = [vp, vp, i, vp, vp, vp, vp, sz, vp, vp]
+        pr, pp, pm, prope = (ctypes.POINTER(t) for t in (rc_rows, rc_paged, rc_paged_mask, rc_rope))
+        L.rc_rope_axes.argtypes = [prope, i, i, i, i, pr, pr, vp, vp]
+        L.rc_paged_append.argtypes = [pp, prope, i, pr, pr, pr, pr, vp, vp]
+        L.rc_paged_workspace.argtypes = [pp, pm, i, i, ctypes.POINTER(sz)]
+        L.rc_paged_attention.argtypes = [pp, pm, i, pr, pr, vp, vp, sz, vp, vp]
         L.rc_last_error.argtypes = []
         L.rc_last_error.restype = ctypes.c_char_p
         for name in EXPORTS[:-1]:
@@ -269,30 +257,24 @@ def rc_profile_end(handle) -> dict:
                     bytes=p.bytes[i]) for i, n in enumerate(RC_KERNEL_NAMES)}
 
 
-def rc_rope_axes(rope: Union[rc_rope, bytes], dtype, n_tok, head_dim, inverse, x, y, status=0, stream=0) -> None:
-    """x, y: (rc_rows * 2) arrays, or their packed bytes."""
-    r = lib().rc_rope_axes(_arg(rope), dtype, n_tok, head_dim, inverse, _arg(x), _arg(y), status, stream)
-    if r:
-        check(r)
+def rc_rope_axes(rope, dtype, n_tok, head_dim, inverse, x, y, status=0, stream=0) -> None:
+    """x, y: (rc_rows * 2) arrays."""
+    check(lib().rc_rope_axes(rope, dtype, n_tok, head_dim, inverse, x, y, status or None, stream or None))
 
 
 def rc_paged_append(paged, rope, n_tok, q, k, v, q_out, status=0, stream=0) -> None:
-    r = lib().rc_paged_append(_arg(paged), _arg(rope), n_tok, _arg(q), _arg(k), _arg(v), _arg(q_out), status, stream)
-    if r:
-        check(r)
+    check(lib().rc_paged_append(paged, rope, n_tok, q, k, v, q_out, status or None, stream or None))
 
 
 def rc_paged_workspace(paged, mask, n_tok, q_heads) -> int:
     n = ctypes.c_size_t()
-    check(lib().rc_paged_workspace(_arg(paged), _arg(mask), n_tok, q_heads, ctypes.byref(n)))
+    check(lib().rc_paged_workspace(paged, mask, n_tok, q_heads, ctypes.byref(n)))
     return n.value
 
 
 def rc_paged_attention(paged, mask, n_tok, q, out, lse, workspace, nbytes, status=0, stream=0) -> None:
-    r = lib().rc_paged_attention(_arg(paged), _arg(mask), n_tok, _arg(q), _arg(out), lse, workspace, nbytes, status,
-                                 stream)
-    if r:
-        check(r)
+    check(lib().rc_paged_attention(paged, mask, n_tok, q, out, lse or None, workspace or None, nbytes,
+                                   status or None, stream or None))
 
 
 def rc_cache_destroy(handle) -> None:
