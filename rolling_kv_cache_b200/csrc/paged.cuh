@@ -85,13 +85,19 @@ struct alignas(64) PagedAttnParams {
   float* part_o;       // [2 * n_ctas][rows][d] fp32: parts of units cut between CTAs, each divided by its sum
   float* part_lse;     // [2 * n_ctas][rows], log2-sum-exp of each part
   int4* rec;           // [n_ctas] what of its range a CTA left in parts (PartRecord)
-  // result over the shared prefix to merge at the last write: fp32 [n_tok][q_heads][d] and [q_heads][n_tok] log2
-  const float* prev_o;
-  const float* prev_lse;
-  // or, when this call is the pass over a prefix: where that result goes (then out and lse are unused)
+  // A prefix that the whole batch sees. Prefill: lead_len > 0 tokens in the pages of lead_table, which
+  // every unit walks first.
+  const int32_t* lead_table;
+  int lead_len;
+  // Or in a pass of its own (batch_pass): one sequence of every query of the batch against keys [0, prefix_len) of
+  // table row 0.
+  int batch_pass, prefix_len;
+  // null, or where the result goes instead of out and lse: fp32 [n_tok][q_heads][d], log2 [q_heads][n_tok]
   float* pre_o;
   float* pre_lse;
-  int prefix_len;      // prefix pass: every query of the batch sees keys [0, prefix_len) of table row 0
+  // null, or such a result that the last write merges with (decode, its combine, and the merge kernel)
+  const float* prev_o;
+  const float* prev_lse;
   int n_tok, Hk, G;
   int box_rows;        // rows of a page per TMA box
   float scale_log2;    // log2(e) * scale
@@ -104,6 +110,8 @@ constexpr int kPrefillRows = 256;
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
+// out = the merge of two results in fp32 (prev_o, prev_lse; pre_o, pre_lse), for the rows of sequences.
+cudaError_t launch_paged_merge(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 cudaError_t launch_paged_combine(const PagedAttnParams& p, bool bf16, int head_dim, bool decode, cudaStream_t s);
 
 cudaError_t launch_rope_axes(const RopeAxesParams& p, int dtype, int head_dim, bool halves, cudaStream_t s);

@@ -162,9 +162,13 @@ cudaError_t sm_count(int* n) {
 
 // Where the parts of an attention call lie in its workspace.
 struct Work {
-  bool decode, prefix;
+  bool decode;    // the kernel for few rows
+  bool lead;      // a prefix is walked by every unit first
+  bool two_pass;  // a prefix has a pass of its own
   int n_ctas, group;
-  size_t part_o, part_lse, rec, pre_o, pre_lse, total;
+  size_t part_o, part_lse, rec, total;
+  size_t x_part_o, x_part_lse, x_rec, pre_o, pre_lse;  // two passes: the prefix's parts and its result
+  size_t own_o, own_lse;                                // and the prefill pass's over the sequences' own tokens
 };
 
 rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_heads, Work* w) {
@@ -184,27 +188,44 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
       (!m->prefix_table || (int64_t)m->prefix_pages * p->page_size < m->prefix_len || m->prefix_len > (1 << 30)))
     return invalid("prefix_table must list the pages of prefix_len tokens");
   w->decode = (int64_t)std::max(1, m->max_q) * w->group <= rc::kDecodeRows;
-  w->prefix = m->prefix_len > 0;
+  // A prefix and many rows: where the sequences fill their query tiles on their
+  // own, each walks the prefix's tiles itself (the same products, the tiles from
+  // L2, no second pass and no merge); where they do not, the whole batch's rows
+  // are packed into tiles for a pass over the prefix.
+  const int per_pair = 2 * (128 / w->group);
+  w->lead = m->prefix_len > 0 && !w->decode && (int64_t)n_tok >= (int64_t)per_pair * p->n_seqs;
+  w->two_pass = m->prefix_len > 0 && !w->lead;
   // positions of the stream-K split are 32-bit: tiles of every unit, summed
-  const int64_t tiles = (int64_t)std::max(p->max_pages, m->prefix_pages) * p->page_size / 64 + 1;
-  const int64_t pairs = (int64_t)n_tok / std::max(1, 2 * (128 / w->group)) + p->n_seqs + 1;
+  const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 2;
+  const int64_t pairs = (int64_t)n_tok / per_pair + p->n_seqs + 1;
   if ((w->decode ? tiles * p->n_seqs : tiles * pairs) * p->kv_heads >= INT_MAX)
     return SetLastError(RC_ERANGE, "the batch has too many key tiles for one call");
   int sms = 0;
   if (cudaError_t e = sm_count(&sms)) return cuda_failed(e, "device attribute");
   w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
-  const size_t rows = (size_t)2 * w->n_ctas * (w->decode && !w->prefix ? rc::kDecodeRows : rc::kPrefillRows);
   size_t o = 0;
-  w->part_o = o;
-  o += align_up(rows * p->head_dim * 4);
-  w->part_lse = o;
-  o += align_up(rows * 4);
-  w->rec = o;
-  o += align_up((size_t)w->n_ctas * sizeof(int4));
-  w->pre_o = o;
-  if (w->prefix) o += align_up((size_t)n_tok * q_heads * p->head_dim * 4);
-  w->pre_lse = o;
-  if (w->prefix) o += align_up((size_t)n_tok * q_heads * 4);
+  auto take = [&](size_t bytes) {
+    const size_t at = o;
+    o += align_up(bytes);
+    return at;
+  };
+  auto parts = [&](int unit_rows, size_t* po, size_t* pl, size_t* rec) {
+    const size_t rows = (size_t)2 * w->n_ctas * unit_rows;
+    *po = take(rows * p->head_dim * 4);
+    *pl = take(rows * 4);
+    *rec = take((size_t)w->n_ctas * sizeof(int4));
+  };
+  parts(w->decode ? rc::kDecodeRows : rc::kPrefillRows, &w->part_o, &w->part_lse, &w->rec);
+  if (w->two_pass) {
+    // its own regions: the kernels of the call overlap at their ends
+    parts(rc::kPrefillRows, &w->x_part_o, &w->x_part_lse, &w->x_rec);
+    w->pre_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
+    w->pre_lse = take((size_t)n_tok * q_heads * 4);
+    if (!w->decode) {
+      w->own_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
+      w->own_lse = take((size_t)n_tok * q_heads * 4);
+    }
+  }
   w->total = o;
   return RC_OK;
 }
@@ -337,27 +358,44 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       if (cudaError_t e = rc::launch_paged_combine(x, bf16, d, false, s)) return cuda_failed(e, "combine launch");
       return RC_OK;
     };
-    if (w.prefix || !w.decode) {
+    if (w.two_pass || !w.decode) {
       const int64_t dims[3] = {d, q->heads, n_tok};
       const int64_t st3[2] = {q->head_stride, q->tok_stride};
       const int box[3] = {64, w.group, 128 / w.group};
       if (rc_status st = encode(&p.tm_q, q->data, pg->dtype, 3, dims, st3, box)) return st;
       if (rc_status st = maps(false, pg->page_size)) return st;
     }
-    if (w.prefix) {
+    if (w.lead) {
+      p.lead_table = m->prefix_table;
+      p.lead_len = m->prefix_len;
+    }
+    if (!w.two_pass && !w.decode) return prefill(p);
+    if (w.two_pass) {
       rc::PagedAttnParams x = p;  // every query of the batch against the prefix's pages
       x.b.page_table = m->prefix_table;
       x.b.max_pages = m->prefix_pages;
       x.b.table_stride = 0;
+      x.batch_pass = 1;
       x.prefix_len = m->prefix_len;
       x.mask = rc::MaskView{1 << 30, 0, 0};
+      x.part_o = reinterpret_cast<float*>(ws + w.x_part_o);
+      x.part_lse = reinterpret_cast<float*>(ws + w.x_part_lse);
+      x.rec = reinterpret_cast<int4*>(ws + w.x_rec);
       x.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
       x.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
       if (rc_status st = prefill(x)) return st;
+      if (!w.decode) {
+        p.pre_o = reinterpret_cast<float*>(ws + w.own_o);
+        p.pre_lse = reinterpret_cast<float*>(ws + w.own_lse);
+        if (rc_status st = prefill(p)) return st;
+      }
       p.prev_o = x.pre_o;
       p.prev_lse = x.pre_lse;
+      if (!w.decode) {
+        if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
+        return RC_OK;
+      }
     }
-    if (!w.decode) return prefill(p);
     if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
     if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, s)) return cuda_failed(e, "paged attention launch");
     if (cudaError_t e = rc::launch_paged_combine(p, bf16, d, true, s)) return cuda_failed(e, "combine launch");

@@ -54,6 +54,7 @@ constexpr int kMmaWarp = 17;
 constexpr int kPreThreads = 18 * 32;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxRounds = 64;
+constexpr int kPlanSeqs = 512;
 
 template <int D>
 struct PreLayout {
@@ -64,11 +65,12 @@ struct PreLayout {
   static constexpr uint32_t kV = 4 * kTile;      // 2 stages
   static constexpr uint32_t kBytes = 6 * kTile;
   static constexpr uint32_t kDynSmem = kBytes + 1024;
-  // the schedule's sums, gone before the first load: tiles and pairs of the
-  // sequences, and each CTA's tiles after each round
-  static constexpr uint32_t kTilesBefore = 0;
-  static constexpr uint32_t kPairsBefore = kTilesBefore + (kMaxSeqs + 1) * 4;
-  static constexpr uint32_t kLoads = kPairsBefore + (kMaxSeqs + 1) * 4;
+  // the schedule's sums, gone before the first load: tiles (low half) and pairs
+  // (high half) of the sequences before each, the first sequences themselves,
+  // and each CTA's tiles after each round
+  static constexpr uint32_t kBefore = 0;
+  static constexpr uint32_t kSeqs = kBefore + ((kMaxSeqs + 1) * 8 + 15) / 16 * 16;
+  static constexpr uint32_t kLoads = kSeqs + kPlanSeqs * 16;
   static_assert(kLoads + kMaxRounds * kMaxPersistentCtas * 4 <= kBytes, "the schedule fits the tiles' memory");
 };
 
@@ -81,14 +83,15 @@ struct Job {
   int L, kv_lo, kv_hi, slot;
   bool has1, head, tail;  // head: begins inside the unit; tail: ends inside it
   int place;              // h * pairs + pair
+  int lead, total;        // tiles of the prefix that it walks first, and in all
   TileSpan<kTileRows> sp;
 };
 
-// The batch as the kernel sees it: the sequences, or, in the pass over a
-// shared prefix, one sequence of every query that sees the prefix whole (the
-// host sets a frame beyond every position and no window).
+// The batch as the kernel sees it: the sequences, or, in a pass over a shared
+// prefix alone, one sequence of every query that sees the prefix whole (the host
+// sets a frame beyond every position and no window).
 __device__ __forceinline__ Seq pre_seq(const PagedAttnParams& p, int b) {
-  if (p.pre_o) {
+  if (p.batch_pass) {
     Seq s;
     const int n = __ldg(p.b.cu_q + p.b.n_seqs);
     s.q0 = 0;
@@ -103,8 +106,10 @@ __device__ __forceinline__ Seq pre_seq(const PagedAttnParams& p, int b) {
 __device__ __forceinline__ void pair_span(const PagedAttnParams& p, const Seq& s, int pair, int tpt, Job& j) {
   const int i0 = pair * 2 * tpt;
   j.tokens = min(2 * tpt, s.n - i0);
-  j.at0 = (p.pre_o ? 0 : s.L - s.n) + i0;
+  j.at0 = (p.batch_pass ? 0 : s.L - s.n) + i0;
   j.sp.init(p.mask, j.at0, j.at0 + j.tokens - 1, s.L);
+  j.lead = (p.lead_len + kTileRows - 1) / kTileRows;
+  j.total = j.lead + j.sp.n;
 }
 
 // A unit as the softmax and MMA warps need it.
@@ -115,6 +120,7 @@ struct JobInfo {
   int at0, L, slot, lo_min, hi_max;
 };
 constexpr int kJobRing = 4;
+constexpr int kLeadTile = 1 << 16;  // in a tile's page bits: it is the prefix's
 
 // A unit, and a tile within it.
 struct Start {
@@ -148,7 +154,7 @@ struct PairWalk {
   }
   __device__ __forceinline__ void init(const PagedAttnParams& prm, const Plan& pl) {
     p = &prm;
-    n_seqs = prm.pre_o ? 1 : prm.b.n_seqs;
+    n_seqs = prm.batch_pass ? 1 : prm.b.n_seqs;
     tpt = kTileRows / prm.G;
     pos = pl.pos;
     end = pl.end;
@@ -160,7 +166,7 @@ struct PairWalk {
   __device__ __forceinline__ bool next(Job& j) {
     if (rounds > 0) {
       pair_span(*p, s, pair, tpt, j);
-      fill(j, 0, max(j.sp.n, 1));
+      fill(j, 0, max(j.total, 1));
       if (--rounds > 0) {
         int i = h * pairs + pair + (int)gridDim.x;
         while (i >= p->Hk * pairs) {
@@ -185,7 +191,7 @@ struct PairWalk {
       }
     }
     pair_span(*p, s, pair, tpt, j);
-    const int len = min(max(j.sp.n, 1) - off, end - pos);
+    const int len = min(max(j.total, 1) - off, end - pos);
     fill(j, off, len);
     pos += len;
     off = 0;
@@ -198,37 +204,46 @@ struct PairWalk {
     j.q0 = s.q0 + pair * 2 * tpt;
     j.L = s.L;
     j.kv_lo = lo;
-    j.kv_hi = min(lo + len, j.sp.n);
+    j.kv_hi = min(lo + len, j.total);
     j.has1 = j.tokens > tpt;
     j.head = lo > 0;
-    j.tail = lo + len < max(j.sp.n, 1);
+    j.tail = lo + len < max(j.total, 1);
     j.slot = j.head ? 2 * (int)blockIdx.x : (j.tail ? 2 * (int)blockIdx.x + 1 : -1);
     j.place = h * pairs + pair;
   }
 };
 
-// The largest b < n with per * before[b] <= x.
-__device__ __forceinline__ int last_at_most(const int* before, int n, int per, int x) {
+__device__ __forceinline__ int tiles_of(unsigned long long x) { return (int)(uint32_t)x; }
+__device__ __forceinline__ int pairs_of(unsigned long long x) { return (int)(x >> 32); }
+
+// The largest b < n with per * of(before[b]) <= x.
+template <typename Fn>
+__device__ __forceinline__ int last_at_most(const unsigned long long* before, int n, int per, int x, Fn of) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (per * before[mid] <= x) lo = mid;
+    if (per * of(before[mid]) <= x) lo = mid;
     else hi = mid - 1;
   }
   return lo;
 }
 
-// The schedule, by all threads; `mem` is scratch of the layout's kLoads + ... bytes.
+// The schedule, by all threads; `mem` is scratch as the layout lays it out.
 template <int D>
-__device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem, int* warp_sums, int* most, int* sums,
-                                          Plan* plan) {
+__device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem, unsigned long long* warp_sums,
+                                          int* most, int* sums, Plan* plan) {
   using L = PreLayout<D>;
-  int* tiles_before = reinterpret_cast<int*>(mem + L::kTilesBefore);
-  int* pairs_before = reinterpret_cast<int*>(mem + L::kPairsBefore);
+  unsigned long long* before = reinterpret_cast<unsigned long long*>(mem + L::kBefore);
+  int4* seqs = reinterpret_cast<int4*>(mem + L::kSeqs);
   int* loads = reinterpret_cast<int*>(mem + L::kLoads);  // [round][CTA]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int n_seqs = p.pre_o ? 1 : p.b.n_seqs, tpt = kTileRows / p.G;
+  const int n_seqs = p.batch_pass ? 1 : p.b.n_seqs, tpt = kTileRows / p.G;
   const int G = gridDim.x, c = blockIdx.x;
+  auto seq = [&](int b) {
+    if (b >= kPlanSeqs) return pre_seq(p, b);
+    const int4 x = seqs[b];
+    return Seq{x.x, x.y, x.z, false};
+  };
   // tiles and pairs of each sequence (one key head), a warp a sequence
   for (int b = warp; b < n_seqs; b += kPreThreads / 32) {
     const Seq s = pre_seq(p, b);
@@ -237,70 +252,72 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
     for (int q = lane; q < pairs; q += 32) {
       Job j;
       pair_span(p, s, q, tpt, j);
-      sum += max(j.sp.n, 1);
+      sum += max(j.total, 1);
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
-      tiles_before[b] = sum;
-      pairs_before[b] = pairs;
+      before[b] = (unsigned long long)pairs << 32 | (uint32_t)sum;
+      if (b < kPlanSeqs) seqs[b] = make_int4(s.q0, s.n, s.L, 0);
     }
   }
   if (tid < kMaxRounds) most[tid] = 0;
   if (tid < 2) sums[tid] = 0;
   __syncthreads();
-  block_prefix<kPreThreads>(tiles_before, n_seqs, warp_sums, [&](int b) { return tiles_before[b]; });
-  block_prefix<kPreThreads>(pairs_before, n_seqs, warp_sums, [&](int b) { return pairs_before[b]; });
-  const int W = p.Hk * tiles_before[n_seqs], U = p.Hk * pairs_before[n_seqs];
+  block_prefix<kPreThreads>(before, n_seqs, warp_sums, [&](int b) { return before[b]; });
+  const int W = p.Hk * tiles_of(before[n_seqs]), U = p.Hk * pairs_of(before[n_seqs]);
   const int r_max = min(U / G, kMaxRounds);
-  // each CTA's tiles after each round, and the most any has
-  if (tid < G) {
-    int load = 0, b = 0;
-    Seq s;
-    for (int r = 0; r < r_max; ++r) {
-      const int u = tid + r * G;
-      if (r == 0) b = last_at_most(pairs_before, n_seqs, p.Hk, u);
-      while (p.Hk * pairs_before[b + 1] <= u) ++b;
-      s = pre_seq(p, b);
+  int rounds = 0, own = 0;
+  if (r_max > 0) {
+    // each CTA's tiles after each round, and the most any has
+    for (int u = tid; u < r_max * G; u += kPreThreads) {
+      const int b = last_at_most(before, n_seqs, p.Hk, u, pairs_of);
+      const int first = pairs_of(before[b]);
       Job j;
-      pair_span(p, s, (u - p.Hk * pairs_before[b]) % (pairs_before[b + 1] - pairs_before[b]), tpt, j);
-      load += max(j.sp.n, 1);
-      loads[r * G + tid] = load;
-      atomicMax(&most[r], load);
+      pair_span(p, seq(b), (u - p.Hk * first) % (pairs_of(before[b + 1]) - first), tpt, j);
+      loads[u] = max(j.total, 1);
     }
+    __syncthreads();
+    if (tid < G) {
+      int load = 0;
+      for (int r = 0; r < r_max; ++r) {
+        load += loads[r * G + tid];
+        loads[r * G + tid] = load;
+        atomicMax(&most[r], load);
+      }
+    }
+    __syncthreads();
+    while (rounds < r_max && most[rounds] <= W / G) ++rounds;
+    // range of this CTA: what brings it, and those before it, to the average
+    if (rounds > 0 && tid < G) {
+      const int load = loads[(rounds - 1) * G + tid];
+      atomicAdd(&sums[0], load);
+      if (tid < c) atomicAdd(&sums[1], load);
+    }
+    __syncthreads();
+    if (rounds > 0) own = loads[(rounds - 1) * G + c];
   }
-  __syncthreads();
-  int rounds = 0;
-  while (rounds < r_max && most[rounds] <= W / G) ++rounds;
-  // range of this CTA: what brings it, and those before it, to the average
-  if (rounds > 0 && tid < G) {
-    const int load = loads[(rounds - 1) * G + tid];
-    atomicAdd(&sums[0], load);
-    if (tid < c) atomicAdd(&sums[1], load);
-  }
-  __syncthreads();
-  const int own = rounds > 0 ? loads[(rounds - 1) * G + c] : 0;
-  const int pos = (int)((long long)W * c / G) - sums[1] + sums[0];
-  const int end = (int)((long long)W * (c + 1) / G) - sums[1] - own + sums[0];
   if (warp == 0) {
+    const int pos = (int)((long long)W * c / G) - sums[1] + sums[0];
+    const int end = (int)((long long)W * (c + 1) / G) - sums[1] - own + sums[0];
     if (rounds > 0 && lane == 0) {
-      const int b = last_at_most(pairs_before, n_seqs, p.Hk, c);
-      const int pairs = pairs_before[b + 1] - pairs_before[b], i = c - p.Hk * pairs_before[b];
+      const int b = last_at_most(before, n_seqs, p.Hk, c, pairs_of);
+      const int first = pairs_of(before[b]), pairs = pairs_of(before[b + 1]) - first, i = c - p.Hk * first;
       plan->whole = Start{b, i / pairs, i % pairs, 0};
     }
     if (pos < end) {
-      const int b = last_at_most(tiles_before, n_seqs, p.Hk, pos);
-      const int w = tiles_before[b + 1] - tiles_before[b];
-      const int rem = pos - p.Hk * tiles_before[b], h = rem / w;
+      const int b = last_at_most(before, n_seqs, p.Hk, pos, tiles_of);
+      const int w = tiles_of(before[b + 1]) - tiles_of(before[b]);
+      const int rem = pos - p.Hk * tiles_of(before[b]), h = rem / w;
       int left = rem - h * w;
-      const Seq s = pre_seq(p, b);
-      const int pairs = pairs_before[b + 1] - pairs_before[b];
+      const Seq s = seq(b);
+      const int pairs = pairs_of(before[b + 1]) - pairs_of(before[b]);
       for (int q0 = 0; q0 < pairs; q0 += 32) {
         int t = 0;
         if (q0 + lane < pairs) {
           Job j;
           pair_span(p, s, q0 + lane, tpt, j);
-          t = max(j.sp.n, 1);
+          t = max(j.total, 1);
         }
         int inc = t;
 #pragma unroll
@@ -322,8 +339,8 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
   }
 }
 
-// What runs once in many tiles stays out of line, so that its registers are
-// not the tile loop's: the masking of a boundary tile, and a unit's last writes.
+// The masking of a boundary tile stays out of line, so that its registers are
+// not the tile loop's.
 
 // -inf over the scores of one row's 64 keys from h0 on (TMEM columns tS ..)
 // that the row does not see or whose page is none.
@@ -336,6 +353,7 @@ __device__ __noinline__ void mask_scores(uint32_t tS, int h0, RowMask rm, int si
 #pragma unroll 1
   for (int cc = 0; cc < 2; ++cc) {
     const uint32_t vis = (uint32_t)(v >> (32 * cc));
+    if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
     uint32_t r[32];
     ptx::tmem_ld32(tS + cc * 32, r);
     ptx::tmem_ld_wait();
@@ -361,41 +379,6 @@ __device__ __noinline__ void zero_values(uint8_t* v, int t0, int lo_min, int hi_
   ptx::fence_proxy_async_smem();
 }
 
-// A row's D / 2 columns from `col0` on: O (TMEM columns tO .., if have_o) times inv_l, to
-// the output, or, slot >= 0, to row `at` of the partial rows.
-template <int D, bool BF16>
-__device__ __noinline__ void write_row(const RowOutput& p, uint32_t tO, bool have_o, bool live, int slot,
-                                       size_t at, int tok, int head, int col0, float inv_l, float lse2) {
-#pragma unroll 1
-  for (int cc = 0; cc < D / 2; cc += 16) {
-    uint32_t o[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = 0u;
-    if (have_o) {
-      ptx::tmem_ld16(tO + cc, o);
-      ptx::tmem_ld_wait();
-    }
-    if (!live) continue;
-#pragma unroll
-    for (int v = 0; v < 2; ++v) {
-      float acc[8];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) acc[k] = inv_l == 0.f ? 0.f : __uint_as_float(o[8 * v + k]) * inv_l;
-      const int col = col0 + cc + 8 * v;
-      if (slot < 0) {
-        float lse = lse2;
-        if (p.prev_o) merge_prev<D>(p, tok, head, col, acc, lse);
-        store_row<D, BF16>(p, tok, head, col, acc, lse);
-      } else {
-        float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
-        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (col == 0) p.part_lse[at] = lse2;
-      }
-    }
-  }
-}
-
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __grid_constant__ PagedAttnParams p) {
   using L = PreLayout<D>;
@@ -407,12 +390,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   // that are there (a bit each), whether every query sees all of it, whether some V
   // rows are seen by none
   __shared__ int4 tile_info[4];
-  __shared__ RowOutput to_sh;  // for code out of line: a reference to the parameters would read them as global memory
   // the units' descriptions, written by the producer (which alone walks the
   // schedule: the walk's state in 18 warps' local memory would not fit L1)
   __shared__ JobInfo jobs[kJobRing];
   __shared__ uint64_t bar_jf[kJobRing], bar_je[kJobRing];
-  __shared__ int warp_sums[18], most[kMaxRounds], sums[2];
+  __shared__ unsigned long long warp_sums[18];
+  __shared__ int most[kMaxRounds], sums[2];
   __shared__ Plan plan;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;
@@ -440,7 +423,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       ptx::mbar_init(&bar_je[i], kSoftmaxWarps + 1);
     }
     abort_sh = 0;
-    to_sh = row_output(p);
     ptx::fence_mbar_init();
   }
   if (warp == kMmaWarp) {
@@ -515,10 +497,17 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         publish(max(0, n - j));
         if (!ok) return false;
       }
-      const int k0 = jb.sp.key(j) + (box << p.b.page_log2);
-      want = k0 < jb.sp.hi_max &&
-             (k0 + (1 << p.b.page_log2) > jb.sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
-      page = want ? __ldg(p.b.page_table + jb.b * p.b.table_stride + (k0 >> p.b.page_log2)) : -1;
+      const int in_tile = box << p.b.page_log2;
+      if (j < jb.lead) {
+        const int k0 = j * kTileRows + in_tile;
+        want = k0 < p.lead_len;
+        page = want ? __ldg(p.lead_table + (k0 >> p.b.page_log2)) : -1;
+      } else {
+        const int k0 = jb.sp.key(j - jb.lead) + in_tile;
+        want = k0 < jb.sp.hi_max &&
+               (k0 + (1 << p.b.page_log2) > jb.sp.lo_min || (p.mask.window > 0 && k0 < p.mask.sink_tok));
+        page = want ? __ldg(p.b.page_table + jb.b * p.b.table_stride + (k0 >> p.b.page_log2)) : -1;
+      }
       return true;
     };
     for (bool more = advance(); more; ++g) {
@@ -526,14 +515,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       const uint32_t free_par = ((g >> 1) - 1) & 1;
       const bool good = page >= 0 && page < p.b.n_pages;
       if (want && !good && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-      const uint32_t pages = __ballot_sync(0xffffffffu, good);
+      const uint32_t pages = __ballot_sync(0xffffffffu, good) & 0xffu;
       const int pg = good ? page : p.b.n_pages;  // a page that is none: read out of bounds on purpose, zeros
-      const int h = jb.h, t0 = jb.sp.key(j), t1 = t0 + kTileRows;
-      const bool in_sink = p.mask.window > 0 && t1 <= p.mask.sink_tok;
-      const int4 info =
-          make_int4(t0, (int)pages,
-                    t1 <= jb.sp.hi_min && (t0 >= jb.sp.lo_max || in_sink) && __all_sync(0xffffffffu, good),
-                    !(t1 <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || in_sink)));
+      const int h = jb.h;
+      const bool all = __all_sync(0xffffffffu, good);
+      int4 info;
+      if (j < jb.lead) {
+        const int t0 = j * kTileRows, hidden = t0 + kTileRows > p.lead_len;
+        info = make_int4(t0, (int)pages | kLeadTile, !hidden && all, hidden);
+      } else {
+        const int t0 = jb.sp.key(j - jb.lead), t1 = t0 + kTileRows;
+        const bool in_sink = p.mask.window > 0 && t1 <= p.mask.sink_tok;
+        info = make_int4(t0, (int)pages, t1 <= jb.sp.hi_min && (t0 >= jb.sp.lo_max || in_sink) && all,
+                         !(t1 <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || in_sink)));
+      }
       if (fresh) {
         ok = nq == 0 || ptx::mbar_wait(&bar_qe, (nq - 1) & 1, abort, p.status, RC_ETIMEOUT);
         ok = __all_sync(0xffffffffu, ok);
@@ -682,8 +677,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     uint64_t* pbar = &bar_pair[grp * 4 + wq];
     const float c = p.scale_log2;
     const float thresh = kRescaleLog2 / c;
-    const int qi = grp * tpt + row / p.G;         // this row's query within the pair
-    const bool row_in = row < tpt * p.G;
     int gs = 0;  // this group's tiles so far (phase of bar_s / bar_p)
     int gt = 0;  // the CTA's tiles so far (stage of K and V)
     int nj = 0;  // this group's jobs so far (phase of bar_o: one commit per job)
@@ -710,7 +703,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
         continue;
       }
-      const bool live = row_in && qi < jb.tokens;
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
       bool ok = true;
       for (int left = n_tiles; left > 0; --left) {
@@ -722,16 +714,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
           // query take the widest mask
           RowMask rm{jb.lo_min, jb.hi_max};
-          if (live) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
-          mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 ? p.mask.sink_tok : 0,
+          const int qi = grp * tpt + row / p.G;  // this row's query within the pair
+          const bool lead = info.y & kLeadTile;
+          if (lead) rm = RowMask{0, p.lead_len};
+          else if (row < tpt * p.G && qi < jb.tokens) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
+          mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 && !lead ? p.mask.sink_tok : 0,
                       (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
-        }
-        // V rows that no query of the pair sees: zero, before group 0's P lets the product start
-        if (grp == 0 && info.w) {
-          const int st = gt & 1;
-          if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
-          zero_values<D>(base + L::kV + st * L::kTile, info.x, jb.lo_min, jb.hi_max,
-                         p.mask.window > 0 ? p.mask.sink_tok : 0);
         }
         // S in halves, read again for the exponentials: 32 scores at a time leave
         // the loop's state in registers
@@ -802,14 +790,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         emit(ra, 32);
         ptx::tmem_st_wait();
         l += sum;
+        // V rows that no query of the pair sees: zero, before group 0's P lets the product start
+        if (grp == 0 && tile_info[gt & 3].w) {
+          const int st = gt & 1;
+          if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          const int4 info = tile_info[gt & 3];
+          const bool lead = info.y & kLeadTile;
+          zero_values<D>(base + L::kV + st * L::kTile, info.x, lead ? 0 : jb.lo_min, lead ? p.lead_len : jb.hi_max,
+                         p.mask.window > 0 && !lead ? p.mask.sink_tok : 0);
+        }
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar_p[grp]);
         ++gs;
         ++gt;
       }
-      // epilogue: O / l, merged with the prefix's result where there is one, to
-      // the output, or to this CTA's partial slot (fp32, log2-sum-exp); each
-      // warp writes its D/2 columns
+      // epilogue: O / l to the output (or, fp32 with its log2-sum-exp, to the prefix
+      // pass's result or to this CTA's partial slot); each warp writes its D/2 columns
       float l_other = 0.f;
       if (ok && !swap(l, l_other)) ok = false;
       const float lt = l + l_other;
@@ -822,8 +818,47 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       const bool none = m == -INFINITY && lt == lt;
       const float inv_l = none ? 0.f : 1.f / lt;
       const float lse2 = none ? -INFINITY : m * c + log2f(lt);
-      write_row<D, BF16>(to_sh, tO, have_o, live, jb.slot, (size_t)max(jb.slot, 0) * kPrefillRows + grp * kTileRows + row,
-                         jb.q0 + qi, jb.head0 + row % p.G, ch * (D / 2), have_o ? inv_l : 0.f, lse2);
+      const int qi = grp * tpt + row / p.G, tok = jb.q0 + qi, head = jb.head0 + row % p.G;
+      const bool live = row < tpt * p.G && qi < jb.tokens;
+      const float a = have_o ? inv_l : 0.f;
+      uint8_t* dst;  // this warp's half of the row
+      float* dst_lse;
+      const bool f32 = jb.slot >= 0 || p.pre_o;
+      if (jb.slot >= 0) {
+        const size_t at = (size_t)jb.slot * kPrefillRows + grp * kTileRows + row;
+        dst = reinterpret_cast<uint8_t*>(p.part_o + at * D) + ch * (D * 2);
+        dst_lse = p.part_lse + at;
+      } else if (p.pre_o) {
+        dst = reinterpret_cast<uint8_t*>(p.pre_o + ((size_t)tok * p.Hk * p.G + head) * D) + ch * (D * 2);
+        dst_lse = p.pre_lse + (size_t)head * p.n_tok + tok;
+      } else {
+        dst = p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + ch * D;
+        dst_lse = p.lse ? p.lse + (size_t)head * p.n_tok + tok : nullptr;
+      }
+      if (live && ch == 0 && dst_lse) *dst_lse = f32 ? lse2 : lse2 * 0.69314718055994531f;
+#pragma unroll 4
+      for (int cc = 0; cc < D / 2; cc += 16) {
+        uint32_t o[16];
+        if (have_o) {
+          ptx::tmem_ld16(tO + cc, o);
+          ptx::tmem_ld_wait();
+        }
+        if (!live) continue;
+#pragma unroll
+        for (int k = 0; k < 16; ++k) o[k] = a != 0.f ? __float_as_uint(__uint_as_float(o[k]) * a) : 0u;
+        if (f32) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            *reinterpret_cast<uint4*>(dst + cc * 4 + 16 * k) =
+                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        } else {
+          auto pair = [&](int e) { return ptx::pack16x2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1])); };
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            *reinterpret_cast<uint4*>(dst + cc * 2 + 16 * k) =
+                make_uint4(pair(8 * k), pair(8 * k + 2), pair(8 * k + 4), pair(8 * k + 6));
+        }
+      }
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
       if (!ok) break;
@@ -847,8 +882,8 @@ cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
                                 (int)PreLayout<D>::kDynSmem);
   });
   if (e != cudaSuccess) return e;
-  paged_prefill_kernel<D, BF16><<<p.n_ctas, kPreThreads, PreLayout<D>::kDynSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_chained(paged_prefill_kernel<D, BF16>, p, dim3(p.n_ctas), kPreThreads, PreLayout<D>::kDynSmem,
+                        false, s);
 }
 
 }  // namespace

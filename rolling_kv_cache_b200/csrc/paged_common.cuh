@@ -73,31 +73,50 @@ using PartRecord = int4;
 
 // Exclusive prefix sums of f(0..n-1) into pre[0..n] (shared memory), by all
 // threads of the block.
-template <int THREADS, typename Fn>
-__device__ __forceinline__ void block_prefix(int* pre, int n, int* warp_sums, Fn f) {
+template <int THREADS, typename T, typename Fn>
+__device__ __forceinline__ void block_prefix(T* pre, int n, T* warp_sums, Fn f) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (n + THREADS - 1) / THREADS;
   const int i0 = min(tid * per, n), i1 = min(i0 + per, n);
-  int sum = 0;
+  T sum = 0;
   for (int i = i0; i < i1; ++i) {
-    const int w = f(i);
+    const T w = f(i);
     pre[i] = sum;
     sum += w;
   }
-  int inc = sum;
+  T inc = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int t = __shfl_up_sync(0xffffffffu, inc, o);
+    const T t = __shfl_up_sync(0xffffffffu, inc, o);
     if (lane >= o) inc += t;
   }
   if (lane == 31) warp_sums[warp] = inc;
   __syncthreads();
-  int base = inc - sum;
+  T base = inc - sum;
   for (int w = 0; w < warp; ++w) base += warp_sums[w];
   for (int i = i0; i < i1; ++i) pre[i] += base;
   if (i0 < i1 && i1 == n) pre[n] = base + sum;
   if (n == 0 && tid == 0) pre[0] = 0;
   __syncthreads();
+}
+
+// Launches a kernel of an attention call; chained: as a programmatic dependent
+// of the call's kernel before it, so that its start overlaps that one's end. Such a
+// kernel calls grid_wait before it reads or overwrites what that one wrote, and before its last block ends.
+template <typename Kernel>
+inline cudaError_t launch_chained(Kernel kernel, const PagedAttnParams& p, dim3 grid, int threads, size_t smem,
+                                  bool chained, cudaStream_t s) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = chained ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
 // Where a row's result goes, and what it is merged with (PagedAttnParams' fields).
@@ -124,11 +143,11 @@ __device__ __forceinline__ RowOutput row_output(const PagedAttnParams& p) {
 template <int D>
 __device__ __forceinline__ void merge_prev(const RowOutput& p, int tok, int head, int col, float (&acc)[8],
                                            float& lse2) {
-  const float pl = p.prev_lse[(size_t)head * p.n_tok + tok];
+  const float pl = __ldcg(p.prev_lse + (size_t)head * p.n_tok + tok);
   const float m = fmaxf(lse2, pl);
   if (m == -INFINITY) return;  // neither side saw a key
   const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.heads + head) * D + col);
-  const float4 a = src[0], b = src[1];
+  const float4 a = __ldcg(src), b = __ldcg(src + 1);
   const float w = exp2f(lse2 - m), wp = exp2f(pl - m), inv = 1.f / (w + wp);
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll

@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       for (int k = max(0, g - L::kStages); k < g; ++k)
         ptx::mbar_wait(&bar_full[k % L::kStages], (k / L::kStages) & 1, &dummy, p.status, RC_ETIMEOUT);
     }
+    ptx::grid_wait();
     return;
   }
 
@@ -385,6 +386,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const int row = tid / (D / 8), col = (tid % (D / 8)) * 8;
+    ptx::grid_wait();  // the kernels before this one in a chain have written what the row is merged with
     if (row < R) {
       const float* b = reinterpret_cast<const float*>(base + L::kMerge) + row * L::kOPad + col;
       float acc[8];
@@ -429,8 +431,8 @@ static cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
                                 (int)DecLayout<D>::kDynSmem);
   });
   if (e != cudaSuccess) return e;
-  paged_decode_kernel<D, BF16><<<p.n_ctas, kDecThreads, DecLayout<D>::kDynSmem, s>>>(p);
-  return cudaGetLastError();
+  return launch_chained(paged_decode_kernel<D, BF16>, p, dim3(p.n_ctas), kDecThreads, DecLayout<D>::kDynSmem,
+                        p.prev_o != nullptr, s);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {

@@ -268,6 +268,12 @@ PREFIX = [  # as above, and the prefix's length
     ([(1, 40)] * 70, 8, 2, 64, 32, (1, 0, 0), 500),
     ([(160, 320), (160, 160), (3, 200)], 4, 4, 128, 64, (160, 0, 0), 700),
     ([(33, 400), (90, 90)], 14, 2, 64, 128, (1, 2, 50), 129),
+    # sequences that fill their query tiles walk the prefix themselves
+    ([(300, 300), (513, 700), (260, 1000)], 2, 2, 128, 16, (1, 0, 0), 257),
+    ([(640, 1280), (320, 320)], 4, 1, 64, 64, (160, 1, 3), 1000),
+    ([(290, 290), (0, 5), (700, 900)], 4, 4, 64, 32, (1, 3, 40), 128),
+    # and those that do not, with the prefix in a pass of its own before a pass for many rows
+    ([(30, 30)] * 12 + [(0, 9), (1, 77)], 6, 3, 128, 32, (1, 0, 0), 260),
 ]
 
 
