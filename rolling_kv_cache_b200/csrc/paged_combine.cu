@@ -18,12 +18,13 @@ namespace {
 
 constexpr int kCombThreads = 256;
 
-// DECODE: up to 16 rows a unit, all in block y = 0; else 256 rows, 32 a block.
+// DECODE: up to 16 rows a unit, all in block y = 0; else 256 rows, 16 a block
+// (few units cut over many CTAs: with 32 a block, 8 units of 18 parts took 22 us).
 template <int D, bool BF16, bool DECODE>
 __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int kChunks = D / 8;
   constexpr int kUnitRows = DECODE ? kDecodeRows : kPrefillRows;
-  constexpr int kRows = DECODE ? kDecodeRows : 32;
+  constexpr int kRows = 16;
   __shared__ int last_sh;
   __shared__ float weight[kMaxPersistentCtas][kRows];
   __shared__ float lse_sh[kRows];
@@ -98,13 +99,12 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
 #pragma unroll 4
       for (int i = grp; i < parts; i += groups) {
         const float w = weight[i][r];
-        if (w != 0.f) {  // nothing was written where it is 0
-          const float4* src = reinterpret_cast<const float4*>(p.part_o + (part_row(i) + r) * D + col);
-          const float4 a = __ldcg(src), b = __ldcg(src + 1);
-          const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+        // nothing was written where the weight is 0: such a load goes to the first part
+        const float4* src = reinterpret_cast<const float4*>(p.part_o + (part_row(w != 0.f ? i : 0) + r) * D + col);
+        const float4 a = __ldcg(src), b = __ldcg(src + 1);
+        const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = fmaf(x[k], w, acc[k]);
-        }
+        for (int k = 0; k < 8; ++k) acc[k] = fmaf(x[k], w, acc[k]);
       }
     }
     if (groups > 1) {
@@ -163,7 +163,7 @@ cudaError_t merge_d(const PagedAttnParams& p, cudaStream_t s) {
 
 template <int D, bool BF16>
 cudaError_t combine_d(const PagedAttnParams& p, bool decode, cudaStream_t s) {
-  const dim3 grid(p.n_ctas, decode ? 1 : kPrefillRows / 32);
+  const dim3 grid(p.n_ctas, decode ? 1 : kPrefillRows / 16);
   return decode ? launch_chained(paged_combine_kernel<D, BF16, true>, p, grid, kCombThreads, 0, true, s)
                 : launch_chained(paged_combine_kernel<D, BF16, false>, p, grid, kCombThreads, 0, true, s);
 }

@@ -213,31 +213,35 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   const uint32_t plane = p.box_rows * 128, box0 = (kw / p.box_rows) * plane * L::kSub;
   const int krow0 = kw & (p.box_rows - 1);
   const float c = p.scale_log2, thresh = kDecRescaleLog2 / c;
+  const int i0 = r0 / p.G, i1 = r1 / p.G, h0 = r0 - i0 * p.G, h1 = r1 - i1 * p.G;  // query and head of the rows
   int g = 0, nu = 0;
   bool alive = true;  // a warp whose wait gave up still meets the others at the merges' barriers
-  while (walk.next(u)) {
-    const Seq s = load_seq(p.b, p.n_tok, u.b);
+  // A unit's sequence and Q fragments (rows r0 and r1, zero behind the last
+  // row). The next unit's are loaded before the current one's merge, which hides
+  // their latency
+  Seq s;
+  uint32_t qf[D / 16][4];
+  auto fetch = [&](const DecUnit& v, Seq& sv, uint32_t (&f)[D / 16][4]) {
+    sv = load_seq(p.b, p.n_tok, v.b);
+    const int rows = min(sv.n, 16 / p.G) * p.G;
+    const uint8_t* q0 = p.q.data + (sv.q0 + i0) * p.q.tok_stride + (v.h * p.G + h0) * p.q.head_stride + cq * 2;
+    const uint8_t* q1 = p.q.data + (sv.q0 + i1) * p.q.tok_stride + (v.h * p.G + h1) * p.q.head_stride + cq * 2;
+#pragma unroll
+    for (int k = 0; k < D / 16; ++k) {
+      f[k][0] = r0 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32)) : 0u;
+      f[k][1] = r1 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32)) : 0u;
+      f[k][2] = r0 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q0 + k * 32 + 16)) : 0u;
+      f[k][3] = r1 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32 + 16)) : 0u;
+    }
+  };
+  bool more = walk.next(u);
+  if (more) fetch(u, s, qf);
+  while (more) {
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
     const int nq = min(s.n, 16 / p.G), R = nq * p.G;
     if (nq < s.n && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-    const int i0 = r0 / p.G, i1 = r1 / p.G;
     const RowMask m0 = row_mask(p.mask, s.L - s.n + i0, s.L), m1 = row_mask(p.mask, s.L - s.n + i1, s.L);
-    const RowMask first = row_mask(p.mask, s.L - s.n, s.L), last = row_mask(p.mask, s.L - 1, s.L);
-    // Q fragments: rows r0 and r1, zero behind the last row
-    uint32_t qf[D / 16][4];
-    {
-      const uint8_t* q0 = p.q.data + (s.q0 + i0) * p.q.tok_stride + (u.h * p.G + r0 - i0 * p.G) * p.q.head_stride;
-      const uint8_t* q1 = p.q.data + (s.q0 + i1) * p.q.tok_stride + (u.h * p.G + r1 - i1 * p.G) * p.q.head_stride;
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        const int off = (k * 16 + cq) * 2;
-        qf[k][0] = r0 < R ? __ldg(reinterpret_cast<const uint32_t*>(q0 + off)) : 0u;
-        qf[k][1] = r1 < R ? __ldg(reinterpret_cast<const uint32_t*>(q1 + off)) : 0u;
-        qf[k][2] = r0 < R ? __ldg(reinterpret_cast<const uint32_t*>(q0 + off + 16)) : 0u;
-        qf[k][3] = r1 < R ? __ldg(reinterpret_cast<const uint32_t*>(q1 + off + 16)) : 0u;
-      }
-    }
     float o[D / 8][4];
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
@@ -265,7 +269,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       }
       // keep: bit pairs of this lane's 4 keys (w0 + cq, +1, +8, +9) that some row sees
       const uint32_t pages = readable[st];
-      const bool whole = w0 + 16 <= first.hi && (w0 >= last.lo || (p.mask.window > 0 && w0 + 16 <= p.mask.sink_tok)) &&
+      const bool whole = w0 + 16 <= sp.hi_min && (w0 >= sp.lo_max || (p.mask.window > 0 && w0 + 16 <= p.mask.sink_tok)) &&
                          ((pages >> (kw / p.box_rows)) & 1u);
       uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
       if (!whole) {
@@ -338,6 +342,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar_empty[st]);
     }
+    const DecUnit done = u;
+    const Seq ds = s;
+    more = walk.next(u);
+    if (more) fetch(u, s, qf);
     // ------------------------------------------------- merge of the 8 warps
 #pragma unroll
     for (int d = 1; d < 4; d <<= 1) {
@@ -403,14 +411,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       float lse2 = l == 0.f ? -INFINITY : gm * c + log2f(l);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] *= inv;
-      if (u.lo > 0 || u.hi < u.total) {
-        const size_t at = (size_t)(2 * blockIdx.x + (u.lo > 0 ? 0 : 1)) * kDecodeRows + row;
+      if (done.lo > 0 || done.hi < done.total) {
+        const size_t at = (size_t)(2 * blockIdx.x + (done.lo > 0 ? 0 : 1)) * kDecodeRows + row;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
         if (col == 0) p.part_lse[at] = lse2;
       } else {
-        const int i = row / p.G, head = u.h * p.G + row - i * p.G, tok = s.q0 + i;
+        const int i = row / p.G, head = done.h * p.G + row - i * p.G, tok = ds.q0 + i;
         const RowOutput to = row_output(p);
         if (to.prev_o) merge_prev<D>(to, tok, head, col, acc, lse2);
         store_row<D, BF16>(to, tok, head, col, acc, lse2);
