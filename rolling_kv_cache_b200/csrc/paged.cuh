@@ -95,7 +95,7 @@ struct alignas(64) PagedAttnParams {
   // null, or where the result goes instead of out and lse: fp32 [n_tok][q_heads][d], log2 [q_heads][n_tok]
   float* pre_o;
   float* pre_lse;
-  // null, or such a result that the last write merges with (decode, its combine, and the merge kernel)
+  // the merge kernel's: such a result that it merges with pre_o, pre_lse
   const float* prev_o;
   const float* prev_lse;
   int n_tok, Hk, G;
@@ -109,7 +109,12 @@ constexpr int kDecodeRows = 16;
 constexpr int kPrefillRows = 256;
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
-cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
+// chained: as a programmatic dependent of the kernel before it, whose results it does not read
+cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
+// out from a decode pass over the sequences' own tokens (`own`) and a pass of the batch over their prefix (`pre`),
+// from whole results (pre_o, pre_lse of each) and parts alike. Launched as a programmatic dependent.
+cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams& pre, bool bf16, int head_dim,
+                              cudaStream_t s);
 // out = the merge of two results in fp32 (prev_o, prev_lse; pre_o, pre_lse), for the rows of sequences.
 cudaError_t launch_paged_merge(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 cudaError_t launch_paged_combine(const PagedAttnParams& p, bool bf16, int head_dim, bool decode, cudaStream_t s);

@@ -168,7 +168,7 @@ struct Work {
   int n_ctas, group;
   size_t part_o, part_lse, rec, total;
   size_t x_part_o, x_part_lse, x_rec, pre_o, pre_lse;  // two passes: the prefix's parts and its result
-  size_t own_o, own_lse;                                // and the prefill pass's over the sequences' own tokens
+  size_t own_o, own_lse;                                // and that over the sequences' own tokens
 };
 
 rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_heads, Work* w) {
@@ -196,7 +196,7 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   w->lead = m->prefix_len > 0 && !w->decode && (int64_t)n_tok >= (int64_t)per_pair * p->n_seqs;
   w->two_pass = m->prefix_len > 0 && !w->lead;
   // positions of the stream-K split are 32-bit: tiles of every unit, summed
-  const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 2;
+  const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 5;
   const int64_t pairs = (int64_t)n_tok / per_pair + p->n_seqs + 1;
   if ((w->decode ? tiles * p->n_seqs : tiles * pairs) * p->kv_heads >= INT_MAX)
     return SetLastError(RC_ERANGE, "the batch has too many key tiles for one call");
@@ -221,10 +221,8 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
     parts(rc::kPrefillRows, &w->x_part_o, &w->x_part_lse, &w->x_rec);
     w->pre_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
     w->pre_lse = take((size_t)n_tok * q_heads * 4);
-    if (!w->decode) {
-      w->own_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
-      w->own_lse = take((size_t)n_tok * q_heads * 4);
-    }
+    w->own_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
+    w->own_lse = take((size_t)n_tok * q_heads * 4);
   }
   w->total = o;
   return RC_OK;
@@ -354,7 +352,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       return RC_OK;
     };
     auto prefill = [&](const rc::PagedAttnParams& x) -> rc_status {
-      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "paged attention launch");
+      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, false, s)) return cuda_failed(e, "paged attention launch");
       if (cudaError_t e = rc::launch_paged_combine(x, bf16, d, false, s)) return cuda_failed(e, "combine launch");
       return RC_OK;
     };
@@ -370,8 +368,8 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       p.lead_len = m->prefix_len;
     }
     if (!w.two_pass && !w.decode) return prefill(p);
+    rc::PagedAttnParams x = p;  // two passes: every query of the batch against the prefix's pages
     if (w.two_pass) {
-      rc::PagedAttnParams x = p;  // every query of the batch against the prefix's pages
       x.b.page_table = m->prefix_table;
       x.b.max_pages = m->prefix_pages;
       x.b.table_stride = 0;
@@ -383,21 +381,24 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       x.rec = reinterpret_cast<int4*>(ws + w.x_rec);
       x.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
       x.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+      p.pre_o = reinterpret_cast<float*>(ws + w.own_o);
+      p.pre_lse = reinterpret_cast<float*>(ws + w.own_lse);
+    }
+    if (!w.decode) {
       if (rc_status st = prefill(x)) return st;
-      if (!w.decode) {
-        p.pre_o = reinterpret_cast<float*>(ws + w.own_o);
-        p.pre_lse = reinterpret_cast<float*>(ws + w.own_lse);
-        if (rc_status st = prefill(p)) return st;
-      }
+      if (rc_status st = prefill(p)) return st;
       p.prev_o = x.pre_o;
       p.prev_lse = x.pre_lse;
-      if (!w.decode) {
-        if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
-        return RC_OK;
-      }
+      if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
+      return RC_OK;
     }
     if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
     if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, s)) return cuda_failed(e, "paged attention launch");
+    if (w.two_pass) {
+      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, true, s)) return cuda_failed(e, "prefix launch");
+      if (cudaError_t e = rc::launch_paged_join(p, x, bf16, d, s)) return cuda_failed(e, "join launch");
+      return RC_OK;
+    }
     if (cudaError_t e = rc::launch_paged_combine(p, bf16, d, true, s)) return cuda_failed(e, "combine launch");
     return RC_OK;
   });

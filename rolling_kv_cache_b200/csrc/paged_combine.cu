@@ -18,6 +18,26 @@ namespace {
 
 constexpr int kCombThreads = 256;
 
+// weight[i][r] from log2-sum-exps to the shares of the sum, for sources i < n
+// and rows r < rows, a warp a row; lse[r]: the log2 of the sum.
+template <int ROWS>
+__device__ __forceinline__ void normalise(float (*weight)[ROWS], int n, int rows, float* lse) {
+  const int lane = threadIdx.x & 31;
+  for (int r = threadIdx.x >> 5; r < rows; r += kCombThreads / 32) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = lane; i < n; i += 32) m = fmaxf(m, weight[i][r]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int i = lane; i < n; i += 32) l += exp2f(weight[i][r] - ref);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int i = lane; i < n; i += 32) weight[i][r] = exp2f(weight[i][r] - ref) * inv;
+    if (lane == 0) lse[r] = l == 0.f ? -INFINITY : ref + log2f(l);
+  }
+}
+
 // DECODE: up to 16 rows a unit, all in block y = 0; else 256 rows, 16 a block
 // (few units cut over many CTAs: with 32 a block, 8 units of 18 parts took 22 us).
 template <int D, bool BF16, bool DECODE>
@@ -29,9 +49,8 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
   __shared__ float weight[kMaxPersistentCtas][kRows];
   __shared__ float lse_sh[kRows];
   __shared__ float so[kCombThreads][9];
-  const int tid = threadIdx.x, lane = tid & 31, c = blockIdx.x;
+  const int tid = threadIdx.x, c = blockIdx.x;
   if (tid == 0) last_sh = p.n_ctas - 1;
-  ptx::grid_launch_dependents();
   ptx::grid_wait();
   // records and parts come from L2 (ld.cg): this block's SM may have cached
   // their addresses before the attention kernel wrote them
@@ -72,19 +91,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
     weight[i][r] = there ? __ldcg(p.part_lse + part_row(i) + r) : -INFINITY;
   }
   __syncthreads();
-  for (int r = tid >> 5; r < rows; r += kCombThreads / 32) {
-    float m = -INFINITY, l = 0.f;
-    for (int i = lane; i < parts; i += 32) m = fmaxf(m, weight[i][r]);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < parts; i += 32) l += exp2f(weight[i][r] - ref);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = lane; i < parts; i += 32) weight[i][r] = exp2f(weight[i][r] - ref) * inv;
-    if (lane == 0) lse_sh[r] = l == 0.f ? -INFINITY : ref + log2f(l);
-  }
+  normalise(weight, parts, rows, lse_sh);
   __syncthreads();
   const RowOutput to = row_output(p);
   const int items = rows * kChunks, groups = max(1, kCombThreads / items);
@@ -128,10 +135,142 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
       h = rr % p.G;
       if (rr >= tpt * p.G || i >= s.n) continue;
     }
-    float lse2 = lse_sh[r];
-    if (DECODE && to.prev_o) merge_prev<D>(to, s.q0 + i, head0 + h, col, acc, lse2);
-    store_row<D, BF16>(to, s.q0 + i, head0 + h, col, acc, lse2);
+    store_row<D, BF16>(to, s.q0 + i, head0 + h, col, acc, lse_sh[r]);
   }
+}
+
+// One result over some of the keys of a unit: where it lies whole, and where in parts.
+struct JoinSide {
+  const float* o;
+  const float* lse;  // whole rows: [n_tok][q_heads][d] and [q_heads][n_tok]
+  const float* part_o;
+  const float* part_lse;
+  const int4* rec;
+};
+struct JoinParams {
+  BatchView b;
+  RowOutput to;
+  JoinSide own, pre;
+  int n_tok, Hk, G, n_ctas;
+};
+
+constexpr int kJoinSources = 2 * kMaxPersistentCtas + 2;
+
+// Block (b, h): the rows of sequence b and key head h (at most 16). A row's
+// sources are its unit's parts in the decode pass, or its whole row, and the
+// parts, or the whole row, of the query pair its token lies in in the pass over the prefix.
+// As in the combine kernel: all sources' weights first, then the weighted sum.
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_constant__ JoinParams p) {
+  constexpr int kChunks = D / 8;
+  __shared__ int first_sh[3], last_sh[3];  // the decode unit's, and the first and last token's pair's
+  __shared__ float scratch[kJoinSources * kDecodeRows];  // small enough to be resident beside the attention kernels
+  __shared__ float lse_sh[kDecodeRows];
+  __shared__ uint8_t there[2][kMaxPersistentCtas];  // a CTA's record: bit 0 it holds a unit's later part, bit 1 the last
+  float(*weight)[kDecodeRows] = reinterpret_cast<float(*)[kDecodeRows]>(scratch);
+  float(*so)[9] = reinterpret_cast<float(*)[9]>(scratch);  // after the weights
+  static_assert(kCombThreads * 9 <= kJoinSources * kDecodeRows, "the sums fit");
+  const int tid = threadIdx.x;
+  const int b = blockIdx.x / p.Hk, h = blockIdx.x - b * p.Hk;
+  const Seq s = load_seq(p.b, p.n_tok, b);
+  const int R = min(s.n, 16 / p.G) * p.G, heads = p.Hk * p.G;
+  const int per_pair = 2 * (128 / p.G);
+  const int total = min(max(__ldg(p.b.cu_q + p.b.n_seqs), 0), p.n_tok);
+  const int pairs = (total + per_pair - 1) / per_pair;
+  const int pair0 = s.q0 / per_pair, pair1 = R > 0 ? (s.q0 + R / p.G - 1) / per_pair : pair0;
+  if (tid < 3) {
+    first_sh[tid] = -1;
+    last_sh[tid] = p.n_ctas - 1;
+  }
+  ptx::grid_wait();
+  if (R == 0) return;
+  __syncthreads();
+  for (int c = tid; c < p.n_ctas; c += kCombThreads) {
+    const int4 x = __ldcg(p.own.rec + c), y = __ldcg(p.pre.rec + c);
+    if (x.z == b && x.w == h) first_sh[0] = c;
+    if (y.z >= 0 && y.w == h * pairs + pair0) first_sh[1] = c;
+    if (y.z >= 0 && y.w == h * pairs + pair1) first_sh[2] = c;
+    there[0][c] = (x.x ? 1 : 0) | (x.y ? 2 : 0);
+    there[1][c] = (y.x ? 1 : 0) | (y.y ? 2 : 0);
+  }
+  __syncthreads();
+  for (int c = tid; c < p.n_ctas; c += kCombThreads)
+    for (int k = 0; k < 3; ++k)
+      if (first_sh[k] >= 0 && c > first_sh[k] && (there[k > 0][c] & 2)) atomicMin(&last_sh[k], c);
+  __syncthreads();
+  const int n_own = first_sh[0] < 0 ? 1 : last_sh[0] - first_sh[0] + 1;
+  const int n_pre0 = first_sh[1] < 0 ? 1 : last_sh[1] - first_sh[1] + 1;
+  const int n_pre1 = first_sh[2] < 0 ? 1 : last_sh[2] - first_sh[2] + 1;
+  const int n = n_own + max(n_pre0, n_pre1);
+  // source e of row r: its values (or null: there is none) and its log-sum-exp
+  auto source = [&](int e, int r, const float** o) -> const float* {
+    const int i = r / p.G, tok = s.q0 + i, head = h * p.G + r - i * p.G;
+    const bool own = e < n_own;
+    const JoinSide& side = own ? p.own : p.pre;
+    const int k = own ? 0 : (tok / per_pair == pair0 ? 1 : 2);
+    if (!own) e -= n_own;
+    *o = nullptr;
+    if (first_sh[k] < 0) {
+      if (e > 0) return nullptr;
+      *o = side.o + ((size_t)tok * heads + head) * D;
+      return side.lse + (size_t)head * p.n_tok + tok;
+    }
+    const int c = first_sh[k] + e;
+    if (c > last_sh[k] || (e > 0 && !(there[!own][c] & 1))) return nullptr;
+    const int in_pair = tok % per_pair, tile = in_pair / (per_pair / 2);
+    const int row = own ? r : tile * 128 + (in_pair - tile * (per_pair / 2)) * p.G + r - i * p.G;
+    const size_t at = (size_t)(2 * c + (e == 0)) * (own ? kDecodeRows : kPrefillRows) + row;
+    *o = side.part_o + at * D;
+    return side.part_lse + at;
+  };
+  for (int x = tid; x < n * kDecodeRows; x += kCombThreads) {
+    const int e = x / kDecodeRows, r = x % kDecodeRows;
+    const float *o, *l = r < R ? source(e, r, &o) : nullptr;
+    weight[e][r] = l ? __ldcg(l) : -INFINITY;
+  }
+  __syncthreads();
+  normalise(weight, n, R, lse_sh);
+  __syncthreads();
+  const int items = R * kChunks, groups = kCombThreads / items;
+  const int item = tid % items, grp = tid / items;
+  const int r = item / kChunks, col = item % kChunks * 8;
+  float acc[8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+  if (grp < groups) {
+    const float* first;
+    source(0, r, &first);
+#pragma unroll 4
+    for (int e = grp; e < n; e += groups) {
+      const float w = weight[e][r];
+      const float* o;
+      source(e, r, &o);
+      // nothing was written where the weight is 0: such a load goes to the first source
+      const float4* src = reinterpret_cast<const float4*>((w != 0.f ? o : first) + col);
+      const float4 a = __ldcg(src), c = __ldcg(src + 1);
+      const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
+#pragma unroll
+      for (int k = 0; k < 8; ++k) acc[k] = fmaf(x[k], w, acc[k]);
+    }
+  }
+  if (groups > 1) {
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 8; ++k) so[tid][k] = acc[k];
+    __syncthreads();
+    if (grp == 0)
+      for (int g = 1; g < groups; ++g)
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] += so[g * items + item][k];
+  }
+  if (grp != 0) return;
+  const int i = r / p.G;
+  store_row<D, BF16>(p.to, s.q0 + i, h * p.G + r - i * p.G, col, acc, lse_sh[r]);
+}
+
+template <int D, bool BF16>
+cudaError_t join_d(const JoinParams& p, cudaStream_t s) {
+  return launch_chained(paged_join_kernel<D, BF16>, p, dim3(p.b.n_seqs * p.Hk), kCombThreads, 0, true, s);
 }
 
 // out = the merge of the results in (pre_o, pre_lse) and (prev_o, prev_lse), 8
@@ -173,6 +312,22 @@ cudaError_t combine_d(const PagedAttnParams& p, bool decode, cudaStream_t s) {
 cudaError_t launch_paged_combine(const PagedAttnParams& p, bool bf16, int head_dim, bool decode, cudaStream_t s) {
   if (head_dim == 64) return bf16 ? combine_d<64, true>(p, decode, s) : combine_d<64, false>(p, decode, s);
   return bf16 ? combine_d<128, true>(p, decode, s) : combine_d<128, false>(p, decode, s);
+}
+
+cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams& pre, bool bf16, int head_dim,
+                              cudaStream_t s) {
+  JoinParams p{};
+  p.b = own.b;
+  p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse, nullptr, nullptr, nullptr,
+                   nullptr,      nullptr,            nullptr,             own.n_tok, own.Hk * own.G};
+  p.own = JoinSide{own.pre_o, own.pre_lse, own.part_o, own.part_lse, own.rec};
+  p.pre = JoinSide{pre.pre_o, pre.pre_lse, pre.part_o, pre.part_lse, pre.rec};
+  p.n_tok = own.n_tok;
+  p.Hk = own.Hk;
+  p.G = own.G;
+  p.n_ctas = own.n_ctas;
+  if (head_dim == 64) return bf16 ? join_d<64, true>(p, s) : join_d<64, false>(p, s);
+  return bf16 ? join_d<128, true>(p, s) : join_d<128, false>(p, s);
 }
 
 cudaError_t launch_paged_merge(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {

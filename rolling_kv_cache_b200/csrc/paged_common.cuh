@@ -103,8 +103,8 @@ __device__ __forceinline__ void block_prefix(T* pre, int n, T* warp_sums, Fn f) 
 // Launches a kernel of an attention call; chained: as a programmatic dependent
 // of the call's kernel before it, so that its start overlaps that one's end. Such a
 // kernel calls grid_wait before it reads or overwrites what that one wrote, and before its last block ends.
-template <typename Kernel>
-inline cudaError_t launch_chained(Kernel kernel, const PagedAttnParams& p, dim3 grid, int threads, size_t smem,
+template <typename Params>
+inline cudaError_t launch_chained(void (*kernel)(const Params), const Params& p, dim3 grid, int threads, size_t smem,
                                   bool chained, cudaStream_t s) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;

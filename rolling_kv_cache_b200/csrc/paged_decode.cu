@@ -8,11 +8,12 @@
 //
 // The units (sequence, key head) are cut into 64-key tiles, and the tiles of
 // the whole batch, in order, into one range per CTA (one CTA per SM), equal to
-// a tile: a ragged batch and a single long sequence keep every SM reading
-// alike. Each CTA finds its range from the lengths on the device. A unit cut
+// a tile, a unit's start and end counted as kUnitCost more: a ragged batch and a single long
+// sequence keep every SM reading alike. Each CTA finds its range from the lengths on the device. A unit cut
 // between CTAs leaves parts for the combine kernel.
 //
-// One warp issues TMA copies of the tiles' pages (a box per page, its 64-dim
+// Two warps (one for K, one for V: with 16-token pages one warp took 1500
+// cycles a tile, as long as HBM does) issue TMA copies of the tiles' pages (a box per page, its 64-dim
 // planes one after the other, 128-byte swizzle) into a ring of 128 KB, running ahead across units, so
 // that about that much of HBM reads is in flight per SM. Two groups of four warps
 // take alternate tiles; a warp owns 16 keys of its tile: S = Q K^T and O += P V
@@ -33,9 +34,12 @@ namespace {
 
 constexpr int kTK = 64;                       // keys per tile
 constexpr int kConsumers = 8;                 // warps
-constexpr int kDecThreads = (kConsumers + 1) * 32;
+constexpr int kDecThreads = (kConsumers + 2) * 32;  // and two producers
 constexpr int kRingBytes = 128 * 1024;
 constexpr float kDecRescaleLog2 = 8.f;
+// What a unit costs beside its tiles, in tiles (its queries, its merge and its
+// writes: 4500 cycles to a tile's 1500)
+constexpr int kUnitCost = 3;
 
 template <int D>
 struct DecLayout {
@@ -60,23 +64,31 @@ struct DecUnit {
   int b, h, lo, hi, total;  // tiles [lo, hi) of the unit's `total`
 };
 
-// Walks the units of positions [pos, end): position Hk * pre[b] + h * w + t is
-// tile t of head h of sequence b, w = pre[b + 1] - pre[b].
+// Walks the units of positions [pos, end): a unit of w tiles takes kUnitCost + w
+// positions, and position Hk * pre[b] + h * (pre[b + 1] - pre[b]) is the first of head h of
+// sequence b. A range that begins or ends among a unit's cost is moved to the
+// unit's start, alike for the CTAs on both sides.
 struct DecWalk {
   const int* pre;
   int Hk, pos, end, b;
+  __device__ __forceinline__ int at(int x, int n, int* seq) const {
+    int lo = 0, hi = n - 1;
+    while (lo < hi) {  // the largest b with Hk * pre[b] <= x
+      const int mid = (lo + hi + 1) >> 1;
+      if (Hk * pre[mid] <= x) lo = mid;
+      else hi = mid - 1;
+    }
+    *seq = lo;
+    if (x >= Hk * pre[n]) return x;
+    const int off = (x - Hk * pre[lo]) % (pre[lo + 1] - pre[lo]);
+    return off <= kUnitCost ? x - off : x;
+  }
   __device__ __forceinline__ void init(const int* pre_, int n, int Hk_, int pos_, int end_) {
     pre = pre_;
     Hk = Hk_;
-    pos = pos_;
-    end = end_;
-    int lo = 0, hi = n - 1;
-    while (lo < hi) {  // the largest b with Hk * pre[b] <= pos
-      const int mid = (lo + hi + 1) >> 1;
-      if (Hk * pre[mid] <= pos) lo = mid;
-      else hi = mid - 1;
-    }
-    b = lo;
+    int unused;
+    end = at(end_, n, &unused);
+    pos = at(pos_, n, &b);
   }
   __device__ __forceinline__ bool next(DecUnit& u) {
     if (pos >= end) return false;
@@ -84,10 +96,11 @@ struct DecWalk {
     const int w = pre[b + 1] - pre[b], rem = pos - Hk * pre[b];
     u.b = b;
     u.h = rem / w;
-    u.lo = rem - u.h * w;
-    u.total = w;
-    u.hi = min(w, u.lo + end - pos);
-    pos += u.hi - u.lo;
+    const int off = rem - u.h * w, len = min(w - off, end - pos);
+    u.total = w - kUnitCost;
+    u.lo = max(off - kUnitCost, 0);
+    u.hi = max(off + len - kUnitCost, 0);
+    pos += len;
     return true;
   }
 };
@@ -99,7 +112,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   __shared__ uint64_t bar_full[L::kStages], bar_empty[L::kStages];
   __shared__ uint32_t readable[L::kStages];  // bit i: page i of the stage's tile is one
   __shared__ float wm[2][kConsumers][16], wl[2][kConsumers][16];
-  __shared__ int warp_sums[kConsumers + 1];
+  __shared__ int warp_sums[kConsumers + 2];
   __shared__ int abort_sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* base = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
@@ -107,7 +120,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   int* pre = reinterpret_cast<int*>(base + L::kPre);
   if (tid == 0) {
     for (int i = 0; i < L::kStages; ++i) {
-      ptx::mbar_init(&bar_full[i], 1);
+      ptx::mbar_init(&bar_full[i], 2);
       ptx::mbar_init(&bar_empty[i], 4);
     }
     abort_sh = 0;
@@ -120,7 +133,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     if (s.n == 0) return 0;
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-    return max(sp.n, 1);
+    return max(sp.n, 1) + kUnitCost;
   });
   const int W = p.Hk * pre[p.b.n_seqs];
   const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
@@ -130,19 +143,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   walk.init(pre, p.b.n_seqs, p.Hk, pos, end);
   DecUnit u;
 
-  if (warp == kConsumers) {
-    // ------------------------------------------------------------ producer
-    if (lane == 0) {
-      ptx::tma_prefetch_desc(&p.tm_k);
-      ptx::tma_prefetch_desc(&p.tm_v);
-    }
+  if (warp >= kConsumers) {
+    // ----------------------------------------------------------- producers
+    const bool is_v = warp > kConsumers;
+    const CUtensorMap* map = is_v ? &p.tm_v : &p.tm_k;
+    if (lane == 0) ptx::tma_prefetch_desc(map);
     const uint64_t pol = ptx::l2_policy(false);
-    // a tile is `boxes` runs of box_rows keys, each in one page; a lane copies
-    // one run of K or of V
+    // a tile is `boxes` runs of box_rows keys, each in one page; a lane copies one
     const int boxes = kTK / p.box_rows;
     const int in_page = (1 << p.b.page_log2) - 1;
     const int box = lane & (boxes - 1);
-    const bool is_k = lane < boxes, is_v = !is_k && lane < 2 * boxes;
     const uint32_t dst0 = (is_v ? L::kTile : 0) + box * p.box_rows * 128 * L::kSub;
     int g = 0, j = 0, n = 0, k0 = 0, page = -1;
     bool want = false, ok = true;
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         if (!walk.next(u)) return false;
         const Seq s = load_seq(p.b, p.n_tok, u.b);
         sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-        if (lane == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        if (lane == 0 && s.bad && !is_v && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
         if (u.lo > 0) {
           rec.x = 1;
           rec.y = u.hi == u.total;
@@ -184,25 +194,23 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         if (!ok) break;
       }
       if (lane == 0) {
-        readable[st] = pages;
-        ptx::mbar_arrive_expect_tx(&bar_full[st], L::kStage);
+        if (!is_v) readable[st] = pages;
+        ptx::mbar_arrive_expect_tx(&bar_full[st], L::kTile);
       }
       __syncwarp();
       // a page that is none is read out of bounds on purpose: the copy fills zeros
-      uint8_t* dst = base + st * L::kStage + dst0;
-      const int row = good ? row0 : 0, pg = good ? pg0 : p.b.n_pages;
-      if (is_k) ptx::tma_load_5d_hint(&p.tm_k, &bar_full[st], dst, 0, row, 0, h, pg, pol);
-      if (is_v) ptx::tma_load_5d_hint(&p.tm_v, &bar_full[st], dst, 0, row, 0, h, pg, pol);
+      if (lane < boxes)
+        ptx::tma_load_5d_hint(map, &bar_full[st], base + st * L::kStage + dst0, 0, good ? row0 : 0, 0, h,
+                              good ? pg0 : p.b.n_pages, pol);
       __syncwarp();
     }
     if (lane == 0) {
-      p.rec[blockIdx.x] = rec;
+      if (!is_v) p.rec[blockIdx.x] = rec;
       // leave no copy in flight (bounded, whether or not the others gave up)
       int dummy = 0;
       for (int k = max(0, g - L::kStages); k < g; ++k)
         ptx::mbar_wait(&bar_full[k % L::kStages], (k / L::kStages) & 1, &dummy, p.status, RC_ETIMEOUT);
     }
-    ptx::grid_wait();
     return;
   }
 
@@ -216,13 +224,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   const int i0 = r0 / p.G, i1 = r1 / p.G, h0 = r0 - i0 * p.G, h1 = r1 - i1 * p.G;  // query and head of the rows
   int g = 0, nu = 0;
   bool alive = true;  // a warp whose wait gave up still meets the others at the merges' barriers
-  // A unit's sequence and Q fragments (rows r0 and r1, zero behind the last
-  // row). The next unit's are loaded before the current one's merge, which hides
-  // their latency
+  // A unit's Q fragments (rows r0 and r1, zero behind the last row). The next
+  // unit's sequence is loaded before the current one's tiles and its Q before the
+  // current one's merge, which hides their latencies
   Seq s;
   uint32_t qf[D / 16][4];
-  auto fetch = [&](const DecUnit& v, Seq& sv, uint32_t (&f)[D / 16][4]) {
-    sv = load_seq(p.b, p.n_tok, v.b);
+  auto fetch = [&](const DecUnit& v, const Seq& sv, uint32_t (&f)[D / 16][4]) {
     const int rows = min(sv.n, 16 / p.G) * p.G;
     const uint8_t* q0 = p.q.data + (sv.q0 + i0) * p.q.tok_stride + (v.h * p.G + h0) * p.q.head_stride + cq * 2;
     const uint8_t* q1 = p.q.data + (sv.q0 + i1) * p.q.tok_stride + (v.h * p.G + h1) * p.q.head_stride + cq * 2;
@@ -235,8 +242,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
   };
   bool more = walk.next(u);
-  if (more) fetch(u, s, qf);
+  if (more) {
+    s = load_seq(p.b, p.n_tok, u.b);
+    fetch(u, s, qf);
+  }
   while (more) {
+    DecUnit un = u;
+    Seq sn = s;
+    more = walk.next(un);
+    if (more) sn = load_seq(p.b, p.n_tok, un.b);
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
     const int nq = min(s.n, 16 / p.G), R = nq * p.G;
@@ -344,7 +358,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     const DecUnit done = u;
     const Seq ds = s;
-    more = walk.next(u);
+    u = un;
+    s = sn;
     if (more) fetch(u, s, qf);
     // ------------------------------------------------- merge of the 8 warps
 #pragma unroll
@@ -394,7 +409,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     asm volatile("bar.sync 1, 256;" ::: "memory");
     const int row = tid / (D / 8), col = (tid % (D / 8)) * 8;
-    ptx::grid_wait();  // the kernels before this one in a chain have written what the row is merged with
     if (row < R) {
       const float* b = reinterpret_cast<const float*>(base + L::kMerge) + row * L::kOPad + col;
       float acc[8];
@@ -419,9 +433,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         if (col == 0) p.part_lse[at] = lse2;
       } else {
         const int i = row / p.G, head = done.h * p.G + row - i * p.G, tok = ds.q0 + i;
-        const RowOutput to = row_output(p);
-        if (to.prev_o) merge_prev<D>(to, tok, head, col, acc, lse2);
-        store_row<D, BF16>(to, tok, head, col, acc, lse2);
+        store_row<D, BF16>(row_output(p), tok, head, col, acc, lse2);
       }
     }
   }
@@ -440,7 +452,7 @@ static cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   return launch_chained(paged_decode_kernel<D, BF16>, p, dim3(p.n_ctas), kDecThreads, DecLayout<D>::kDynSmem,
-                        p.prev_o != nullptr, s);
+                        false, s);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {
