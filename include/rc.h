@@ -456,7 +456,8 @@ typedef struct rc_paged {
   int32_t head_dim;       /* 64 or 128 */
   int32_t dtype;          /* RC_BF16 or RC_F16 */
   int32_t n_seqs;
-  const int32_t* cu_q;    /* [n_seqs + 1], ascending from 0 */
+  const int32_t* cu_q;    /* [n_seqs + 1], ascending from 0 (where it descends, the attention's results
+                             are undefined, with RC_ERANGE in *status) */
   const int32_t* kv_len;  /* [n_seqs] tokens in the pages, this call's among them */
   const int32_t* page_table;
   int64_t table_stride;
@@ -510,6 +511,7 @@ rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n
  * a key that some query sees must be finite, or the NaN it makes can reach the
  * queries of the same sequence that are computed with it.
  *   lse: NULL or [q_heads][n_tok] fp32, natural log.
+ *   out may be q (same strides), else must not overlap it.
  * max_q * (q_heads / kv_heads) <= 16 takes the kernel for few rows; it
  * computes no more than that many, so max_q must not be below the longest
  * (queries beyond are left out, with RC_ERANGE in *status). */

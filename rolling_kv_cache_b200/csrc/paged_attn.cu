@@ -97,6 +97,7 @@ __device__ __forceinline__ Seq pre_seq(const PagedAttnParams& p, int b) {
     s.q0 = 0;
     s.n = min(max(n, 0), p.n_tok);
     s.L = p.prefix_len;
+    s.falls = false;
     s.bad = s.n != n;
     return s;
   }
@@ -242,8 +243,11 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
   auto seq = [&](int b) {
     if (b >= kPlanSeqs) return pre_seq(p, b);
     const int4 x = seqs[b];
-    return Seq{x.x, x.y, x.z, false};
+    return Seq{x.x, x.y, x.z, false, false};
   };
+  if (tid < kMaxRounds) most[tid] = 0;
+  if (tid < 3) sums[tid] = 0;
+  __syncthreads();
   // tiles and pairs of each sequence (one key head), a warp a sequence
   for (int b = warp; b < n_seqs; b += kPreThreads / 32) {
     const Seq s = pre_seq(p, b);
@@ -257,15 +261,16 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
+      if (s.falls) sums[2] = 1;
       before[b] = (unsigned long long)pairs << 32 | (uint32_t)sum;
       if (b < kPlanSeqs) seqs[b] = make_int4(s.q0, s.n, s.L, 0);
     }
   }
-  if (tid < kMaxRounds) most[tid] = 0;
-  if (tid < 2) sums[tid] = 0;
   __syncthreads();
   block_prefix<kPreThreads>(before, n_seqs, warp_sums, [&](int b) { return before[b]; });
-  const int W = p.Hk * tiles_of(before[n_seqs]), U = p.Hk * pairs_of(before[n_seqs]);
+  const bool falls = sums[2];
+  if (falls && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+  const int W = falls ? 0 : p.Hk * tiles_of(before[n_seqs]), U = falls ? 0 : p.Hk * pairs_of(before[n_seqs]);
   const int r_max = min(U / G, kMaxRounds);
   int rounds = 0, own = 0;
   if (r_max > 0) {
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
   __shared__ JobInfo jobs[kJobRing];
   __shared__ uint64_t bar_jf[kJobRing], bar_je[kJobRing];
   __shared__ unsigned long long warp_sums[18];
-  __shared__ int most[kMaxRounds], sums[2];
+  __shared__ int most[kMaxRounds], sums[3];
   __shared__ Plan plan;
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_sh;

@@ -48,10 +48,12 @@ struct TileSpan {
 
 // One sequence of the batch, with whatever the device arrays hold brought
 // into range: rows [q0, q0 + n) of q, L tokens in the pages. `bad` says that
-// something was out of range.
+// something was out of range. Where cu_q descends (`falls`), rows could be
+// claimed many times over and the sums of the split pass 32 bits: the
+// attention kernels then do nothing but record it.
 struct Seq {
   int q0, n, L;
-  bool bad;
+  bool bad, falls;
 };
 
 __device__ __forceinline__ Seq load_seq(const BatchView& v, int n_tok, int b) {
@@ -60,7 +62,8 @@ __device__ __forceinline__ Seq load_seq(const BatchView& v, int n_tok, int b) {
   s.q0 = min(max(a, 0), n_tok);
   s.n = min(max(e - s.q0, 0), n_tok - s.q0);
   s.L = min(max(l, 0), v.max_pages << v.page_log2);
-  s.bad = s.q0 != a || e - a != s.n || s.L != l;
+  s.falls = e < a;
+  s.bad = s.falls || s.q0 != a || e - a != s.n || s.L != l;
   return s;
 }
 

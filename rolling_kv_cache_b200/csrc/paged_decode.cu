@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   __shared__ uint32_t readable[L::kStages];  // bit i: page i of the stage's tile is one
   __shared__ float wm[2][kConsumers][16], wl[2][kConsumers][16];
   __shared__ int warp_sums[kConsumers + 2];
-  __shared__ int abort_sh;
+  __shared__ int abort_sh, falls_sh;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* base = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
   const uint32_t base_u32 = ptx::smem_u32(base);
@@ -124,18 +124,22 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       ptx::mbar_init(&bar_empty[i], 4);
     }
     abort_sh = 0;
+    falls_sh = 0;
     ptx::fence_mbar_init();
   }
+  __syncthreads();
   ptx::grid_launch_dependents();
   // tiles of each sequence, and this CTA's range of the batch's
   block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
     const Seq s = load_seq(p.b, p.n_tok, b);
+    if (s.falls) falls_sh = 1;
     if (s.n == 0) return 0;
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
     return max(sp.n, 1) + kUnitCost;
   });
-  const int W = p.Hk * pre[p.b.n_seqs];
+  if (falls_sh && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+  const int W = falls_sh ? 0 : p.Hk * pre[p.b.n_seqs];
   const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
   const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
   volatile int* abort = &abort_sh;

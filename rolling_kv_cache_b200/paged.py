@@ -129,7 +129,7 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     included, and the first ``sink_frames``. Entries of pages that no query sees
     may hold anything. ``max_q``: the most queries of a sequence, where the
     caller knows it (default: all tokens); it chooses the kernel and must not be
-    too small. Rows behind the last sequence are left as they are (uninitialised without ``out``).
+    too small. ``out`` may be q itself. Rows behind the last sequence are left as they are (uninitialised without ``out``).
     Returns out, or (out, lse [q_heads, tokens] fp32). A query that sees
     nothing gets zeros and -inf.
     """

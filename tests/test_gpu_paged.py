@@ -6,7 +6,7 @@ import torch
 from rolling_kv_cache_b200 import binding as B
 from rolling_kv_cache_b200 import paged
 
-from paged_util import Batch, assert_attend, assert_turned, generator, randn, turned
+from paged_util import Batch, assert_attend, assert_turned, attend, generator, randn, turned
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -335,3 +335,422 @@ def test_more_queries_than_max_q_says():
     with pytest.raises(B.RcError) as e:
         paged.device_status()
     assert e.value.status == B.RC_ERANGE
+
+
+# ------------------------------------------------- calls together, and their surroundings
+
+def _cold():
+    return torch.empty(96 * 2 ** 20, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("case", [
+    ([(1, 300 + 211 * i) for i in range(24)], 32, 8, 128, 32, (1, 0, 0), None),
+    ([(1, 4000 + 97 * i) for i in range(9)], 12, 12, 64, 16, (1, 4, 700), None),
+    ([(200 + 31 * i, 700 + 40 * i) for i in range(5)], 14, 2, 128, 64, (1, 0, 0), None),
+    ([(1, 1 + 13 * i) for i in range(40)], 16, 4, 128, 16, (1, 0, 0), 900),
+], ids=["decode", "window", "prompts", "prefix"])
+def test_same_bits_on_every_run_with_cold_and_warm_caches(case):
+    lens, hq, hk, d, page, (f, sinks, window), n = case
+    pages = ((n or 0) + page - 1) // page
+    bt = Batch(31, lens, hq, hk, d, page, spare=pages + 1, fill=0.0)
+    kw = dict(max_q=max(a for a, _ in lens), frame_seqlen=f, sink_frames=sinks, window_frames=window,
+              return_lse=True)
+    if n:
+        table = torch.tensor(bt.free[:pages], dtype=torch.int32, device="cuda")
+        j = torch.arange(n, device="cuda")
+        for pool in (bt.k_pages, bt.v_pages):
+            pool[table[j // page].long(), :, j % page] = randn(bt.gen, n, hk, d)
+        call = lambda: paged.prefix_attention(*bt.args()[:3], table, n, *bt.args()[3:], **kw)  # noqa: E731
+    else:
+        call = lambda: paged.paged_attention(*bt.args(), **kw)  # noqa: E731
+    o, lse = call()
+    flush = _cold()
+    for i in range(40):
+        if i % 2:
+            flush.fill_(i)  # the caches hold something else
+        o2, lse2 = call()
+        assert torch.equal(o, o2) and torch.equal(lse, lse2), i
+
+
+def _place(n, device="cuda"):
+    g = torch.arange(n, device=device)
+    return torch.stack((g // 64, g // 8 % 8, g % 8), -1).int()
+
+
+@pytest.mark.parametrize("q_len,group,f,window", [(1, 4, 1, 0), (1, 1, 1, 40), (48, 2, 16, 5), (150, 1, 64, 0)])
+def test_a_stream_appended_and_attended_step_by_step(q_len, group, f, window):
+    """Tokens go in through the append, queries come out rotated and attend; after every step the output is that
+    of the formula over all tokens so far, rotated by the library's own tables in 64 bits."""
+    hk, d, page, steps, sinks = 2, 64, 16, 3, 1 if window else 0
+    start = [5, 130, 0]
+    bt = Batch(41, [(q_len, n + steps * q_len) for n in start], hk * group, hk, d, page)
+    c = d // 6
+    tables = paged.rope_tables((500, 8, 8), (d // 2 - 2 * c, c, c))
+    g = bt.gen
+    bt.k_pages.fill_(float("nan"))
+    bt.v_pages.fill_(float("nan"))
+    done = [0, 0, 0]
+    for step in range(steps + 1):
+        new = start if step == 0 else [q_len] * 3
+        total = [a + b for a, b in zip(done, new)]
+        cu = torch.tensor([0, new[0], new[0] + new[1], sum(new)], dtype=torch.int32, device="cuda")
+        kv_len = torch.tensor(total, dtype=torch.int32, device="cuda")
+        n = sum(new)
+        fused = randn(g, n, hk * group + 2 * hk, d)
+        q, k, v = fused.split((hk * group, hk, hk), 1)
+        pos = torch.cat([_place(t)[t - m:] for t, m in zip(total, new)])
+        qr = paged.paged_append(q, k, v, bt.k_pages, bt.v_pages, cu, kv_len, bt.page_table, pos=pos, tables=tables)
+        assert_turned(qr, q, pos, tables, False)
+        o, lse = paged.paged_attention(qr, bt.k_pages, bt.v_pages, cu, kv_len, bt.page_table, max_q=max(new),
+                                       frame_seqlen=f, sink_frames=sinks, window_frames=window, return_lse=True)
+        one = Batch.__new__(Batch)
+        one.__dict__.update(bt.__dict__)
+        one.lens, one.cu, one.n_tok, one.q = list(zip(new, total)), cu.tolist(), n, qr
+        assert_attend((o, lse), one, f=f, sinks=sinks, window=window)
+        done = total
+    # what lies in the pages is what was appended
+    assert not bool(bt.k_pages[bt.page_table[1][0].long()].isnan().any())
+
+
+def test_continuations_of_a_prefix_equal_whole_sequences():
+    """prefix_attention over (prefix, own tokens) against paged_attention over sequences that hold both."""
+    n, own, hq, hk, d, page = 160, [1, 33, 70], 8, 2, 128, 16
+    whole = Batch(43, [(1, n + m) for m in own], hq, hk, d, page, spare=20)
+    for b in range(1, len(own)):  # all sequences begin with the first one's pages
+        whole.page_table[b, :n // page] = whole.page_table[0, :n // page]
+    a, la = paged.paged_attention(*whole.args(), max_q=1, return_lse=True)
+    table = whole.page_table[0, :n // page].contiguous()
+    own_table = torch.full_like(whole.page_table, -1)
+    own_table[:, :whole.page_table.shape[1] - n // page] = whole.page_table[:, n // page:]
+    kv = torch.tensor(own, dtype=torch.int32, device="cuda")
+    o, lo = paged.prefix_attention(*whole.args()[:3], table, n, whole.cu_q, kv, own_table, max_q=1, return_lse=True)
+    bound = attend(whole)[2]
+    assert bool(((a.double() - o.double()).abs() <= 2 * bound).all())
+    assert float((la - lo).abs().max()) <= 2.0 ** -11
+
+
+def test_paged_stream_equals_the_ring():
+    """A stream short enough to keep every frame: the ring's step and the paged append and attention agree."""
+    from rolling_kv_cache_b200.cache import RollingKVCache, make_config
+    H, d, gh, gw, chunk = 4, 128, 6, 10, 3
+    F = gh * gw
+    cfg = make_config(layers=1, heads=H, head_dim=d, grid_h=gh, grid_w=gw, sink_frames=1, window_frames=9,
+                      chunk_frames=chunk)
+    cache = RollingKVCache(cfg)
+    c = (d // 2) // 3
+    tables = paged.rope_tables((64, gh, gw), (d // 2 - 2 * c, c, c))
+    g = generator(44)
+    chunks = 3
+    pages = (chunks * chunk * F + 63) // 64
+    k_pages, v_pages = (torch.full((pages + 2, H, 64, d), float("nan"), dtype=BF16, device="cuda") for _ in range(2))
+    table = torch.randperm(pages + 2, generator=g, device="cuda")[:pages].int()[None].contiguous()
+    for i in range(chunks):
+        q, k, v = (randn(g, chunk * F, H, d) for _ in range(3))
+        lse = torch.empty((H, chunk * F), dtype=torch.float32, device="cuda")
+        want = cache.step(0, q, k, v, i * chunk, lse=lse)
+        t = torch.arange(i * chunk * F, (i + 1) * chunk * F, device="cuda")
+        pos = torch.stack((t // F, t % F // gw, t % gw), -1).int()
+        cu = torch.tensor([0, chunk * F], dtype=torch.int32, device="cuda")
+        kv = torch.tensor([(i + 1) * chunk * F], dtype=torch.int32, device="cuda")
+        qr = paged.paged_append(q, k, v, k_pages, v_pages, cu, kv, table, pos=pos, tables=tables)
+        got, l2 = paged.paged_attention(qr, k_pages, v_pages, cu, kv, table, frame_seqlen=F, return_lse=True)
+        # both round P and the output to bf16: 2 * (2^-8 + 2^-8) of the largest value weighted, and as much
+        # again for rotated keys that round differently (the ring's products are rounded apart)
+        assert float((got.float() - want.float()).abs().max()) <= 2e-2
+        assert float((l2 - lse).abs().max()) <= 1e-2
+    cache.close()
+
+
+@pytest.mark.parametrize("kind", ["decode", "prompt", "prefix"])
+def test_captured_calls_see_each_replays_lengths(kind):
+    lens = [(1, 100), (1, 20)] if kind != "prompt" else [(40, 100), (40, 40)]
+    bt = Batch(45, [(a, n + 60) for a, n in lens], 8, 2, 128, 16, spare=8)
+    table = torch.tensor(bt.free[:5], dtype=torch.int32, device="cuda")
+    j = torch.arange(70, device="cuda")
+    for pool in (bt.k_pages, bt.v_pages):
+        pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, 70, 2, 128)
+    max_q = lens[0][0]
+
+    def call():
+        if kind == "prefix":
+            return paged.prefix_attention(*bt.args()[:3], table, 70, *bt.args()[3:], max_q=max_q, return_lse=True)
+        return paged.paged_attention(*bt.args(), max_q=max_q, return_lse=True)
+
+    call()
+    graphs = []
+    for _ in range(2):  # two graphs of one call share nothing
+        gr = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(gr):
+            got = call()
+        graphs.append((gr, got))
+    for extra in (0, 7, 60):
+        now = [(a, n + extra) for a, n in lens]
+        bt.kv_len.copy_(torch.tensor([n for _, n in now], dtype=torch.int32))
+        bt.q.copy_(randn(bt.gen, *bt.q.shape))
+        bt.lens = now
+        torch.cuda.synchronize()
+        side = torch.cuda.Stream()
+        graphs[0][0].replay()
+        with torch.cuda.stream(side):
+            graphs[1][0].replay()
+        torch.cuda.synchronize()
+        for _, got in graphs:
+            assert_attend(got, bt, **(dict(prefix=(table, 70)) if kind == "prefix" else {}))
+
+
+def test_captured_append_and_rotation():
+    bt = Batch(46, [(1, 30), (1, 90)], 4, 2, 64, 16, fill=0.0)
+    k, v = randn(bt.gen, 2, 2, 64), randn(bt.gen, 2, 2, 64)
+    tables = paged.rope_tables((200,), (32,))
+    pos = torch.tensor([[29], [89]], dtype=torch.int32, device="cuda")
+    paged.paged_append(bt.q, k, v, bt.k_pages, bt.v_pages, bt.cu_q, bt.kv_len, bt.page_table, pos=pos, tables=tables)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = paged.paged_append(bt.q, k, v, bt.k_pages, bt.v_pages, bt.cu_q, bt.kv_len, bt.page_table, pos=pos,
+                                 tables=tables)
+    for n in (17, 55):
+        k.copy_(randn(bt.gen, 2, 2, 64))
+        bt.kv_len.fill_(n)
+        pos.fill_(n - 1)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert_turned(out, bt.q, pos, tables, False)
+        for b in range(2):
+            pg = int(bt.page_table[b, (n - 1) // 16])
+            if pg >= 0:
+                assert_turned(bt.k_pages[pg, :, (n - 1) % 16][None], k[b:b + 1], pos[b:b + 1], tables, False)
+    paged_status_or_clear()
+
+
+def paged_status_or_clear():
+    try:
+        paged.device_status()
+    except B.RcError:
+        pass  # sequence 0 has no page for 55 tokens: that is reported, and kept out
+
+
+def test_rotation_gradient_captured_into_a_graph():
+    g = generator(47)
+    tables = paged.rope_tables((50,), (64,))
+    pos = _positions(g, 20, (50,))
+    x = randn(g, 20, 3, 128, dtype=F32).requires_grad_(True)
+    gy = randn(g, 20, 3, 128, dtype=F32)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):  # warm-up as graphs ask for
+        for _ in range(2):
+            torch.autograd.grad(paged.rope_axes(x, pos, tables), (x,), gy)
+    torch.cuda.current_stream().wait_stream(side)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        (dx,) = torch.autograd.grad(paged.rope_axes(x, pos, tables), (x,), gy)
+    gy.copy_(randn(g, 20, 3, 128, dtype=F32))
+    gr.replay()
+    torch.cuda.synchronize()
+    assert_turned(dx, gy, pos, tables, False, inverse=True)
+
+
+def test_two_streams_and_two_threads_at_once():
+    import threading
+    batches = [Batch(50 + i, [(1, 900 + 100 * i), (1, 40)] * 6, 8, 2, 128, 16) for i in range(2)]
+    batches += [Batch(60 + i, [(130, 400), (31, 31)], 8, 2, 128, 16) for i in range(2)]
+    want = [paged.paged_attention(*b.args(), max_q=max(a for a, _ in b.lens)) for b in batches]
+    torch.cuda.synchronize()
+    errors = []
+
+    def work(b, w):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = paged.paged_attention(*b.args(), max_q=max(a for a, _ in b.lens))
+                    torch.cuda.current_stream().synchronize()
+                    if not torch.equal(got, w):
+                        errors.append("differs")
+        except Exception as e:  # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=x) for x in zip(batches, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=300)
+    assert not errors, errors
+
+
+def test_refusals_on_the_device():
+    bt = Batch(70, [(1, 30)], 4, 2, 64, 16)
+    q, k_pages, v_pages, cu, kv, table = bt.args()
+    bad = [
+        dict(q=q[:, :, ::2]), dict(q=q.float()), dict(q=q[:, :3]), dict(cu_q=cu.long()), dict(kv_len=kv[:0]),
+        dict(page_table=table[0]), dict(v_pages=v_pages[:, :1]), dict(q=q.cpu()), dict(q=q.half()),
+        dict(out=torch.empty_like(q)[:, :2]), dict(scale=0.0), dict(scale=-1.0), dict(frame_seqlen=0),
+        dict(max_q=-1), dict(max_q=2 ** 31), dict(q=q[..., :32]), dict(q=q.expand(1, 4, 64)[:, :1].expand(1, 4, 64)),
+    ]
+    for over in bad:
+        args = dict(q=q, k_pages=k_pages, v_pages=v_pages, cu_q=cu, kv_len=kv, page_table=table, max_q=1)
+        args.update(over)
+        with pytest.raises((ValueError, B.RcError)):
+            paged.paged_attention(**args)
+    with pytest.raises(ValueError):
+        paged.paged_attention(q.requires_grad_(True), k_pages, v_pages, cu, kv, table)
+    q.requires_grad_(False)
+    with pytest.raises(ValueError):
+        paged.prefix_attention(q, k_pages, v_pages, table[0], 0, cu, kv, table)
+    with pytest.raises(B.RcError):
+        paged.prefix_attention(q, k_pages, v_pages, table[0][:1].contiguous(), 17, cu, kv, table)
+    k = randn(bt.gen, 1, 2, 64)
+    with pytest.raises(ValueError):
+        paged.paged_append(q, k, k, k_pages, v_pages, cu, kv, table, pos=torch.zeros(1, 1, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ValueError):
+        paged.paged_append(q, k, k.half(), k_pages, v_pages, cu, kv, table)
+    with pytest.raises(ValueError):
+        paged.paged_append(None, k, k, k_pages, v_pages, cu, kv, table, q_out=q)
+    tables = paged.rope_tables((9,), (32,))
+    pos = torch.zeros(1, 1, dtype=torch.int32, device="cuda")
+    for args in [(q, pos.long(), tables), (q, pos[:0], tables), (q, pos, tables + tables), (q.long(), pos, tables),
+                 (q[0], pos, tables), ((q, k, k), pos, tables), (q, pos, (tables[0].half(),))]:
+        with pytest.raises((ValueError, B.RcError)):
+            paged.rope_axes(*args)
+    with pytest.raises(ValueError):
+        paged.rope_axes(q, pos, tables, pairing="quarter")
+    # a slice that starts off a 16-byte boundary
+    with pytest.raises(B.RcError):
+        paged.rope_axes(torch.zeros(1 * 4 * 64 + 1, dtype=BF16, device="cuda")[1:].view(1, 4, 64), pos, tables)
+
+
+def test_an_empty_batch():
+    bt = Batch(71, [(1, 30)], 4, 2, 64, 16)
+    none = torch.empty((0, 4, 64), dtype=BF16, device="cuda")
+    cu, kv, table = torch.zeros(1, dtype=torch.int32, device="cuda"), bt.kv_len[:0], bt.page_table[:0]
+    assert paged.paged_attention(none, bt.k_pages, bt.v_pages, cu, kv, table).shape == (0, 4, 64)
+    k = none[:, :2]
+    assert paged.paged_append(none, k, k, bt.k_pages, bt.v_pages, cu, kv, table).shape == (0, 4, 64)
+    # tokens, but no sequence: nothing is written
+    out = torch.full((3, 4, 64), 7.0, dtype=BF16, device="cuda")
+    paged.paged_attention(torch.zeros_like(out), bt.k_pages, bt.v_pages, cu, kv, table, out=out)
+    assert bool((out == 7).all())
+
+
+def test_a_pool_past_32_bit_offsets():
+    """Pages whose offsets in bytes and in elements pass 2^32: the first and the last of 9 GB."""
+    hk, d, page = 8, 128, 128
+    n = (9 * 2 ** 30) // (hk * page * d * 2)
+    pool = torch.empty((n, hk, page, d), dtype=BF16, device="cuda")
+    g = generator(72)
+    table = torch.tensor([[n - 1, 0, n - 2, 3]], dtype=torch.int32, device="cuda")
+    for i in table[0].tolist():
+        pool[i] = randn(g, hk, page, d)
+    for a in (1, 60):
+        bt = Batch.__new__(Batch)
+        bt.lens, bt.hq, bt.hk, bt.d, bt.page, bt.dtype, bt.cu, bt.n_tok = [(a, 500)], 16, hk, d, page, BF16, [0, a], a
+        bt.q, bt.k_pages, bt.v_pages, bt.page_table = randn(g, a, 16, d), pool, pool, table
+        bt.cu_q = torch.tensor([0, a], dtype=torch.int32, device="cuda")
+        bt.kv_len = torch.tensor([500], dtype=torch.int32, device="cuda")
+        assert_attend(paged.paged_attention(*bt.args(), max_q=a, return_lse=True), bt)
+    k, v = randn(g, 1, hk, d), randn(g, 1, hk, d)
+    kv = torch.tensor([1], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    v_pool = torch.empty_like(pool)
+    paged.paged_append(None, k, v, pool, v_pool, cu, kv, table)
+    assert torch.equal(pool[n - 1, :, 0], k[0]) and torch.equal(v_pool[n - 1, :, 0], v[0])
+
+
+@pytest.mark.parametrize("max_q", [1, 50])
+def test_keys_of_one_stream_do_not_reach_another(max_q):
+    """Infinities and NaN in one stream's pages leave the other's result as it was."""
+    lens = [(max_q, 200), (max_q, 333)]
+    a, b = (Batch(73, lens, 4, 2, 64, 16, fill=0.0) for _ in range(2))
+    own = b.page_table[1][:21].long()
+    b.k_pages[own] = float("inf")
+    b.v_pages[own] = float("nan")
+    x = paged.paged_attention(*a.args(), max_q=max_q)
+    y = paged.paged_attention(*b.args(), max_q=max_q)
+    assert torch.equal(x[:max_q], y[:max_q]) and bool(y[max_q:].isnan().any())
+
+
+def test_thousands_of_sequences():
+    """The most sequences of a call, in both kernels; more units than whole rounds are planned for in one of them."""
+    lens = [(1 + i % 2, 1 + i * 7 % 30 + i % 2) for i in range(4096)]
+    bt = Batch(74, lens, 24, 3, 64, 16)
+    a, la = paged.paged_attention(*bt.args(), max_q=2, return_lse=True)
+    b, lb = paged.paged_attention(*bt.args(), max_q=17, return_lse=True)
+    sample = Batch.__new__(Batch)
+    sample.__dict__.update(bt.__dict__)
+    pick = [0, 1, 511, 512, 513, 2000, 4094, 4095]
+    sample.lens = [lens[i] for i in pick]
+    rows = [r for i in pick for r in range(bt.cu[i], bt.cu[i + 1])]
+    sample.cu = [0]
+    for q, _ in sample.lens:
+        sample.cu.append(sample.cu[-1] + q)
+    sample.n_tok, sample.q, sample.page_table = len(rows), bt.q[rows], bt.page_table[pick]
+    for o, lse in ((a, la), (b, lb)):
+        assert_attend((o[rows], lse[:, rows]), sample)
+    # everywhere else the two differ by no more than both bounds allow a value of the largest magnitude
+    most = float(bt.v_pages[~bt.v_pages.isnan()].abs().max())
+    assert float((a.float() - b.float()).abs().max()) <= 4 * 2.0 ** -8 * 2 * most
+    assert float((la - lb).abs().max()) <= 2.0 ** -10
+    more = torch.zeros(4098, dtype=torch.int32, device="cuda")
+    with pytest.raises(B.RcError):
+        paged.paged_attention(bt.q[:1], bt.k_pages, bt.v_pages, more, more[:-1], bt.page_table[:1].expand(4097, -1))
+
+
+@pytest.mark.parametrize("max_q", [1, 70])
+def test_in_place_and_a_table_row_shared_by_all(max_q):
+    bt = Batch(75, [(max_q, 300)] * 3, 8, 2, 128, 16)
+    bt.page_table = bt.page_table[:1].expand(3, -1)  # stride 0
+    want, wl = paged.paged_attention(*bt.args(), max_q=max_q, return_lse=True)
+    assert_attend((want, wl), bt)
+    q = bt.q.clone()
+    got = paged.paged_attention(q, *bt.args()[1:], max_q=max_q, out=q)
+    assert got is q and torch.equal(q, want)
+
+
+def test_queries_that_see_only_the_prefix():
+    """kv_len 0 and a table without columns: the sequences' own tokens are none."""
+    for a, hq in ((1, 8), (300, 2), (30, 8)):
+        bt = Batch(76, [(a, 0)] * 2, hq, 2, 64, 16, spare=9)
+        bt.page_table = bt.page_table[:, :0]
+        table = torch.tensor(bt.free[:8], dtype=torch.int32, device="cuda")
+        j = torch.arange(120, device="cuda")
+        for pool in (bt.k_pages, bt.v_pages):
+            pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, 120, 2, 64)
+        got = paged.prefix_attention(*bt.args()[:3], table, 120, *bt.args()[3:], max_q=a, return_lse=True)
+        bt.page_table = torch.zeros(2, 1, dtype=torch.int32, device="cuda")
+        assert_attend(got, bt, prefix=(table, 120))
+
+
+def test_lengths_past_the_table_are_cut_and_reported():
+    bt = Batch(77, [(1, 40), (1, 9)], 4, 2, 64, 16)
+    bt.page_table = bt.page_table[:, :3].contiguous()
+    want, wl = paged.paged_attention(*bt.args(), max_q=1, return_lse=True)
+    bt.kv_len = torch.tensor([49, 9], dtype=torch.int32, device="cuda")  # 48 places
+    long = torch.tensor([2 ** 31 - 1, -4], dtype=torch.int32, device="cuda")
+    for kv in (bt.kv_len, long):
+        for max_q in (1, 20):
+            paged.paged_attention(bt.q, bt.k_pages, bt.v_pages, bt.cu_q, kv, bt.page_table, max_q=max_q)
+            with pytest.raises(B.RcError) as e:
+                paged.device_status()
+            assert e.value.status == B.RC_ERANGE
+    again, al = paged.paged_attention(bt.q, bt.k_pages, bt.v_pages, bt.cu_q,
+                                      torch.tensor([40, 9], dtype=torch.int32, device="cuda"), bt.page_table, max_q=1,
+                                      return_lse=True)
+    assert torch.equal(again, want) and torch.equal(al, wl)
+
+
+def test_rows_listed_out_of_order_fault_nothing():
+    """cu_q that descends or passes the tokens: brought into range and reported."""
+    bt = Batch(78, [(2, 40), (3, 30), (1, 9)], 4, 2, 64, 16)
+    for cu in ([0, 5, 2, 6], [0, 2, 500, 6], [-3, 2, 5, 6], [4, 4, 4, 2 ** 31 - 1]):
+        t = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        for max_q in (3, 20):
+            paged.paged_attention(bt.q, bt.k_pages, bt.v_pages, t, bt.kv_len, bt.page_table, max_q=max_q)
+            with pytest.raises(B.RcError) as e:
+                paged.device_status()
+            assert e.value.status == B.RC_ERANGE
+        k = randn(bt.gen, bt.n_tok, 2, 64)
+        paged.paged_append(None, k, k, bt.k_pages, bt.v_pages, t, bt.kv_len, bt.page_table)
+        torch.cuda.synchronize()
+    try:
+        paged.device_status()  # some of these give a token a place that is none
+    except B.RcError:
+        pass
