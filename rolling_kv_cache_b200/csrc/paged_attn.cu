@@ -31,10 +31,9 @@
 // average (units differ in length: ragged batches, causal and window masks).
 // A unit cut between CTAs leaves its parts for the combine kernel.
 //
-// Keys that no query of the pair sees (behind the sequence, before its windows)
-// are masked in S (-inf, written back to TMEM by a tile's softmax warps before
-// they use it, in boundary tiles only), and their V rows are zeroed in shared
-// memory before the product, so that what their bits hold stays out; pages that are none are
+// Keys that a query does not see are masked in S (-inf, written back to TMEM by a tile's softmax warps before
+// they use it, in boundary tiles only); V rows behind the sequence or before the
+// pair's windows are zeroed in shared memory before the product, so that what their bits hold stays out; pages that are none are
 // filled with zeros by an out-of-range copy and masked.
 //
 // Every wait is bounded (2 s) and reports RC_ETIMEOUT through the status
@@ -348,32 +347,36 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
 // not the tile loop's.
 
 // -inf over the scores of one row's 64 keys from h0 on (TMEM columns tS ..)
-// that the row does not see or whose page is none.
-__device__ __noinline__ void mask_scores(uint32_t tS, int h0, RowMask rm, int sink, uint32_t pages, int page_log2) {
+// that the row does not see or whose page is none; returns the largest other score.
+__device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int sink, uint32_t pages, int page_log2) {
   auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
   unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
   const int step = min(64, 1 << page_log2);
   for (int k = 0; k < 64; k += step)
     if (!((pages >> (k >> page_log2)) & 1)) v &= ~(below(step) << k);
+  float mx = -INFINITY;
 #pragma unroll 1
   for (int cc = 0; cc < 2; ++cc) {
     const uint32_t vis = (uint32_t)(v >> (32 * cc));
-    if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
     uint32_t r[32];
     ptx::tmem_ld32(tS + cc * 32, r);
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
-    ptx::tmem_st32(tS + cc * 32, r);
+    for (int k = 0; k < 32; ++k) {
+      r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
+      mx = fmaxf(mx, __uint_as_float(r[k]));
+    }
+    if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) ptx::tmem_st32(tS + cc * 32, r);
   }
   ptx::tmem_st_wait();
+  return mx;
 }
 
-// Zeros the V rows of a tile (from key t0 on, one row to two threads) that no query of the pair sees.
+// Zeros the V rows of a tile (from key t0 on, one row to two threads) outside [lo, hi) and the sinks.
 template <int D>
-__device__ __noinline__ void zero_values(uint8_t* v, int t0, int lo_min, int hi_max, int sink) {
+__device__ __noinline__ void zero_values(uint8_t* v, int t0, int lo, int hi, int sink) {
   const int row = (int)threadIdx.x >> 1, key = t0 + row;
-  if (!(key < hi_max && (key >= lo_min || key < sink))) {
+  if (!(key < hi && (key >= lo || key < sink))) {
     uint8_t* dst = v + row * 128 + (threadIdx.x & 1) * 64;
 #pragma unroll
     for (int k = 0; k < PreLayout<D>::kSub; ++k)
@@ -392,8 +395,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       bar_fin, bar_pair[8];
   __shared__ float swap_buf[2][2][2][kTileRows];  // [group][exchange parity][column half][row]
   // what the softmax has to know of tile g, at g % 4: its first key, its pages
-  // that are there (a bit each), whether every query sees all of it, whether some V
-  // rows are seen by none
+  // that are there (a bit each), whether every query sees all of it, whether it has V
+  // rows behind the sequence or before the pair's windows
   __shared__ int4 tile_info[4];
   // the units' descriptions, written by the producer (which alone walks the
   // schedule: the walk's state in 18 warps' local memory would not fit L1)
@@ -532,7 +535,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         const int t0 = jb.sp.key(j - jb.lead), t1 = t0 + kTileRows;
         const bool in_sink = p.mask.window > 0 && t1 <= p.mask.sink_tok;
         info = make_int4(t0, (int)pages, t1 <= jb.sp.hi_min && (t0 >= jb.sp.lo_max || in_sink) && all,
-                         !(t1 <= jb.sp.hi_max && (t0 >= jb.sp.lo_min || in_sink)));
+                         !(t1 <= jb.L && (t0 >= jb.sp.lo_min || in_sink)));
       }
       if (fresh) {
         ok = nq == 0 || ptx::mbar_wait(&bar_qe, (nq - 1) & 1, abort, p.status, RC_ETIMEOUT);
@@ -714,7 +717,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         ptx::tc_fence_after();
         const int4 info = tile_info[gt & 3];
-        if (!info.z) {
+        uint32_t ra[32];
+        float mx = -INFINITY;
+        if (info.z) {
+          // S in halves, read again for the exponentials: 32 scores at a time leave
+          // the loop's state in registers
+          ptx::tmem_ld32(tS, ra);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+          ptx::tmem_ld32(tS + 32, ra);
+          ptx::tmem_ld_wait();
+#pragma unroll
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+        } else {
           // some key of the tile is hidden from some row: those scores become
           // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
           // query take the widest mask
@@ -723,21 +739,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           const bool lead = info.y & kLeadTile;
           if (lead) rm = RowMask{0, p.lead_len};
           else if (row < tpt * p.G && qi < jb.tokens) rm = row_mask(p.mask, jb.at0 + qi, jb.L);
-          mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 && !lead ? p.mask.sink_tok : 0,
-                      (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
+          mx = mask_scores(tS, info.x + ch * 64, rm, p.mask.window > 0 && !lead ? p.mask.sink_tok : 0,
+                           (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
         }
-        // S in halves, read again for the exponentials: 32 scores at a time leave
-        // the loop's state in registers
-        uint32_t ra[32];
-        float mx = -INFINITY;
-        ptx::tmem_ld32(tS, ra);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
-        ptx::tmem_ld32(tS + 32, ra);
-        ptx::tmem_ld_wait();
-#pragma unroll
-        for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
         float mo;
         if (!swap(mx, mo)) { ok = false; break; }
         const float m_new = ptx::fmax3(m, mx, mo);
@@ -795,13 +799,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         emit(ra, 32);
         ptx::tmem_st_wait();
         l += sum;
-        // V rows that no query of the pair sees: zero, before group 0's P lets the product start
+        // V rows behind the sequence or before the windows may hold anything: zero, before group 0's P lets the
+        // product start (a key that only later queries see is data, and meets P = 0)
         if (grp == 0 && tile_info[gt & 3].w) {
           const int st = gt & 1;
           if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
           const int4 info = tile_info[gt & 3];
           const bool lead = info.y & kLeadTile;
-          zero_values<D>(base + L::kV + st * L::kTile, info.x, lead ? 0 : jb.lo_min, lead ? p.lead_len : jb.hi_max,
+          zero_values<D>(base + L::kV + st * L::kTile, info.x, lead ? 0 : jb.lo_min, lead ? p.lead_len : jb.L,
                          p.mask.window > 0 && !lead ? p.mask.sink_tok : 0);
         }
         ptx::tc_fence_before();
@@ -840,6 +845,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         dst = p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + ch * D;
         dst_lse = p.lse ? p.lse + (size_t)head * p.n_tok + tok : nullptr;
       }
+      // the job's words are read: its slot is free (before the stores, which an
+      // arrive behind them would wait for)
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
       if (live && ch == 0 && dst_lse) *dst_lse = f32 ? lse2 : lse2 * 0.69314718055994531f;
 #pragma unroll 4
       for (int cc = 0; cc < D / 2; cc += 16) {
@@ -864,8 +873,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
                 make_uint4(pair(8 * k), pair(8 * k + 2), pair(8 * k + 4), pair(8 * k + 6));
         }
       }
-      __syncwarp();
-      if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
       if (!ok) break;
     }
   }
