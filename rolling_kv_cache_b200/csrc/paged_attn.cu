@@ -845,6 +845,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         dst = p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + ch * D;
         dst_lse = p.lse ? p.lse + (size_t)head * p.n_tok + tok : nullptr;
       }
+      const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // fp32 rows always are
       // the job's words are read: its slot is free (before the stores, which an
       // arrive behind them would wait for)
       __syncwarp();
@@ -862,15 +863,23 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         for (int k = 0; k < 16; ++k) o[k] = a != 0.f ? __float_as_uint(__uint_as_float(o[k]) * a) : 0u;
         if (f32) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            *reinterpret_cast<uint4*>(dst + cc * 4 + 16 * k) =
-                make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        } else {
-          auto pair = [&](int e) { return ptx::pack16x2<BF16>(__uint_as_float(o[e]), __uint_as_float(o[e + 1])); };
+          for (int k = 0; k < 2; ++k) {
+            uint32_t y[8];
 #pragma unroll
-          for (int k = 0; k < 2; ++k)
-            *reinterpret_cast<uint4*>(dst + cc * 2 + 16 * k) =
-                make_uint4(pair(8 * k), pair(8 * k + 2), pair(8 * k + 4), pair(8 * k + 6));
+            for (int e = 0; e < 8; ++e) y[e] = o[8 * k + e];
+            ptx::stg8(dst + cc * 4 + 32 * k, y);
+          }
+        } else {
+          uint32_t y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            y[e] = ptx::pack16x2<BF16>(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          if (wide) {
+            ptx::stg8(dst + cc * 2, y);
+          } else {
+            *reinterpret_cast<uint4*>(dst + cc * 2) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(dst + cc * 2 + 16) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
         }
       }
       if (!ok) break;

@@ -311,6 +311,16 @@ __device__ __forceinline__ void discard_l2(const void* p) {
       : "memory");
 }
 
+// 32 bytes in one store (p 32-byte aligned, global memory).
+__device__ __forceinline__ void stg8(void* p, const uint32_t (&r)[8]) {
+  asm volatile(
+      "{\n\t.reg .u64 g;\n\t"
+      "cvta.to.global.u64 g, %0;\n\t"
+      "st.global.v8.b32 [g], {%1, %2, %3, %4, %5, %6, %7, %8};\n\t}" ::"l"(p),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+      : "memory");
+}
+
 // Two fp32 lanes in one instruction (sm_100 packed f32x2 forms).
 __device__ __forceinline__ float2 ffma2(float2 a, float2 b, float2 c) {
   float2 d;
