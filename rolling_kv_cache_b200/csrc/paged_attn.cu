@@ -81,7 +81,6 @@ struct Job {
   int tokens, at0;   // queries of the pair, position of the first
   int L, kv_lo, kv_hi, slot;
   bool has1, head, tail;  // head: begins inside the unit; tail: ends inside it
-  int place;              // h * pairs + pair
   int lead, total;        // tiles of the prefix that it walks first, and in all
   TileSpan<kTileRows> sp;
 };
@@ -209,7 +208,6 @@ struct PairWalk {
     j.head = lo > 0;
     j.tail = lo + len < max(j.total, 1);
     j.slot = j.head ? 2 * (int)blockIdx.x : (j.tail ? 2 * (int)blockIdx.x + 1 : -1);
-    j.place = h * pairs + pair;
   }
 };
 
@@ -456,7 +454,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       ptx::tma_prefetch_desc(&p.tm_v);
     }
     int nq = 0, g = 0, nw = 0;
-    PartRecord rec = make_int4(0, 0, -1, 0);
+    PartRecord rec = make_int4(0, 0, 0, 0);
     PairWalk walk;
     walk.init(p, plan);
     Job jb;
@@ -492,13 +490,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           return false;
         }
         if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-        if (jb.head) {
-          rec.x = 1;
-          rec.y = !jb.tail;
-        } else if (jb.tail) {
-          rec.z = jb.b;
-          rec.w = jb.place;
-        }
+        if (jb.head) rec.x = kHasHead | (jb.tail ? 0 : kHeadEnds);
+        else if (jb.tail) rec = make_int4(rec.x, jb.q0, jb.tokens, jb.h * p.G);
         j = jb.kv_lo;
         n = jb.kv_hi;
         fresh = true;

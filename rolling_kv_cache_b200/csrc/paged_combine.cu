@@ -45,50 +45,37 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
   constexpr int kChunks = D / 8;
   constexpr int kUnitRows = DECODE ? kDecodeRows : kPrefillRows;
   constexpr int kRows = 16;
-  __shared__ int last_sh;
+  constexpr int kEarly = kCombThreads / kRows;
+  __shared__ int last_sh, flags_sh[kCombThreads];
   __shared__ float weight[kMaxPersistentCtas][kRows];
+  static_assert(kMaxPersistentCtas <= kCombThreads, "a thread a CTA");
   __shared__ float lse_sh[kRows];
   __shared__ float so[kCombThreads][9];
-  const int tid = threadIdx.x, c = blockIdx.x;
+  const int tid = threadIdx.x, c = blockIdx.x, row_lo = blockIdx.y * kRows;
   if (tid == 0) last_sh = p.n_ctas - 1;
+  auto part_row = [&](int i) { return (size_t)(2 * (c + i) + (i == 0)) * kUnitRows + row_lo; };
   ptx::grid_wait();
   // records and parts come from L2 (ld.cg): this block's SM may have cached
-  // their addresses before the attention kernel wrote them
+  // their addresses before the attention kernel wrote them. The first parts'
+  // log-sum-exps are asked for along with the records, before it is known which of them exist
   const PartRecord rec = __ldcg(p.rec + c);
-  if (rec.z < 0 || rec.z >= p.b.n_seqs) return;
+  const int ahead = c + 1 + tid < p.n_ctas ? __ldcg(&p.rec[c + 1 + tid].x) : 0;
+  float early = 0.f;
+  if (tid < kEarly * kRows && c + tid / kRows < p.n_ctas) early = __ldcg(p.part_lse + part_row(tid / kRows) + tid % kRows);
+  if (rec.z <= 0) return;
+  flags_sh[tid] = ahead;
   __syncthreads();
-  for (int i = c + 1 + tid; i < p.n_ctas; i += kCombThreads)
-    if (__ldcg(&p.rec[i].y)) atomicMin(&last_sh, i);
-  // the unit's rows
-  int n_rows, head0, pair = 0;
-  Seq s;
-  if constexpr (DECODE) {
-    s = load_seq(p.b, p.n_tok, rec.z);
-    n_rows = min(s.n, 16 / p.G) * p.G;
-    head0 = rec.w * p.G;
-  } else {
-    if (p.batch_pass) {
-      s.q0 = 0;
-      s.n = min(max(__ldg(p.b.cu_q + p.b.n_seqs), 0), p.n_tok);
-    } else {
-      s = load_seq(p.b, p.n_tok, rec.z);
-    }
-    const int tpt = 128 / p.G, pairs = max((s.n + 2 * tpt - 1) / (2 * tpt), 1);
-    pair = rec.w % pairs;
-    head0 = rec.w / pairs * p.G;
-    n_rows = kUnitRows;
-  }
+  if (ahead & kHeadEnds) atomicMin(&last_sh, c + 1 + tid);
+  const int n_rows = DECODE ? rec.z * p.G : kUnitRows, head0 = rec.w;
   __syncthreads();
   const int parts = last_sh - c + 1;
-  const int row_lo = blockIdx.y * kRows;
   const int rows = min(kRows, n_rows - row_lo);
   if (rows <= 0) return;
-  auto part_row = [&](int i) { return (size_t)(2 * (c + i) + (i == 0)) * kUnitRows + row_lo; };
   for (int x = tid; x < parts * kRows; x += kCombThreads) {
     const int i = x / kRows, r = x % kRows;
     // a CTA whose range is empty left no part
-    const bool there = r < rows && (i == 0 || __ldcg(&p.rec[c + i].x));
-    weight[i][r] = there ? __ldcg(p.part_lse + part_row(i) + r) : -INFINITY;
+    const bool there = r < rows && (i == 0 || (flags_sh[i - 1] & kHasHead));
+    weight[i][r] = !there ? -INFINITY : (x < kEarly * kRows ? early : __ldcg(p.part_lse + part_row(i) + r));
   }
   __syncthreads();
   normalise(weight, parts, rows, lse_sh);
@@ -131,11 +118,11 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
       h = row - i * p.G;
     } else {
       const int tpt = 128 / p.G, rr = row & 127;
-      i = (pair * 2 + (row >> 7)) * tpt + rr / p.G;
+      i = (row >> 7) * tpt + rr / p.G;
       h = rr % p.G;
-      if (rr >= tpt * p.G || i >= s.n) continue;
+      if (rr >= tpt * p.G || i >= rec.z) continue;
     }
-    store_row<D, BF16>(to, s.q0 + i, head0 + h, col, acc, lse_sh[r]);
+    store_row<D, BF16>(to, rec.y + i, head0 + h, col, acc, lse_sh[r]);
   }
 }
 
@@ -166,7 +153,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   __shared__ int first_sh[3], last_sh[3];  // the decode unit's, and the first and last token's pair's
   __shared__ float scratch[kJoinSources * kDecodeRows];  // small enough to be resident beside the attention kernels
   __shared__ float lse_sh[kDecodeRows];
-  __shared__ uint8_t there[2][kMaxPersistentCtas];  // a CTA's record: bit 0 it holds a unit's later part, bit 1 the last
+  __shared__ uint8_t there[2][kMaxPersistentCtas];  // the CTAs' records' flags
   float(*weight)[kDecodeRows] = reinterpret_cast<float(*)[kDecodeRows]>(scratch);
   float(*so)[9] = reinterpret_cast<float(*)[9]>(scratch);  // after the weights
   static_assert(kCombThreads * 9 <= kJoinSources * kDecodeRows, "the sums fit");
@@ -175,8 +162,6 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   const Seq s = load_seq(p.b, p.n_tok, b);
   const int R = min(s.n, 16 / p.G) * p.G, heads = p.Hk * p.G;
   const int per_pair = 2 * (128 / p.G);
-  const int total = min(max(__ldg(p.b.cu_q + p.b.n_seqs), 0), p.n_tok);
-  const int pairs = (total + per_pair - 1) / per_pair;
   const int pair0 = s.q0 / per_pair, pair1 = R > 0 ? (s.q0 + R / p.G - 1) / per_pair : pair0;
   if (tid < 3) {
     first_sh[tid] = -1;
@@ -187,16 +172,16 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   __syncthreads();
   for (int c = tid; c < p.n_ctas; c += kCombThreads) {
     const int4 x = __ldcg(p.own.rec + c), y = __ldcg(p.pre.rec + c);
-    if (x.z == b && x.w == h) first_sh[0] = c;
-    if (y.z >= 0 && y.w == h * pairs + pair0) first_sh[1] = c;
-    if (y.z >= 0 && y.w == h * pairs + pair1) first_sh[2] = c;
-    there[0][c] = (x.x ? 1 : 0) | (x.y ? 2 : 0);
-    there[1][c] = (y.x ? 1 : 0) | (y.y ? 2 : 0);
+    if (x.z > 0 && x.y == s.q0 && x.w == h * p.G) first_sh[0] = c;
+    if (y.z > 0 && y.y == pair0 * per_pair && y.w == h * p.G) first_sh[1] = c;
+    if (y.z > 0 && y.y == pair1 * per_pair && y.w == h * p.G) first_sh[2] = c;
+    there[0][c] = x.x;
+    there[1][c] = y.x;
   }
   __syncthreads();
   for (int c = tid; c < p.n_ctas; c += kCombThreads)
     for (int k = 0; k < 3; ++k)
-      if (first_sh[k] >= 0 && c > first_sh[k] && (there[k > 0][c] & 2)) atomicMin(&last_sh[k], c);
+      if (first_sh[k] >= 0 && c > first_sh[k] && (there[k > 0][c] & kHeadEnds)) atomicMin(&last_sh[k], c);
   __syncthreads();
   const int n_own = first_sh[0] < 0 ? 1 : last_sh[0] - first_sh[0] + 1;
   const int n_pre0 = first_sh[1] < 0 ? 1 : last_sh[1] - first_sh[1] + 1;
@@ -216,7 +201,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
       return side.lse + (size_t)head * p.n_tok + tok;
     }
     const int c = first_sh[k] + e;
-    if (c > last_sh[k] || (e > 0 && !(there[!own][c] & 1))) return nullptr;
+    if (c > last_sh[k] || (e > 0 && !(there[!own][c] & kHasHead))) return nullptr;
     const int in_pair = tok % per_pair, tile = in_pair / (per_pair / 2);
     const int row = own ? r : tile * 128 + (in_pair - tile * (per_pair / 2)) * p.G + r - i * p.G;
     const size_t at = (size_t)(2 * c + (e == 0)) * (own ? kDecodeRows : kPrefillRows) + row;

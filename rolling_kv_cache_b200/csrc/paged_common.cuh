@@ -67,12 +67,13 @@ __device__ __forceinline__ Seq load_seq(const BatchView& v, int n_tok, int b) {
   return s;
 }
 
-// What a CTA's stream-K range left in the partial rows. Slot 2c holds the
-// part of the unit its range begins inside (x: 1 if there is one, y: 1 if
-// that unit ends in the range); slot 2c + 1 the first part of a unit that
-// begins in the range and goes on in the next CTA's (z: its sequence, or -1;
-// w: its place within the sequence, kernel-defined).
+// What a CTA's range of tiles left in the partial rows. Slot 2c holds the part
+// of the unit its range begins inside (x: kHasHead if there is one, kHeadEnds if
+// that unit ends in the range); slot 2c + 1 the first part of a unit that begins
+// in the range and goes on in the next CTA's: rows [y, y + z) of q (z 0: there
+// is none) and query heads from w on.
 using PartRecord = int4;
+constexpr int kHasHead = 1, kHeadEnds = 2;
 
 // Exclusive prefix sums of f(0..n-1) into pre[0..n] (shared memory), by all
 // threads of the block.

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     const uint32_t dst0 = (is_v ? L::kTile : 0) + box * p.box_rows * 128 * L::kSub;
     int g = 0, j = 0, n = 0, k0 = 0, page = -1;
     bool want = false, ok = true;
-    PartRecord rec = make_int4(0, 0, -1, 0);
+    PartRecord rec = make_int4(0, 0, 0, 0);
     TileSpan<kTK> sp;
     // the next tile, with the load of its page entry under way
     auto advance = [&]() -> bool {
@@ -169,13 +169,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         const Seq s = load_seq(p.b, p.n_tok, u.b);
         sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
         if (lane == 0 && s.bad && !is_v && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-        if (u.lo > 0) {
-          rec.x = 1;
-          rec.y = u.hi == u.total;
-        } else if (u.hi < u.total) {
-          rec.z = u.b;
-          rec.w = u.h;
-        }
+        if (u.lo > 0) rec.x = kHasHead | (u.hi == u.total ? kHeadEnds : 0);
+        else if (u.hi < u.total) rec = make_int4(rec.x, s.q0, min(s.n, 16 / p.G), u.h * p.G);
         j = u.lo;
         n = min(u.hi, sp.n);
       }
