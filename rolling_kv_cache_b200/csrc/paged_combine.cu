@@ -187,31 +187,41 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   const int n_pre0 = first_sh[1] < 0 ? 1 : last_sh[1] - first_sh[1] + 1;
   const int n_pre1 = first_sh[2] < 0 ? 1 : last_sh[2] - first_sh[2] + 1;
   const int n = n_own + max(n_pre0, n_pre1);
-  // source e of row r: its values (or null: there is none) and its log-sum-exp
-  auto source = [&](int e, int r, const float** o) -> const float* {
-    const int i = r / p.G, tok = s.q0 + i, head = h * p.G + r - i * p.G;
-    const bool own = e < n_own;
-    const JoinSide& side = own ? p.own : p.pre;
-    const int k = own ? 0 : (tok / per_pair == pair0 ? 1 : 2);
-    if (!own) e -= n_own;
-    *o = nullptr;
-    if (first_sh[k] < 0) {
-      if (e > 0) return nullptr;
-      *o = side.o + ((size_t)tok * heads + head) * D;
-      return side.lse + (size_t)head * p.n_tok + tok;
-    }
-    const int c = first_sh[k] + e;
-    if (c > last_sh[k] || (e > 0 && !(there[!own][c] & kHasHead))) return nullptr;
-    const int in_pair = tok % per_pair, tile = in_pair / (per_pair / 2);
-    const int row = own ? r : tile * 128 + (in_pair - tile * (per_pair / 2)) * p.G + r - i * p.G;
-    const size_t at = (size_t)(2 * c + (e == 0)) * (own ? kDecodeRows : kPrefillRows) + row;
-    *o = side.part_o + at * D;
-    return side.part_lse + at;
+  // Row r's values and log-sum-exp on one side: whole (c < 0), or in the parts
+  // from CTA c on, whose slots lie `unit` rows apart.
+  struct Rows {
+    const float* o;
+    const float* l;
+    int c, last, unit;
   };
-  for (int x = tid; x < n * kDecodeRows; x += kCombThreads) {
-    const int e = x / kDecodeRows, r = x % kDecodeRows;
-    const float *o, *l = r < R ? source(e, r, &o) : nullptr;
-    weight[e][r] = l ? __ldcg(l) : -INFINITY;
+  auto rows_of = [&](int r, bool own) {
+    const int i = r / p.G, g = r - i * p.G, tok = s.q0 + i, head = h * p.G + g;
+    const JoinSide& side = own ? p.own : p.pre;
+    const int in_pair = tok % per_pair;
+    const int k = own ? 0 : (tok - in_pair == pair0 * per_pair ? 1 : 2);
+    Rows x;
+    x.c = first_sh[k];
+    x.last = last_sh[k];
+    x.unit = own ? kDecodeRows : kPrefillRows;
+    const int tpt = per_pair / 2, tile = in_pair >= tpt;
+    const size_t at = x.c < 0 ? (size_t)tok * heads + head
+                              : (size_t)(own ? r : tile * 128 + (in_pair - tile * tpt) * p.G + g);
+    x.o = (x.c < 0 ? side.o : side.part_o) + at * D;
+    x.l = x.c < 0 ? side.lse + (size_t)head * p.n_tok + tok : side.part_lse + at;
+    return x;
+  };
+  auto slot = [](const Rows& x, int e) { return x.c < 0 ? (size_t)0 : (size_t)(2 * (x.c + e) + (e == 0)) * x.unit; };
+  {
+    const int r = tid % kDecodeRows;  // the same for all of a thread's sources
+    const Rows own = rows_of(min(r, R - 1), true), pre = rows_of(min(r, R - 1), false);
+    for (int e = tid / kDecodeRows; e < n; e += kCombThreads / kDecodeRows) {
+      const bool mine = e < n_own;
+      const Rows& x = mine ? own : pre;
+      const int i = mine ? e : e - n_own;
+      // a CTA whose range is empty left no part
+      const bool is = r < R && (i == 0 || (x.c >= 0 && x.c + i <= x.last && (there[!mine][x.c + i] & kHasHead)));
+      weight[e][r] = is ? __ldcg(x.l + slot(x, i)) : -INFINITY;
+    }
   }
   __syncthreads();
   normalise(weight, n, R, lse_sh);
@@ -223,15 +233,14 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = 0.f;
   if (grp < groups) {
-    const float* first;
-    source(0, r, &first);
+    const Rows own = rows_of(r, true), pre = rows_of(r, false);
 #pragma unroll 4
     for (int e = grp; e < n; e += groups) {
       const float w = weight[e][r];
-      const float* o;
-      source(e, r, &o);
-      // nothing was written where the weight is 0: such a load goes to the first source
-      const float4* src = reinterpret_cast<const float4*>((w != 0.f ? o : first) + col);
+      const bool mine = e < n_own;
+      // nothing was written where the weight is 0: such a load goes to the side's first source
+      const int i = w != 0.f ? (mine ? e : e - n_own) : 0;
+      const float4* src = reinterpret_cast<const float4*>((mine ? own.o + slot(own, i) * D : pre.o + slot(pre, i) * D) + col);
       const float4 a = __ldcg(src), c = __ldcg(src + 1);
       const float x[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
 #pragma unroll
