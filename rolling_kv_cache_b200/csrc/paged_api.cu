@@ -196,7 +196,7 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   w->lead = m->prefix_len > 0 && !w->decode && (int64_t)n_tok >= (int64_t)per_pair * p->n_seqs;
   w->two_pass = m->prefix_len > 0 && !w->lead;
   // positions of the stream-K split are 32-bit: tiles of every unit, summed
-  const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 5;
+  const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 6;
   const int64_t pairs = (int64_t)n_tok / per_pair + p->n_seqs + 1;
   if ((w->decode ? tiles * p->n_seqs : tiles * pairs) * p->kv_heads >= INT_MAX)
     return SetLastError(RC_ERANGE, "the batch has too many key tiles for one call");

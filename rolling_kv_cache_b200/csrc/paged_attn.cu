@@ -53,6 +53,9 @@ constexpr int kMmaWarp = 17;
 constexpr int kPreThreads = 18 * 32;
 constexpr float kRescaleLog2 = 8.0f;
 constexpr int kMaxRounds = 64;
+// What a unit costs beside its tiles, in tiles (its queries, its first tile's
+// start and its last writes: 9000 cycles to a tile's 3850)
+constexpr int kPairCost = 2;
 constexpr int kPlanSeqs = 512;
 
 template <int D>
@@ -121,13 +124,15 @@ struct JobInfo {
 constexpr int kJobRing = 4;
 constexpr int kLeadTile = 1 << 16;  // in a tile's page bits: it is the prefix's
 
-// A unit, and a tile within it.
+// A unit, and a position within it: 0, or kPairCost + a tile after the first.
 struct Start {
   int b, h, pair, off;
 };
 
 // This CTA's work: `rounds` whole units from `whole` on, G apart, then the
-// tiles [pos, end) of the batch, which begin at `range`.
+// positions [pos, end) of the batch, which begin at `range`; a unit of n tiles
+// takes kPairCost + n. A bound that falls among a unit's cost is moved to the unit's
+// start, alike for the CTAs on both sides.
 struct Plan {
   Start whole, range;
   int rounds, pos, end;
@@ -190,8 +195,8 @@ struct PairWalk {
       }
     }
     pair_span(*p, s, pair, tpt, j);
-    const int len = min(max(j.total, 1) - off, end - pos);
-    fill(j, off, len);
+    const int len = min(max(j.total, 1) + kPairCost - off, end - pos), lo = max(off - kPairCost, 0);
+    fill(j, lo, off + len - kPairCost - lo);
     pos += len;
     off = 0;
     ++pair;
@@ -253,7 +258,7 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
     for (int q = lane; q < pairs; q += 32) {
       Job j;
       pair_span(p, s, q, tpt, j);
-      sum += max(j.total, 1);
+      sum += max(j.total, 1) + kPairCost;
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
@@ -277,7 +282,7 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
       const int first = pairs_of(before[b]);
       Job j;
       pair_span(p, seq(b), (u - p.Hk * first) % (pairs_of(before[b + 1]) - first), tpt, j);
-      loads[u] = max(j.total, 1);
+      loads[u] = max(j.total, 1) + kPairCost;
     }
     __syncthreads();
     if (tid < G) {
@@ -299,18 +304,21 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
     __syncthreads();
     if (rounds > 0) own = loads[(rounds - 1) * G + c];
   }
-  if (warp == 0) {
-    const int pos = (int)((long long)W * c / G) - sums[1] + sums[0];
-    const int end = (int)((long long)W * (c + 1) / G) - sums[1] - own + sums[0];
-    if (rounds > 0 && lane == 0) {
+  if (warp == 0 && lane == 0) {
+    plan->rounds = rounds;
+    if (rounds > 0) {
       const int b = last_at_most(before, n_seqs, p.Hk, c, pairs_of);
       const int first = pairs_of(before[b]), pairs = pairs_of(before[b + 1]) - first, i = c - p.Hk * first;
       plan->whole = Start{b, i / pairs, i % pairs, 0};
     }
-    if (pos < end) {
-      const int b = last_at_most(before, n_seqs, p.Hk, pos, tiles_of);
+  }
+  if (warp < 2) {  // the range's begin, and its end
+    int x = warp == 0 ? (int)((long long)W * c / G) - sums[1] + sums[0]
+                      : (int)((long long)W * (c + 1) / G) - sums[1] - own + sums[0];
+    if (x < W) {
+      const int b = last_at_most(before, n_seqs, p.Hk, x, tiles_of);
       const int w = tiles_of(before[b + 1]) - tiles_of(before[b]);
-      const int rem = pos - p.Hk * tiles_of(before[b]), h = rem / w;
+      const int rem = x - p.Hk * tiles_of(before[b]), h = rem / w;
       int left = rem - h * w;
       const Seq s = seq(b);
       const int pairs = pairs_of(before[b + 1]) - pairs_of(before[b]);
@@ -319,25 +327,30 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
         if (q0 + lane < pairs) {
           Job j;
           pair_span(p, s, q0 + lane, tpt, j);
-          t = max(j.total, 1);
+          t = max(j.total, 1) + kPairCost;
         }
         int inc = t;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-          const int x = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += x;
+          const int y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
         }
-        if (left >= inc - t && left < inc) plan->range = Start{b, h, q0 + lane, left - (inc - t)};
         const int sum = __shfl_sync(0xffffffffu, inc, 31);
-        if (left < sum) break;
+        if (left < sum) {
+          const uint32_t here = __ballot_sync(0xffffffffu, left >= inc - t && left < inc);
+          const int src = __ffs(here) - 1;
+          int off = left - __shfl_sync(0xffffffffu, inc - t, src);
+          if (off <= kPairCost) {
+            x -= off;
+            off = 0;
+          }
+          if (warp == 0 && lane == 0) plan->range = Start{b, h, q0 + src, off};
+          break;
+        }
         left -= sum;
       }
     }
-    if (lane == 0) {
-      plan->rounds = rounds;
-      plan->pos = pos;
-      plan->end = end;
-    }
+    if (lane == 0) (warp == 0 ? plan->pos : plan->end) = x;
   }
 }
 
