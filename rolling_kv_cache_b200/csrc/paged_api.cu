@@ -191,9 +191,15 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   // A prefix and many rows: where the sequences fill their query tiles on their
   // own, each walks the prefix's tiles itself (the same products, the tiles from
   // L2, no second pass and no merge); where they do not, the whole batch's rows
-  // are packed into tiles for a pass over the prefix.
+  // are packed into tiles for a pass over the prefix. The line is a fill of 3/4 of
+  // an average sequence's tile pairs: 48 sequences of 64-token pairs over 7021
+  // prefix tokens take 388 us in two passes and 394 walked at 48 tokens each, 476
+  // and 398 at 63, 194 and 347 at 16; 16 of 256-token pairs over 9360, 357 and 327
+  // at 200, 253 and 284 at 100.
   const int per_pair = 2 * (128 / w->group);
-  w->lead = m->prefix_len > 0 && !w->decode && (int64_t)n_tok >= (int64_t)per_pair * p->n_seqs;
+  const int64_t each = p->n_seqs > 0 ? ((int64_t)n_tok + p->n_seqs - 1) / p->n_seqs : 0;
+  const int64_t room = (each + per_pair - 1) / per_pair * per_pair;
+  w->lead = m->prefix_len > 0 && !w->decode && 4 * each >= 3 * room;
   w->two_pass = m->prefix_len > 0 && !w->lead;
   // positions of the stream-K split are 32-bit: tiles of every unit, summed
   const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 6;
