@@ -19,7 +19,9 @@ namespace {
 constexpr int kCombThreads = 256;
 
 // weight[i][r] from log2-sum-exps to the shares of the sum, for sources i < n
-// and rows r < rows, a warp a row; lse[r]: the log2 of the sum.
+// and rows r < rows, a warp a row; lse[r]: the log2 of the sum. A source with
+// -inf gets the weight 0 whatever the others hold (a NaN among them included): it
+// may not exist, and is not read.
 template <int ROWS>
 __device__ __forceinline__ void normalise(float (*weight)[ROWS], int n, int rows, float* lse) {
   const int lane = threadIdx.x & 31;
@@ -33,7 +35,10 @@ __device__ __forceinline__ void normalise(float (*weight)[ROWS], int n, int rows
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
-    for (int i = lane; i < n; i += 32) weight[i][r] = exp2f(weight[i][r] - ref) * inv;
+    for (int i = lane; i < n; i += 32) {
+      const float x = weight[i][r];
+      weight[i][r] = x == -INFINITY ? 0.f : exp2f(x - ref) * inv;
+    }
     if (lane == 0) lse[r] = l == 0.f ? -INFINITY : ref + log2f(l);
   }
 }

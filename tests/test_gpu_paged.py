@@ -754,3 +754,25 @@ def test_rows_listed_out_of_order_fault_nothing():
         paged.device_status()  # some of these give a token a place that is none
     except B.RcError:
         pass
+
+
+def test_a_nan_in_the_prefix_reaches_every_row_and_reads_no_part_that_is_none():
+    """Rows whose sum is NaN, with parts of unequal number on both sides of a pair of query tiles."""
+    lens = [(1, 70)] + [(2, 40)] * 31 + [(1, 0)]  # 8 heads a key head: 32 queries a pair, the 16th of the twos in both
+    bt = Batch(79, lens, 8, 1, 64, 16, spare=200)
+    n = 16 * 190 + 3
+    table = torch.tensor(bt.free[:191], dtype=torch.int32, device="cuda")
+    j = torch.arange(n, device="cuda")
+    for pool in (bt.k_pages, bt.v_pages):
+        pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, n, 1, 64)
+    call = lambda: paged.prefix_attention(*bt.args()[:3], table, n, *bt.args()[3:], max_q=2, return_lse=True)
+    want = call()
+    assert_attend(want, bt, prefix=(table, n))
+    at = (int(table[100]), 0, 5)
+    key = bt.k_pages[at].clone()
+    bt.k_pages[at] = float("nan")
+    o, lse = call()
+    assert bool(o.isnan().all()) and bool(lse.isnan().all())
+    bt.k_pages[at] = key
+    again = call()
+    assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
