@@ -358,7 +358,7 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
 // not the tile loop's.
 
 // -inf over the scores of one row's 64 keys from h0 on (TMEM columns tS ..)
-// that the row does not see or whose page is none; returns the largest other score.
+// that the row does not see or whose page is none; returns the largest other score (NaN if one is).
 __device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int sink, uint32_t pages, int page_log2) {
   auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
   unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
@@ -373,10 +373,9 @@ __device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int s
     ptx::tmem_ld32(tS + cc * 32, r);
     ptx::tmem_ld_wait();
 #pragma unroll
-    for (int k = 0; k < 32; ++k) {
-      r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
-      mx = fmaxf(mx, __uint_as_float(r[k]));
-    }
+    for (int k = 0; k < 32; ++k) r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
     if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) ptx::tmem_st32(tS + cc * 32, r);
   }
   ptx::tmem_st_wait();
@@ -731,11 +730,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           ptx::tmem_ld32(tS, ra);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
           ptx::tmem_ld32(tS + 32, ra);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
         } else {
           // some key of the tile is hidden from some row: those scores become
           // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
@@ -750,9 +749,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         }
         float mo;
         if (!swap(mx, mo)) { ok = false; break; }
-        const float m_new = ptx::fmax3(m, mx, mo);
-        const bool need = m_new > m + thresh;       // also true for the first visible tile
-        const bool real = need && m != -INFINITY;   // O already holds weighted values
+        // a NaN score makes the maximum NaN, and with it the row's sum and output: the
+        // cubic's clamp would turn the NaN itself into 2^-126
+        const float m_new = ptx::fmax3_nan(m, mx, mo);
+        const bool need = !(m_new <= m + thresh);  // also true for the first visible tile
+        const bool real = need && m > -INFINITY;   // O already holds weighted values
         if (__any_sync(0xffffffffu, real)) {
           // PV of the previous tile is complete: it was issued before this
           // tile's S, which the wait above saw complete
@@ -824,7 +825,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       // pass's result or to this CTA's partial slot); each warp writes its D/2 columns
       float l_other = 0.f;
       if (ok && !swap(l, l_other)) ok = false;
-      const float lt = l + l_other;
+      // a maximum of +inf: inf - inf, which the clamp hides as it does NaN
+      const float lt = m == INFINITY ? NAN : l + l_other;
       const bool have_o =
           ok && n_tiles > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
       if (n_tiles > 0) ++nj;

@@ -776,3 +776,19 @@ def test_a_nan_in_the_prefix_reaches_every_row_and_reads_no_part_that_is_none():
     bt.k_pages[at] = key
     again = call()
     assert torch.equal(again[0], want[0]) and torch.equal(again[1], want[1])
+
+
+@pytest.mark.parametrize("a", [1, 40])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_a_key_that_is_no_number_makes_the_rows_that_see_it_nan(a, value):
+    """A NaN score, and one of +inf (inf - inf in the softmax), wherever in a tile; other sequences keep their bits."""
+    for at in (0, 3, 5, 118, 127, 130, 4001):
+        bt = Batch(80, [(a, 5000), (a, 300), (a, 40)], 2, 1, 64, 16)
+        want, wl = paged.paged_attention(*bt.args(), max_q=a, return_lse=True)
+        row = bt.k_pages[int(bt.page_table[0, at // 16]), 0, at % 16]
+        row.copy_(torch.full_like(row, value) if value != value else value * bt.q[a - 1, 0].sign())
+        o, lse = paged.paged_attention(*bt.args(), max_q=a, return_lse=True)
+        rows = slice(0, a) if value != value else slice(a - 1, a)
+        heads = slice(0, 2) if value != value else slice(0, 1)
+        assert bool(o[rows, heads].isnan().all()) and bool(lse[heads, rows].isnan().all()), at
+        assert torch.equal(o[a:], want[a:]) and torch.equal(lse[:, a:], wl[:, a:])
