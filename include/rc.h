@@ -494,7 +494,7 @@ rc_status rc_paged_append(const rc_paged* p, const rc_rope* rope, int n_tok, con
 typedef struct rc_paged_mask {
   int32_t frame_seqlen, sink_frames, window_frames;
   int32_t max_q;                /* no sequence has more queries (a hint where it may be more; see below) */
-  float scale;                  /* of q . k; 0: 1 / sqrt(head_dim) */
+  float scale;                  /* of q . k, in [1e-30, 1e30]; 0: 1 / sqrt(head_dim) */
   int32_t prefix_len;
   const int32_t* prefix_table;  /* [prefix_pages] */
   int32_t prefix_pages;         /* at least prefix_len / page_size, rounded up */

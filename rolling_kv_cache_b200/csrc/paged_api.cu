@@ -182,7 +182,8 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   if (m->sink_frames < 0 || m->window_frames < 0) return invalid("sink_frames and window_frames must not be negative");
   if (m->sink_frames > 0 && m->window_frames == 0) return invalid("sink_frames need a window");
   if (m->max_q < 0) return invalid("max_q must not be negative");
-  if (!(m->scale >= 0.f) || !std::isfinite(m->scale)) return invalid("scale must be finite and not negative");
+  // within these bounds its product with the log2 of e, and what is divided by that, are finite and normal
+  if (m->scale != 0.f && !(m->scale >= 1e-30f && m->scale <= 1e30f)) return invalid("scale must be 0 or in [1e-30, 1e30]");
   if (m->prefix_len < 0 || m->prefix_pages < 0) return invalid("prefix_len must not be negative");
   if (m->prefix_len > 0 &&
       (!m->prefix_table || (int64_t)m->prefix_pages * p->page_size < m->prefix_len || m->prefix_len > (1 << 30)))

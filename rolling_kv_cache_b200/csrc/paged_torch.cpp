@@ -365,7 +365,7 @@ std::pair<Tensor, std::optional<Tensor>> attention(const Tensor& q, const Tensor
   const int32_t n_tok = tokens_of(q);
   for (int64_t v : {max_q.value_or(0), frame_seqlen, sink_frames, window_frames, prefix_len})
     if (v < 0 || v > INT32_MAX) refuse("max_q, frames and prefix_len must be 32-bit and not negative");
-  if (scale && !(*scale > 0)) refuse("scale must be positive");
+  if (scale && !(*scale >= 1e-30 && *scale <= 1e30)) refuse("scale must be in [1e-30, 1e30]");
   rc_paged_mask m{};
   m.frame_seqlen = static_cast<int32_t>(frame_seqlen);
   m.sink_frames = static_cast<int32_t>(sink_frames);

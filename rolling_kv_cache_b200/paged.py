@@ -126,7 +126,8 @@ def paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tenso
     h // (q_heads // kv_heads). With f = position // frame_seqlen, a query sees
     the keys of frames <= its own (frame_seqlen 1: causal; a frame beyond every
     length: full attention); with ``window_frames`` only the last that many, its own
-    included, and the first ``sink_frames``. Entries of pages that no query sees
+    included, and the first ``sink_frames`` (0 without a window). ``scale``
+    (default 1 / sqrt(head_dim)) lies in [1e-30, 1e30]. Rows of pages that no query of the call sees
     may hold anything. ``max_q``: the most queries of a sequence, where the
     caller knows it (default: all tokens); it chooses the kernel and must not be
     too small. ``out`` may be q itself. Rows behind the last sequence are left as they are (uninitialised without ``out``).

@@ -792,3 +792,12 @@ def test_a_key_that_is_no_number_makes_the_rows_that_see_it_nan(a, value):
         heads = slice(0, 2) if value != value else slice(0, 1)
         assert bool(o[rows, heads].isnan().all()) and bool(lse[heads, rows].isnan().all()), at
         assert torch.equal(o[a:], want[a:]) and torch.equal(lse[:, a:], wl[:, a:])
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_the_smallest_scale_and_scales_beyond_the_bounds(max_q):
+    bt = Batch(81, [(max_q, 500), (max_q, 70)], 4, 2, 64, 16)
+    assert_attend(paged.paged_attention(*bt.args(), max_q=max_q, scale=1e-30, return_lse=True), bt, scale=1e-30)
+    for scale in (1e-31, 1e-46, 1.1e30, 1e300, float("nan"), float("inf")):
+        with pytest.raises(ValueError):
+            paged.paged_attention(*bt.args(), max_q=max_q, scale=scale)

@@ -94,6 +94,12 @@ def test_bad_masks_are_refused(over):
     _refused(B.RC_EINVAL, B.rc_paged_workspace, _pool(), m, 3, 4)
 
 
+@pytest.mark.parametrize("scale", [1e-44, 9e-31, 1.1e30, 3e38])
+def test_scales_whose_reciprocal_or_product_overflows_are_refused(scale):
+    m = B.rc_paged_mask(frame_seqlen=1, max_q=1, scale=scale)
+    _refused(B.RC_EINVAL, B.rc_paged_workspace, _pool(), m, 3, 4)
+
+
 def test_bad_heads_rows_and_workspaces_are_refused():
     m = B.rc_paged_mask(frame_seqlen=1, max_q=1)
     for heads in (0, 3, -2, 2 * 129):
