@@ -484,8 +484,8 @@ rc_status rc_paged_append(const rc_paged* p, const rc_rope* rope, int n_tok, con
  * sequence in frames <= f (its own frame whole; frame_seqlen 1 is causal
  * attention token by token, one beyond every length is full attention). With
  * window_frames > 0 only the last window_frames of them, its own included, and the first
- * sink_frames frames. Entries of pages that no query of the call sees are not
- * read and may hold anything.
+ * sink_frames frames (0 without a window). What no query of the call sees, entries
+ * of page_table and rows of pages, may hold anything.
  *
  * A prefix (prefix_len > 0) is one more run of keys that every query of the
  * batch sees whole, held once in the pages prefix_table lists, and multiplied
@@ -506,10 +506,10 @@ rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n
 
 /* out = softmax(scale q k^T + mask) v over the batch's pages. Query head h
  * reads key head h / (q_heads / kv_heads). A query that sees no key gets
- * zeros and lse -inf. Keys that no query of its tile sees (behind a sequence, before its
+ * zeros and lse -inf. Keys that no query of the call sees (behind a sequence, before its
  * windows, rows not written yet) do not reach the result whatever their bits;
- * a key that some query sees must be finite, or the NaN it makes can reach the
- * queries of the same sequence that are computed with it.
+ * a key that some query sees must be finite, or the NaN it makes reaches that
+ * query and can reach queries of the same sequence that do not see it.
  *   lse: NULL or [q_heads][n_tok] fp32, natural log.
  *   out may be q (same strides), else must not overlap it.
  * max_q * (q_heads / kv_heads) <= 16 takes the kernel for few rows; it
