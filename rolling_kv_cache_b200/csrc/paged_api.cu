@@ -44,6 +44,7 @@ size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 int elem_size(int dtype) { return dtype == RC_F32 ? 4 : 2; }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
 // `distinct`: rows that are written, or copied by TMA: every stride over more than one entry is at least a row.
 rc_status check_rows(const rc_rows& r, int n_tok, int d, int size, bool distinct, const char* what) {
@@ -70,7 +71,7 @@ rc_status make_axes(const rc_rope* rope, int n_tok, int head_dim, rc::AxisTables
   if (!rope || rope->n_axes == 0) return RC_OK;
   if (rope->n_axes < 0 || rope->n_axes > 3) return invalid("rope: n_axes must be 1 to 3");
   if (rope->pairing != RC_PAIR_ADJACENT && rope->pairing != RC_PAIR_HALVES) return invalid("rope: unknown pairing");
-  if (n_tok > 0 && (!rope->pos || reinterpret_cast<uintptr_t>(rope->pos) % 4)) return invalid("rope: null or misaligned positions");
+  if (n_tok > 0 && (!rope->pos || !aligned4(rope->pos))) return invalid("rope: null or misaligned positions");
   int sum = 0;
   for (int a = 0; a < rope->n_axes; ++a) {
     if (rope->pairs[a] < 0 || rope->pairs[a] > head_dim / 2) return invalid("rope: pairs out of range");
@@ -108,6 +109,8 @@ rc_status check_paged(const rc_paged* p, int n_tok, rc::BatchView* b) {
   if (n_tok < 0 || n_tok > (1 << 30)) return invalid("n_tok out of range");
   if (p->n_seqs < 0 || p->n_seqs > rc::kMaxSeqs) return invalid("n_seqs must be in [0, 4096]");
   if (p->n_seqs > 0 && (!p->cu_q || !p->kv_len)) return invalid("null cu_q or kv_len");
+  if (!aligned4(p->cu_q) || !aligned4(p->kv_len) || !aligned4(p->page_table))
+    return invalid("misaligned cu_q, kv_len or page_table");
   if (p->max_pages < 0) return invalid("max_pages must not be negative");
   if ((int64_t)p->max_pages * p->page_size > (1 << 30))
     return SetLastError(RC_ERANGE, "max_pages * page_size exceeds 2^30");
@@ -188,6 +191,7 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   if (m->prefix_len > 0 &&
       (!m->prefix_table || (int64_t)m->prefix_pages * p->page_size < m->prefix_len || m->prefix_len > (1 << 30)))
     return invalid("prefix_table must list the pages of prefix_len tokens");
+  if (!aligned4(m->prefix_table)) return invalid("misaligned prefix_table");
   w->decode = (int64_t)std::max(1, m->max_q) * w->group <= rc::kDecodeRows;
   // A prefix and many rows: where the sequences fill their query tiles on their
   // own, each walks the prefix's tiles itself (the same products, the tiles from
@@ -248,6 +252,7 @@ rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, 
     if (n_tok < 0 || n_tok > (1 << 30)) return invalid("n_tok out of range");
     rc::RopeAxesParams p{};
     if (rope->n_axes == 0) return invalid("rope: n_axes must be 1 to 3");
+    if (!aligned4(status)) return invalid("misaligned status");
     if (rc_status st = make_axes(rope, n_tok, head_dim, &p.ax)) return st;
     const int size = elem_size(dtype);
     for (int i = 0; i < 2; ++i) {
@@ -273,6 +278,7 @@ rc_status rc_paged_append(const rc_paged* pg, const rc_rope* rope, int n_tok, co
     rc::PagedAppendParams p{};
     if (rc_status st = check_paged(pg, n_tok, &p.b)) return st;
     if (!q || !k || !v || !q_out) return invalid("null argument");
+    if (!aligned4(status)) return invalid("misaligned status");
     if (rc_status st = make_axes(rope, n_tok, pg->head_dim, &p.ax)) return st;
     if (rc_status st = check_rows(*q, n_tok, pg->head_dim, 2, false, "q")) return st;
     if (rc_status st = check_rows(*q_out, n_tok, pg->head_dim, 2, true, "q_out")) return st;
@@ -310,6 +316,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
                              void* stream) {
   return guarded([&]() -> rc_status {
     if (!q || !out) return invalid("null argument");
+    if (!aligned4(status) || !aligned4(lse)) return invalid("misaligned status or lse");
     Work w;
     if (rc_status st = plan_work(pg, m, n_tok, q->heads, &w)) return st;
     const int d = pg->head_dim;

@@ -181,3 +181,19 @@ def test_both_attention_kernels_use_one_exponential():
         return re.search(r"float2 exp2_cubic2\(float2 x\) \{.*?\n\}", text, re.S).group(0)
 
     assert body("attn_fwd.cu") == body("exp2_cubic.cuh")
+
+
+@pytest.mark.parametrize("name", ["cu_q", "kv_len", "page_table", "prefix_table", "status", "lse"])
+def test_words_off_their_alignment_are_refused(name):
+    p = _pool(**({name: P + 2} if name in ("cu_q", "kv_len", "page_table") else {}))
+    m = B.rc_paged_mask(frame_seqlen=1, max_q=1)
+    if name == "prefix_table":
+        m = B.rc_paged_mask(frame_seqlen=1, max_q=1, prefix_len=5, prefix_table=P + 2, prefix_pages=1)
+    status, lse = (P + 2 if name == n else 0 for n in ("status", "lse"))
+    two = _rows(2)
+    _refused(B.RC_EINVAL, B.rc_paged_attention, p, m, 3, _rows(), _rows(), lse, P, 1 << 30, status)
+    if name not in ("prefix_table", "lse"):
+        _refused(B.RC_EINVAL, B.rc_paged_append, p, None, 3, _rows(), two, two, _rows(), status)
+    if name == "status":
+        one = (B.rc_rows * 2)(_rows(), B.rc_rows())
+        _refused(B.RC_EINVAL, B.rc_rope_axes, _rope(), B.RC_BF16, 3, 64, 0, one, one, status)
