@@ -404,8 +404,10 @@ rc_status rc_cache_destroy(void* handle);
  * Conventions beside those above
  *   - Element types: RC_BF16 and RC_F16, and RC_F32 for rc_rope_axes only; one type per call.
  *   - Strides are in elements and multiples of 16 bytes, at least 0 where only
- *     read by plain loads (x of rc_rope_axes; q, k, v of rc_paged_append), else at least head_dim; the last dimension (head_dim) is
- *     contiguous; every tensor starts on a 16-byte boundary.
+ *     read by plain loads (x of rc_rope_axes; q, k, v of rc_paged_append), else at
+ *     least head_dim; rows that a call writes do not overlap, whatever the order of
+ *     the dimensions; the last dimension (head_dim) is contiguous; every tensor
+ *     starts on a 16-byte boundary.
  *   - Lengths, tables and positions are int32 device arrays, read when the
  *     kernels run: a captured call sees their values of each replay.
  *   - What such an array holds out of range (a position outside its rotation

@@ -7,8 +7,10 @@
 #include <cmath>
 #include <cstring>
 #include <exception>
+#include <initializer_list>
 #include <mutex>
 #include <string>
+#include <utility>
 
 #include "paged.cuh"
 
@@ -46,8 +48,26 @@ int elem_size(int dtype) { return dtype == RC_F32 ? 4 : 2; }
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 bool aligned4(const void* p) { return reinterpret_cast<uintptr_t>(p) % 4 == 0; }
 
-// `distinct`: rows that are written, or copied by TMA: every stride over more than one entry is at least a row.
-rc_status check_rows(const rc_rows& r, int n_tok, int d, int size, bool distinct, const char* what) {
+// Whether entries of `row` elements at every combination of indices i[k] < n[k] and strides are apart: dimension by
+// dimension, smallest stride first, each steps over all that the ones before it cover.
+bool apart(std::initializer_list<std::pair<int64_t, int64_t>> dims, int64_t row) {
+  std::pair<int64_t, int64_t> d[3];  // (stride, entries)
+  int n = 0;
+  for (const auto& x : dims)
+    if (x.second > 1) d[n++] = x;
+  std::sort(d, d + n);
+  __int128 extent = row;
+  for (int i = 0; i < n; ++i) {
+    if (d[i].first < extent) return false;
+    extent += (__int128)(d[i].second - 1) * d[i].first;
+  }
+  return true;
+}
+
+// How a call uses rows: plain loads take any strides, a TMA copy's are at least a row, written rows are apart.
+enum class Use { kRead, kCopied, kWritten };
+
+rc_status check_rows(const rc_rows& r, int n_tok, int d, int size, Use use, const char* what) {
   const std::string name(what);
   if (r.heads < 0 || r.heads > 16384) return invalid((name + ": heads out of range").c_str());
   if (r.heads == 0 || n_tok == 0) return RC_OK;
@@ -57,7 +77,9 @@ rc_status check_rows(const rc_rows& r, int n_tok, int d, int size, bool distinct
   const int64_t most = (int64_t)1 << 40;
   if (r.tok_stride < 0 || r.head_stride < 0 || r.tok_stride > most || r.head_stride > most)
     return invalid((name + ": stride out of range").c_str());
-  if (distinct && ((n_tok > 1 && r.tok_stride < d) || (r.heads > 1 && r.head_stride < d)))
+  if (use == Use::kCopied && ((n_tok > 1 && r.tok_stride < d) || (r.heads > 1 && r.head_stride < d)))
+    return invalid((name + ": strides must be at least a row").c_str());
+  if (use == Use::kWritten && !apart({{r.tok_stride, n_tok}, {r.head_stride, r.heads}}, d))
     return invalid((name + ": the rows overlap").c_str());
   return RC_OK;
 }
@@ -256,8 +278,8 @@ rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, 
     if (rc_status st = make_axes(rope, n_tok, head_dim, &p.ax)) return st;
     const int size = elem_size(dtype);
     for (int i = 0; i < 2; ++i) {
-      if (rc_status st = check_rows(x[i], n_tok, head_dim, size, false, "x")) return st;
-      if (rc_status st = check_rows(y[i], n_tok, head_dim, size, true, "y")) return st;
+      if (rc_status st = check_rows(x[i], n_tok, head_dim, size, Use::kRead, "x")) return st;
+      if (rc_status st = check_rows(y[i], n_tok, head_dim, size, Use::kWritten, "y")) return st;
       if (x[i].heads != y[i].heads) return invalid("x and y differ in heads");
       p.x[i] = view(x[i], size);
       p.y[i] = view(y[i], size);
@@ -280,11 +302,14 @@ rc_status rc_paged_append(const rc_paged* pg, const rc_rope* rope, int n_tok, co
     if (!q || !k || !v || !q_out) return invalid("null argument");
     if (!aligned4(status)) return invalid("misaligned status");
     if (rc_status st = make_axes(rope, n_tok, pg->head_dim, &p.ax)) return st;
-    if (rc_status st = check_rows(*q, n_tok, pg->head_dim, 2, false, "q")) return st;
-    if (rc_status st = check_rows(*q_out, n_tok, pg->head_dim, 2, true, "q_out")) return st;
-    if (rc_status st = check_rows(*k, n_tok, pg->head_dim, 2, false, "k")) return st;
-    if (rc_status st = check_rows(*v, n_tok, pg->head_dim, 2, false, "v")) return st;
+    if (rc_status st = check_rows(*q, n_tok, pg->head_dim, 2, Use::kRead, "q")) return st;
+    if (rc_status st = check_rows(*q_out, n_tok, pg->head_dim, 2, Use::kWritten, "q_out")) return st;
+    if (rc_status st = check_rows(*k, n_tok, pg->head_dim, 2, Use::kRead, "k")) return st;
+    if (rc_status st = check_rows(*v, n_tok, pg->head_dim, 2, Use::kRead, "v")) return st;
     if (q->heads != q_out->heads) return invalid("q and q_out differ in heads");
+    for (const int64_t* st : {pg->k_stride, pg->v_stride})
+      if (!apart({{st[0], pg->n_pages}, {st[1], pg->kv_heads}, {st[2], pg->page_size}}, pg->head_dim))
+        return invalid("the pages' rows overlap");
     if (k->heads != pg->kv_heads || v->heads != pg->kv_heads) return invalid("k and v must have the pool's heads");
     p.q = view(*q, 2);
     p.q_out = view(*q_out, 2);
@@ -317,20 +342,20 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
   return guarded([&]() -> rc_status {
     if (!q || !out) return invalid("null argument");
     if (!aligned4(status) || !aligned4(lse)) return invalid("misaligned status or lse");
+    rc::PagedAttnParams p;
+    std::memset(&p, 0, sizeof(p));
+    if (rc_status st = check_paged(pg, n_tok, &p.b)) return st;
+    const int d = pg->head_dim;
+    if (rc_status st = check_rows(*q, n_tok, d, 2, Use::kCopied, "q")) return st;
+    if (rc_status st = check_rows(*out, n_tok, d, 2, Use::kWritten, "out")) return st;
+    if (q->heads != out->heads) return invalid("q and out differ in heads");
     Work w;
     if (rc_status st = plan_work(pg, m, n_tok, q->heads, &w)) return st;
-    const int d = pg->head_dim;
-    if (rc_status st = check_rows(*q, n_tok, d, 2, true, "q")) return st;
-    if (rc_status st = check_rows(*out, n_tok, d, 2, true, "out")) return st;
-    if (q->heads != out->heads) return invalid("q and out differ in heads");
     if (n_tok == 0 || pg->n_seqs == 0) return RC_OK;
     if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign)
       return invalid("the workspace must be 256-byte aligned");
     if (workspace_bytes < w.total) return SetLastError(RC_ENOMEM, "workspace smaller than rc_paged_workspace()");
     const bool bf16 = pg->dtype == RC_BF16;
-    rc::PagedAttnParams p;
-    std::memset(&p, 0, sizeof(p));
-    if (rc_status st = check_paged(pg, n_tok, &p.b)) return st;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     p.q = view(*q, 2);
     p.out = view(*out, 2);

@@ -197,3 +197,26 @@ def test_words_off_their_alignment_are_refused(name):
     if name == "status":
         one = (B.rc_rows * 2)(_rows(), B.rc_rows())
         _refused(B.RC_EINVAL, B.rc_rope_axes, _rope(), B.RC_BF16, 3, 64, 0, one, one, status)
+
+
+def test_written_rows_that_overlap_are_refused():
+    """Also where each stride is at least a row: [3][4] rows of 64, a token's heads reaching into the next token's."""
+    two, one = _rows(2), (B.rc_rows * 2)(_rows(), B.rc_rows())
+    m = B.rc_paged_mask(frame_seqlen=1, max_q=1)
+    for tok, head in ((64, 64), (128, 64), (192, 64), (64, 128), (64, 184), (200, 72)):
+        r = B.rc_rows(P, tok, head, 4)
+        _refused(B.RC_EINVAL, B.rc_paged_attention, _pool(), m, 3, _rows(), r, 0, P, 1 << 30)
+        _refused(B.RC_EINVAL, B.rc_paged_append, _pool(), None, 3, _rows(), two, two, r)
+        _refused(B.RC_EINVAL, B.rc_rope_axes, _rope(), B.RC_BF16, 3, 64, 0, one, (B.rc_rows * 2)(r, B.rc_rows()))
+    # the pool an append writes: pages closer than a page, heads closer than 16 rows
+    for st in ((1024, 1024, 64), (2048, 512, 64), (1088, 1024, 128)):
+        for name in ("k_stride", "v_stride"):
+            _refused(B.RC_EINVAL, B.rc_paged_append, _pool(**{name: st}), None, 3, _rows(), two, two, _rows())
+
+
+def test_written_rows_in_every_nesting_pass_the_checks():
+    """Refused only for the workspace, which is looked at after the rows (or, without a GPU, for that)."""
+    m = B.rc_paged_mask(frame_seqlen=1, max_q=1)
+    for tok, head in ((256, 64), (64, 192), (320, 72), (512, 128), (72, 256)):
+        with pytest.raises(B.RcError, match="workspace|device attribute"):
+            B.rc_paged_attention(_pool(), m, 3, _rows(), B.rc_rows(P, tok, head, 4), 0, 0, 0)
