@@ -135,6 +135,11 @@ int32_t tokens_of(const Tensor& t) {
   return static_cast<int32_t>(t.size(0));
 }
 
+// Tells autograd that the library wrote to t.
+void written(const Tensor& t) {
+  if (!t.is_inference()) torch::autograd::impl::bump_version(t);
+}
+
 Tensor new_like(const Tensor& t) { return at::empty(t.sizes(), t.options()); }
 
 // ---------------------------------------------------------------- rotation
@@ -260,6 +265,7 @@ Tensors rope_axes(const Tensors& xs, const Tensor& pos, const Tensors& tables, b
       for (const Tensor& t : *ts)
         if (t.requires_grad()) refuse("out= takes no part in autograd; call it under torch.no_grad()");
   turn(xs, *out, pos, tables, halves, inverse);
+  for (const Tensor& t : *out) written(t);
   return *out;
 }
 
@@ -344,6 +350,9 @@ std::optional<Tensor> append(const std::optional<Tensor>& q, const Tensor& k, co
   const c10::cuda::CUDAGuard guard(dev.index);
   check(rc_paged_append(&p, pos ? &r : nullptr, tokens_of(k), &rq, &rk, &rv, &ro, status_word(dev.index),
                         at::cuda::getCurrentCUDAStream(dev.index).stream()));
+  written(k_pages);
+  written(v_pages);
+  if (q_out) written(*q_out);
   return out;
 }
 
@@ -392,6 +401,7 @@ std::pair<Tensor, std::optional<Tensor>> attention(const Tensor& q, const Tensor
   const Tensor work = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
   check(rc_paged_attention(&p, &m, n_tok, &rq, &ro, lse ? lse->data_ptr<float>() : nullptr, work.data_ptr(), bytes,
                            status_word(dev.index), at::cuda::getCurrentCUDAStream(dev.index).stream()));
+  if (out_) written(out);
   return {out, lse};
 }
 

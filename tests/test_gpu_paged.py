@@ -801,3 +801,27 @@ def test_the_smallest_scale_and_scales_beyond_the_bounds(max_q):
     for scale in (1e-31, 1e-46, 1.1e30, 1e300, float("nan"), float("inf")):
         with pytest.raises(ValueError):
             paged.paged_attention(*bt.args(), max_q=max_q, scale=scale)
+
+
+def test_writes_into_tensors_that_autograd_saved_are_noticed():
+    bt = Batch(82, [(2, 30), (1, 9)], 4, 2, 64, 16)
+    q, k_pages, v_pages, cu, kv, table = bt.args()
+    tables = paged.rope_tables((9,), (32,))
+    pos = torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+    k = randn(bt.gen, 3, 2, 64)
+    writes = [(q, lambda: paged.rope_axes(q, pos, tables, out=q)),
+              (k, lambda: paged.rope_axes((q, k), pos, tables, out=(torch.empty_like(q), k))),
+              (q, lambda: paged.paged_append(q, k, k, k_pages, v_pages, cu, kv, table, q_out=q)),
+              (k_pages, lambda: paged.paged_append(None, k, k, k_pages, v_pages, cu, kv, table)),
+              (v_pages, lambda: paged.paged_append(None, k, k, k_pages, v_pages, cu, kv, table)),
+              (q, lambda: paged.paged_attention(q, k_pages, v_pages, cu, kv, table, max_q=2, out=q))]
+    w = torch.ones((), dtype=BF16, device="cuda", requires_grad=True)
+    for t, write in writes:
+        y = (w * t).sum()  # saves t
+        with torch.no_grad():
+            write()
+        with pytest.raises(RuntimeError, match="inplace"):
+            y.backward()
+    with torch.inference_mode():  # tensors without a version
+        x = randn(bt.gen, 3, 2, 64)
+        paged.rope_axes(x, pos, tables, out=x)
