@@ -241,10 +241,27 @@ struct Turn2 : torch::autograd::Function<Turn2> {
   }
 };
 
+// While a graph is captured: refuses a leaf that an earlier graph of another
+// stream still holds. The captured backward would hand its gradient to that
+// graph's node on that stream, and a wait that leaves the capture ends the process.
+void no_older_graph(const Tensors& xs) {
+  if (!xs[0].is_cuda()) return;
+  const c10::cuda::CUDAGuard guard(xs[0].get_device());
+  if (at::cuda::currentStreamCaptureStatus() == at::cuda::CaptureStatus::None) return;
+  for (const Tensor& x : xs) {
+    if (!x.requires_grad() || !x.is_leaf()) continue;
+    const auto node = torch::autograd::impl::try_get_grad_accumulator(x);
+    const auto stream = node ? node->stream() : std::nullopt;
+    if (stream && *stream != at::cuda::getCurrentCUDAStream(xs[0].get_device()).unwrap())
+      refuse("an earlier autograd graph of this tensor, made on another stream, is alive: free it before the capture");
+  }
+}
+
 Tensors turned(const Tensors& xs, const Tensor& pos, const Tensors& tables, bool halves, bool inverse) {
   if (at::GradMode::is_enabled()) {
     bool any = false;
     for (const Tensor& x : xs) any |= x.requires_grad();
+    if (any) no_older_graph(xs);
     if (any)
       return xs.size() == 1 ? Turn1::apply(xs[0], pos, tables, halves, inverse)
                             : Turn2::apply(xs[0], xs[1], pos, tables, halves, inverse);

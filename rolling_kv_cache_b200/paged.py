@@ -86,6 +86,8 @@ def rope_axes(x, pos: torch.Tensor, tables: Sequence[torch.Tensor], *, pairing: 
     ("adjacent") or (m, m + head_dim / 2) ("halves"). ``inverse`` turns back.
     Differentiable in x (the gradient is the turn back). With ``out`` (a tensor
     or a pair; x itself for in place) the result is written there, outside autograd.
+    A leaf whose earlier graph, made on another stream, is alive is refused while
+    a CUDA graph is captured.
     """
     if pairing not in _HALVES:
         raise ValueError("pairing must be 'adjacent' or 'halves'")

@@ -825,3 +825,27 @@ def test_writes_into_tensors_that_autograd_saved_are_noticed():
     with torch.inference_mode():  # tensors without a version
         x = randn(bt.gen, 3, 2, 64)
         paged.rope_axes(x, pos, tables, out=x)
+
+
+def test_capture_beside_a_living_eager_graph_is_refused():
+    g = generator(83)
+    tables = paged.rope_tables((50,), (64,))
+    pos = _positions(g, 20, (50,))
+    x = randn(g, 20, 3, 128, dtype=F32).requires_grad_(True)
+    gy = randn(g, 20, 3, 128, dtype=F32)
+    y = paged.rope_axes(x, pos, tables)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        z = gy + 1
+        with pytest.raises(ValueError, match="graph of this tensor"):
+            paged.rope_axes(x, pos, tables)
+        with pytest.raises(ValueError, match="graph of this tensor"):
+            paged.rope_axes((gy, x), pos, tables)
+        paged.rope_axes(x.detach(), pos, tables)
+    del y
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        (dx,) = torch.autograd.grad(paged.rope_axes(x, pos, tables), (x,), gy)
+    gr.replay()
+    torch.cuda.synchronize()
+    assert_turned(dx, gy, pos, tables, False, inverse=True)
