@@ -459,7 +459,8 @@ typedef struct rc_paged {
   int32_t dtype;          /* RC_BF16 or RC_F16 */
   int32_t n_seqs;
   const int32_t* cu_q;    /* [n_seqs + 1], ascending from 0 (where it descends, the attention's results
-                             are undefined, with RC_ERANGE in *status) */
+                             are undefined, with RC_ERANGE in *status; rows before
+                             cu_q[0] are left as they are, with RC_ERANGE) */
   const int32_t* kv_len;  /* [n_seqs] tokens in the pages, this call's among them */
   const int32_t* page_table;
   int64_t table_stride;

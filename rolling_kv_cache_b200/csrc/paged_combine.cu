@@ -273,7 +273,7 @@ cudaError_t join_d(const JoinParams& p, cudaStream_t s) {
 }
 
 // out = the merge of the results in (pre_o, pre_lse) and (prev_o, prev_lse), 8
-// columns of a row a thread, rows behind the last sequence left alone.
+// columns of a row a thread, rows of no sequence left alone.
 template <int D, bool BF16>
 __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int kChunks = D / 8;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   const int heads = p.Hk * p.G;
   const long long row = x / kChunks;
   const int tok = (int)(row / heads), head = (int)(row - (long long)tok * heads), col = (int)(x % kChunks) * 8;
-  if (tok >= min(p.n_tok, __ldg(p.b.cu_q + p.b.n_seqs))) return;
+  if (tok >= min(p.n_tok, __ldg(p.b.cu_q + p.b.n_seqs)) || tok < __ldg(p.b.cu_q)) return;
   const float4* src = reinterpret_cast<const float4*>(p.pre_o + (size_t)row * D + col);
   const float4 a = src[0], b = src[1];
   float acc[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};

@@ -63,7 +63,7 @@ __device__ __forceinline__ Seq load_seq(const BatchView& v, int n_tok, int b) {
   s.n = min(max(e - s.q0, 0), n_tok - s.q0);
   s.L = min(max(l, 0), v.max_pages << v.page_log2);
   s.falls = e < a;
-  s.bad = s.falls || s.q0 != a || e - a != s.n || s.L != l;
+  s.bad = s.falls || s.q0 != a || e - a != s.n || s.L != l || (b == 0 && a != 0);
   return s;
 }
 

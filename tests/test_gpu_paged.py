@@ -849,3 +849,25 @@ def test_capture_beside_a_living_eager_graph_is_refused():
     gr.replay()
     torch.cuda.synchronize()
     assert_turned(dx, gy, pos, tables, False, inverse=True)
+
+
+@pytest.mark.parametrize("max_q,prefix", [(3, 0), (30, 0), (3, 40), (30, 40), (300, 200)])
+def test_rows_before_the_first_sequence_are_left_and_reported(max_q, prefix):
+    """cu_q that begins above 0, as a slice of a larger batch's does."""
+    bt = Batch(84, [(2, 2), (max_q, max_q + 40), (1, 9)], 4, 2, 64, 16, spare=14)
+    table = torch.tensor(bt.free[:13], dtype=torch.int32, device="cuda")
+    j = torch.arange(prefix, device="cuda")
+    for pool in (bt.k_pages, bt.v_pages):
+        pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, prefix, 2, 64)
+    attend = lambda *a, **k: (paged.prefix_attention(*a[:3], table, prefix, *a[3:], **k) if prefix
+                              else paged.paged_attention(*a, **k))
+    out = torch.full_like(bt.q, 7.0)
+    _, lse = attend(bt.q, bt.k_pages, bt.v_pages, bt.cu_q[1:], bt.kv_len[1:], bt.page_table[1:], max_q=max_q, out=out,
+                    return_lse=True)
+    assert bool((out[:2] == 7).all())
+    bt.lens, bt.cu, bt.q, bt.page_table = bt.lens[1:], [n - 2 for n in bt.cu[1:]], bt.q[2:], bt.page_table[1:]
+    bt.n_tok -= 2
+    assert_attend((out[2:], lse[:, 2:]), bt, prefix=(table, prefix) if prefix else None)
+    with pytest.raises(B.RcError) as e:
+        paged.device_status()
+    assert e.value.status == B.RC_ERANGE
