@@ -401,7 +401,7 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __grid_constant__ PagedAttnParams p) {
   using L = PreLayout<D>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ uint64_t bar_q, bar_qe, bar_kf[2], bar_vf[2], bar_ke[2], bar_ve[2], bar_s[2], bar_p[2], bar_o[2],
+  __shared__ uint64_t bar_q, bar_qe, bar_kf[2], bar_vf[2], bar_ke[2], bar_ve[2], bar_s[2], bar_h[2], bar_p[2], bar_o[2],
       bar_fin, bar_pair[8];
   __shared__ float swap_buf[2][2][2][kTileRows];  // [group][exchange parity][column half][row]
   // what the softmax has to know of tile g, at g % 4: its first key, its pages
@@ -431,6 +431,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       ptx::mbar_init(&bar_ke[i], 1);
       ptx::mbar_init(&bar_ve[i], 1);
       ptx::mbar_init(&bar_s[i], 1);
+      ptx::mbar_init(&bar_h[i], 256);
       ptx::mbar_init(&bar_p[i], 256);
       ptx::mbar_init(&bar_o[i], 1);
     }
@@ -611,14 +612,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     };
     // O_i += P_i V; committed for the epilogue after a job's last PV only (a
     // softmax that rescales O at tile j has waited for S_i(j), issued after PV_i(j-1))
-    auto issue_pv = [&](int i, int st, bool acc, bool last) {
+    auto issue_pv = [&](int i, int st, int part, bool acc) {
       const uint32_t sV = base_u32 + L::kV + st * L::kTile;
       // P of keys [16 ks, 16 ks + 16): column (ks / 4) * 64 + (ks % 4) * 8 of S_i
 #pragma unroll
-      for (int ks = 0; ks < kTileRows / 16; ++ks)
+      for (int k = 0; k < kTileRows / 32; ++k) {
+        const int ks = (k >> 1) * 4 + part * 2 + (k & 1);
         ptx::mma_ts(tmem + 256 + i * 128, tmem + i * 128 + (ks >> 2) * 64 + (ks & 3) * 8,
-                    ptx::sdesc_sw128(sV + ks * 2048, kSubTileBytes, 1024), idesc_o, acc || ks > 0);
-      if (last) ptx::mma_commit(&bar_o[i]);
+                    ptx::sdesc_sw128(sV + ks * 2048, kSubTileBytes, 1024), idesc_o, acc || part > 0 || k > 0);
+      }
     };
     int nq = 0, g = 0, gp[2] = {0, 0};
     bool ok = true;
@@ -641,10 +643,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       for (int j = 0; j < n; ++j, ++g) {
         const int st = g & 1, st1 = (g + 1) & 1;
         const bool more = j + 1 < n;
-        if (!ptx::mbar_wait(&bar_p[0], gp[0] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         if (!ptx::mbar_wait(&bar_vf[st], (g >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        if (!ptx::mbar_wait(&bar_h[0], gp[0] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
         ptx::tc_fence_after();
-        issue_pv(0, st, j > 0, !more);
+        issue_pv(0, st, 0, j > 0);
+        if (!ptx::mbar_wait(&bar_p[0], gp[0] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        ptx::tc_fence_after();
+        issue_pv(0, st, 1, true);
+        if (!more) ptx::mma_commit(&bar_o[0]);
         ++gp[0];
         if (!two) ptx::mma_commit(&bar_ve[st]);
         if (more) {
@@ -657,9 +663,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           }
         }
         if (two) {
+          if (!ptx::mbar_wait(&bar_h[1], gp[1] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          ptx::tc_fence_after();
+          issue_pv(1, st, 0, j > 0);
           if (!ptx::mbar_wait(&bar_p[1], gp[1] & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
           ptx::tc_fence_after();
-          issue_pv(1, st, j > 0, !more);
+          issue_pv(1, st, 1, true);
+          if (!more) ptx::mma_commit(&bar_o[1]);
           ++gp[1];
           ptx::mma_commit(&bar_ve[st]);
           if (more) {
@@ -801,11 +811,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         ptx::tmem_ld32(tS, ra);
         ptx::tmem_ld_wait();
         emit(ra, 0);
-        ptx::tmem_ld32(tS + 32, ra);
-        ptx::tmem_ld_wait();
-        emit(ra, 32);
-        ptx::tmem_st_wait();
-        l += sum;
         // V rows behind the sequence or before the windows may hold anything: zero, before group 0's P lets the
         // product start (a key that only later queries see is data, and meets P = 0)
         if (grp == 0 && tile_info[gt & 3].w) {
@@ -816,6 +821,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           zero_values<D>(base + L::kV + st * L::kTile, info.x, lead ? 0 : jb.lo_min, lead ? p.lead_len : jb.L,
                          p.mask.window > 0 && !lead ? p.mask.sink_tok : 0);
         }
+        ptx::tmem_ld32(tS + 32, ra);
+        ptx::tmem_st_wait();
+        ptx::tmem_ld_wait();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar_h[grp]);
+        emit(ra, 32);
+        ptx::tmem_st_wait();
+        l += sum;
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar_p[grp]);
         ++gs;
