@@ -20,7 +20,9 @@
 // P_i (16-bit) overwrites columns [0,32) and [64,96) of S_i and is the A operand of
 // O_i += P_i V. MMA issue order per KV tile j: PV0(j), S0(j+1), PV1(j), S1(j+1),
 // so that while one softmax group turns S into P the tensor core runs the
-// other group's two products.
+// other group's two products. P comes in two halves (the first and the last 32
+// keys of each warp's 64), each with its barrier: PV of the first runs while the
+// exponentials of the second do (video chunk 847 -> 818 us; a third step, 851).
 //
 // Schedule, found by every CTA from the lengths on the device: units in
 // (sequence, key head, pair) order; CTA c of G first takes whole units c, c + G,
@@ -38,7 +40,6 @@
 //
 // Every wait is bounded (2 s) and reports RC_ETIMEOUT through the status
 // word; no trap.
-#include "exp2_cubic.cuh"
 #include "paged_common.cuh"
 
 namespace rc {
@@ -358,7 +359,7 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
 // not the tile loop's.
 
 // -inf over the scores of one row's 64 keys from h0 on (TMEM columns tS ..)
-// that the row does not see or whose page is none; returns the largest other score (NaN if one is).
+// that the row does not see or whose page is none; returns the largest other score.
 __device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int sink, uint32_t pages, int page_log2) {
   auto below = [](int x) { return x >= 64 ? ~0ull : (x <= 0 ? 0ull : (1ull << x) - 1); };
   unsigned long long v = below(rm.hi - h0) & (~below(rm.lo - h0) | below(sink - h0));
@@ -375,7 +376,7 @@ __device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int s
 #pragma unroll
     for (int k = 0; k < 32; ++k) r[k] = (vis >> k) & 1u ? r[k] : 0xff800000u;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
+    for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1]));
     if (!__all_sync(0xffffffffu, vis == 0xffffffffu)) ptx::tmem_st32(tS + cc * 32, r);
   }
   ptx::tmem_st_wait();
@@ -740,11 +741,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           ptx::tmem_ld32(tS, ra);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
           ptx::tmem_ld32(tS + 32, ra);
           ptx::tmem_ld_wait();
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mx = ptx::fmax3_nan(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
+          for (int k = 0; k < 16; ++k) mx = ptx::fmax3(mx, __uint_as_float(ra[2 * k]), __uint_as_float(ra[2 * k + 1]));
         } else {
           // some key of the tile is hidden from some row: those scores become
           // -inf in TMEM, and the rest of the tile's work needs no mask. Rows of no
@@ -759,11 +760,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         }
         float mo;
         if (!swap(mx, mo)) { ok = false; break; }
-        // a NaN score makes the maximum NaN, and with it the row's sum and output: the
-        // cubic's clamp would turn the NaN itself into 2^-126
-        const float m_new = ptx::fmax3_nan(m, mx, mo);
-        const bool need = !(m_new <= m + thresh);  // also true for the first visible tile
-        const bool real = need && m > -INFINITY;   // O already holds weighted values
+        const float m_new = ptx::fmax3(m, mx, mo);
+        const bool need = m_new > m + thresh;      // also true for the first visible tile
+        const bool real = need && m != -INFINITY;  // O already holds weighted values
         if (__any_sync(0xffffffffu, real)) {
           // PV of the previous tile is complete: it was issued before this
           // tile's S, which the wait above saw complete
@@ -785,7 +784,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         // P = 2^(s c - m c) as packed 16-bit pairs over the first 32 columns of
         // this half of S (already read): keys h0 + 2i, h0 + 2i + 1 -> column i.
         // P is rounded to the values' type, the product's operand: off by at most
-        // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it
+        // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it.
+        // Every exponential is the SFU's: with one pair in eight or two on the FMA pipe the
+        // video chunk takes 834 and 835 us instead of 819
         float sum = 0.f;
         auto emit = [&](const uint32_t (&r)[32], int k0) {
           uint32_t pk[16];
@@ -795,13 +796,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           for (int k = 0; k < 16; ++k) {
             const float2 x =
                 ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nmc2);
-            float2 e;
-            if ((k & 7) < kCubicPairs) {
-              e = exp2_cubic2(x);
-            } else {
-              e.x = ptx::ex2(x.x);
-              e.y = ptx::ex2(x.y);
-            }
+            const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             s2 = ptx::fadd2(s2, e);
             pk[k] = ptx::pack16x2<BF16>(e.x, e.y);
           }
@@ -838,15 +833,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       // pass's result or to this CTA's partial slot); each warp writes its D/2 columns
       float l_other = 0.f;
       if (ok && !swap(l, l_other)) ok = false;
-      // a maximum of +inf: inf - inf, which the clamp hides as it does NaN
-      const float lt = m == INFINITY ? NAN : l + l_other;
+      const float lt = l + l_other;
       const bool have_o =
           ok && n_tiles > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
       if (n_tiles > 0) ++nj;
       ptx::tc_fence_after();
-      // a row that saw nothing kept m = -inf (the cubic turns its scores into
-      // 2^-126, not 0): zeros and -inf; a NaN sum stays NaN
-      const bool none = m == -INFINITY && lt == lt;
+      // a row that saw nothing has l = 0: zeros and -inf; a NaN sum stays NaN
+      const bool none = lt == 0.f;
       const float inv_l = none ? 0.f : 1.f / lt;
       const float lse2 = none ? -INFINITY : m * c + log2f(lt);
       const int qi = grp * tpt + row / p.G, tok = jb.q0 + qi, head = jb.head0 + row % p.G;

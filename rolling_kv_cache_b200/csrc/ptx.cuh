@@ -301,13 +301,6 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
-// The same, NaN if any of the three is.
-__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
-
 // Drops the 128-byte L2 line at p (128-byte aligned, global memory) without
 // writing it back: for scratch that has been read for the last time.
 __device__ __forceinline__ void discard_l2(const void* p) {

@@ -104,8 +104,8 @@ def attend(bt, f=1, sinks=0, window=0, scale=None, prefix=None):
 
     The bounds: a score is a sum of d exact products in fp32 (each addition off by at most
     2^-23 of the terms' sum of magnitudes) and the multiplication to base 2; its error dx is
-    a relative error of its weight. The exponential adds at most 2^-13 (its cubic is within
-    7.5e-5; the stale maximum cancels), a weight's rounding to the type UNIT, the sums of n
+    a relative error of its weight. The exponential is allowed 2^-13 (the hardware's is far
+    within it; the stale maximum cancels), a weight's rounding to the type UNIT, the sums of n
     terms in fp32 n 2^-23, all relative to the sum of |weights values| A; the division
     and the merge of parts a few 2^-22; the output's rounding UNIT of the value."""
     hq, hk, d, dt = bt.hq, bt.hk, bt.d, bt.dtype

@@ -1,8 +1,6 @@
 """Paged-cache operators without a GPU: refusals of the C entries and of the Python functions, struct
-layouts, rotation tables, and the exponential that two kernels share."""
+layouts, and rotation tables."""
 import ctypes
-import os
-import re
 
 import numpy as np
 import pytest
@@ -13,7 +11,6 @@ from rolling_kv_cache_b200 import paged
 
 from test_abi import _header_layout
 
-CSRC = os.path.join(os.path.dirname(os.path.abspath(B.__file__)), "csrc")
 P = 1 << 20  # an aligned address that nothing reads: every call here is refused before a launch
 
 
@@ -172,15 +169,6 @@ def test_rope_tables_match_the_librarys():
             assert np.max(np.abs(B.rc_rope_table(h, axis) - t.numpy().ravel())) <= 2.0 ** -24
     finally:
         B.rc_cache_destroy(h)
-
-
-def test_both_attention_kernels_use_one_exponential():
-    """The cubic's pins (its fit and its bound) are read from attn_fwd.cu; the paged kernel's is the same text."""
-    def body(name):
-        text = open(os.path.join(CSRC, name)).read()
-        return re.search(r"float2 exp2_cubic2\(float2 x\) \{.*?\n\}", text, re.S).group(0)
-
-    assert body("attn_fwd.cu") == body("exp2_cubic.cuh")
 
 
 @pytest.mark.parametrize("name", ["cu_q", "kv_len", "page_table", "prefix_table", "status", "lse"])
