@@ -705,19 +705,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
     int gt = 0;  // the CTA's tiles so far (stage of K and V)
     int nj = 0;  // this group's jobs so far (phase of bar_o: one commit per job)
     int nx = 0;  // partner exchanges so far (phase of pbar, slot of swap_buf)
-    // writes v, returns the partner's value (bounded wait)
+    bool alive = true;
+    // A bounded wait, with one answer for the warp: lanes that gave up alone would leave
+    // the others at the next warp-wide step for good (and a warp that is whole again
+    // after each wait runs faster: video chunk 819 -> 811 us)
+    auto wait = [&](uint64_t* bar, int phase) {
+      alive = __all_sync(0xffffffffu, ptx::mbar_wait(bar, phase & 1, abort, p.status, RC_ETIMEOUT));
+      return alive;
+    };
+    // writes v, returns the partner's value
     auto swap = [&](float v, float& other) -> bool {
       float(*buf)[128] = swap_buf[grp][nx & 1];
       buf[ch][row] = v;
       ptx::mbar_arrive(pbar);
-      if (!ptx::mbar_wait(pbar, nx & 1, abort, p.status, RC_ETIMEOUT)) return false;
+      if (!wait(pbar, nx)) return false;
       ++nx;
       other = buf[ch ^ 1][row];
       return true;
     };
     for (int nw = 0;; ++nw) {
       const int slot = nw % kJobRing;
-      if (!ptx::mbar_wait(&bar_jf[slot], (nw / kJobRing) & 1, abort, p.status, RC_ETIMEOUT)) break;
+      if (!wait(&bar_jf[slot], nw / kJobRing)) break;
       const JobInfo& jb = jobs[slot];
       const int n_tiles = jb.tiles;
       if (n_tiles < 0) break;
@@ -728,9 +736,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         continue;
       }
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
-      bool ok = true;
       for (int left = n_tiles; left > 0; --left) {
-        if (!ptx::mbar_wait(&bar_s[grp], gs & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+        if (!wait(&bar_s[grp], gs)) break;
         ptx::tc_fence_after();
         const int4 info = tile_info[gt & 3];
         uint32_t ra[32];
@@ -759,7 +766,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
                            (uint32_t)info.y >> ((ch * 64) >> p.b.page_log2), p.b.page_log2);
         }
         float mo;
-        if (!swap(mx, mo)) { ok = false; break; }
+        if (!swap(mx, mo)) break;
         const float m_new = ptx::fmax3(m, mx, mo);
         const bool need = m_new > m + thresh;      // also true for the first visible tile
         const bool real = need && m != -INFINITY;  // O already holds weighted values
@@ -810,7 +817,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         // product start (a key that only later queries see is data, and meets P = 0)
         if (grp == 0 && tile_info[gt & 3].w) {
           const int st = gt & 1;
-          if (!ptx::mbar_wait(&bar_vf[st], (gt >> 1) & 1, abort, p.status, RC_ETIMEOUT)) { ok = false; break; }
+          if (!wait(&bar_vf[st], gt >> 1)) break;
           const int4 info = tile_info[gt & 3];
           const bool lead = info.y & kLeadTile;
           zero_values<D>(base + L::kV + st * L::kTile, info.x, lead ? 0 : jb.lo_min, lead ? p.lead_len : jb.L,
@@ -832,11 +839,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       // epilogue: O / l to the output (or, fp32 with its log2-sum-exp, to the prefix
       // pass's result or to this CTA's partial slot); each warp writes its D/2 columns
       float l_other = 0.f;
-      if (ok && !swap(l, l_other)) ok = false;
+      if (!alive || !swap(l, l_other)) break;
       const float lt = l + l_other;
-      const bool have_o =
-          ok && n_tiles > 0 && ptx::mbar_wait(&bar_o[grp], nj & 1, abort, p.status, RC_ETIMEOUT);
-      if (n_tiles > 0) ++nj;
+      const bool have_o = n_tiles > 0;
+      if (have_o && !wait(&bar_o[grp], nj)) break;
+      nj += have_o;
       ptx::tc_fence_after();
       // a row that saw nothing has l = 0: zeros and -inf; a NaN sum stays NaN
       const bool none = lt == 0.f;
@@ -896,7 +903,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           }
         }
       }
-      if (!ok) break;
     }
   }
   if (threadIdx.x == 0) ptx::grid_wait();  // in a chain, this grid ends after the one before it
