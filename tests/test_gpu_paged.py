@@ -871,3 +871,10 @@ def test_rows_before_the_first_sequence_are_left_and_reported(max_q, prefix):
     with pytest.raises(B.RcError) as e:
         paged.device_status()
     assert e.value.status == B.RC_ERANGE
+
+
+def test_cut_units_with_more_queries_than_max_q_says():
+    """Few rows all the same: the kernel computes them, and the merge of parts does too."""
+    for lens in ([(3, 9000)], [(4, 30), (3, 20000), (1, 5)]):
+        bt = Batch(85, lens, 8, 2, 64, 16)
+        assert_attend(paged.paged_attention(*bt.args(), max_q=1, return_lse=True), bt)
