@@ -214,15 +214,18 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
       (!m->prefix_table || (int64_t)m->prefix_pages * p->page_size < m->prefix_len || m->prefix_len > (1 << 30)))
     return invalid("prefix_table must list the pages of prefix_len tokens");
   if (!aligned4(m->prefix_table)) return invalid("misaligned prefix_table");
+  // The kernel for few rows while a unit's rows fit its one 16-row matrix step: 64
+  // streams of up to 16384 keys, 4 query heads a key head, take 355 us there and 494
+  // in the other kernel with one query each, 363 and 498 with four (16 rows).
   w->decode = (int64_t)std::max(1, m->max_q) * w->group <= rc::kDecodeRows;
   // A prefix and many rows: where the sequences fill their query tiles on their
   // own, each walks the prefix's tiles itself (the same products, the tiles from
   // L2, no second pass and no merge); where they do not, the whole batch's rows
   // are packed into tiles for a pass over the prefix. The line is a fill of 3/4 of
   // an average sequence's tile pairs: 48 sequences of 64-token pairs over 7021
-  // prefix tokens take 388 us in two passes and 394 walked at 48 tokens each, 476
-  // and 398 at 63, 194 and 347 at 16; 16 of 256-token pairs over 9360, 357 and 327
-  // at 200, 253 and 284 at 100.
+  // prefix tokens take 381 us in two passes and 379 walked at 48 tokens each, 466
+  // and 382 at 63, 191 and 338 at 16; 16 of 256-token pairs over 9360, 279 and 256
+  // at 200, 177 and 231 at 100.
   const int per_pair = 2 * (128 / w->group);
   const int64_t each = p->n_seqs > 0 ? ((int64_t)n_tok + p->n_seqs - 1) / p->n_seqs : 0;
   const int64_t room = (each + per_pair - 1) / per_pair * per_pair;
