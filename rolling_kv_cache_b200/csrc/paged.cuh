@@ -108,9 +108,9 @@ struct alignas(64) PagedAttnParams {
 constexpr int kDecodeRows = 16;
 constexpr int kPrefillRows = 256;
 
-cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 // chained: as a programmatic dependent of the kernel before it, whose results it does not read
-cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
+cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 // out from a decode pass over the sequences' own tokens (`own`) and a pass of the batch over their prefix (`pre`),
 // from whole results (pre_o, pre_lse of each) and parts alike. Launched as a programmatic dependent.
 cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams& pre, bool bf16, int head_dim,

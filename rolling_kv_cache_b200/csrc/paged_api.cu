@@ -191,6 +191,7 @@ struct Work {
   bool lead;      // a prefix is walked by every unit first
   bool two_pass;  // a prefix has a pass of its own
   int n_ctas, group;
+  int x_ctas;     // of the prefix's own pass
   size_t part_o, part_lse, rec, total;
   size_t x_part_o, x_part_lse, x_rec, pre_o, pre_lse;  // two passes: the prefix's parts and its result
   size_t own_o, own_lse;                                // and that over the sequences' own tokens
@@ -239,6 +240,10 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   int sms = 0;
   if (cudaError_t e = sm_count(&sms)) return cuda_failed(e, "device attribute");
   w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
+  // One SM is left to the pass that follows, whose first block is then in place and
+  // the rest start without delay as the prefix's end: 48 continuations 62 us with
+  // 147 CTAs (63 with 136 or 110), 68 with all 148
+  w->x_ctas = w->two_pass && w->decode ? std::max(1, w->n_ctas - 1) : w->n_ctas;
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -394,7 +399,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       return RC_OK;
     };
     auto prefill = [&](const rc::PagedAttnParams& x) -> rc_status {
-      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, false, s)) return cuda_failed(e, "paged attention launch");
+      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "paged attention launch");
       if (cudaError_t e = rc::launch_paged_combine(x, bf16, d, false, s)) return cuda_failed(e, "combine launch");
       return RC_OK;
     };
@@ -416,6 +421,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       x.b.max_pages = m->prefix_pages;
       x.b.table_stride = 0;
       x.batch_pass = 1;
+      x.n_ctas = w.x_ctas;
       x.prefix_len = m->prefix_len;
       x.mask = rc::MaskView{1 << 30, 0, 0};
       x.part_o = reinterpret_cast<float*>(ws + w.x_part_o);
@@ -434,10 +440,12 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
       return RC_OK;
     }
+    // the prefix first, its CTAs end together: 48 continuations 65 us the other way round, 62 so
+    if (w.two_pass)
+      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "prefix launch");
     if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
-    if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, s)) return cuda_failed(e, "paged attention launch");
+    if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, w.two_pass, s)) return cuda_failed(e, "paged attention launch");
     if (w.two_pass) {
-      if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, true, s)) return cuda_failed(e, "prefix launch");
       if (cudaError_t e = rc::launch_paged_join(p, x, bf16, d, s)) return cuda_failed(e, "join launch");
       return RC_OK;
     }

@@ -927,7 +927,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       }
     }
   }
-  if (threadIdx.x == 0) ptx::grid_wait();  // in a chain, this grid ends after the one before it
   ptx::tc_fence_before();
   __syncthreads();
   if (warp == kMmaWarp) {
@@ -937,7 +936,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
 }
 
 template <int D, bool BF16>
-cudaError_t launch_d(const PagedAttnParams& p, bool chained, cudaStream_t s) {
+cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
   static PerDevice attr_set;
   int done = 0;
   cudaError_t e = attr_set.get(&done, [](int, int* x) {
@@ -947,14 +946,14 @@ cudaError_t launch_d(const PagedAttnParams& p, bool chained, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   return launch_chained(paged_prefill_kernel<D, BF16>, p, dim3(p.n_ctas), kPreThreads, PreLayout<D>::kDynSmem,
-                        chained, s);
+                        false, s);
 }
 
 }  // namespace
 
-cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s) {
-  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, chained, s) : launch_d<64, false>(p, chained, s);
-  return bf16 ? launch_d<128, true>(p, chained, s) : launch_d<128, false>(p, chained, s);
+cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {
+  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
+  return bf16 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
 }
 
 }  // namespace rc

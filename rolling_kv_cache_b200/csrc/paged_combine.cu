@@ -138,12 +138,13 @@ struct JoinSide {
   const float* part_o;
   const float* part_lse;
   const int4* rec;
+  int n_ctas;
 };
 struct JoinParams {
   BatchView b;
   RowOutput to;
   JoinSide own, pre;
-  int n_tok, Hk, G, n_ctas;
+  int n_tok, Hk, G;
 };
 
 constexpr int kJoinSources = 2 * kMaxPersistentCtas + 2;
@@ -170,13 +171,15 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   const int pair0 = s.q0 / per_pair, pair1 = R > 0 ? (s.q0 + R / p.G - 1) / per_pair : pair0;
   if (tid < 3) {
     first_sh[tid] = -1;
-    last_sh[tid] = p.n_ctas - 1;
+    last_sh[tid] = (tid == 0 ? p.own : p.pre).n_ctas - 1;
   }
   ptx::grid_wait();
   if (R == 0) return;
   __syncthreads();
-  for (int c = tid; c < p.n_ctas; c += kCombThreads) {
-    const int4 x = __ldcg(p.own.rec + c), y = __ldcg(p.pre.rec + c);
+  const int most = max(p.own.n_ctas, p.pre.n_ctas);
+  for (int c = tid; c < most; c += kCombThreads) {
+    const int4 none = make_int4(0, 0, 0, 0);
+    const int4 x = c < p.own.n_ctas ? __ldcg(p.own.rec + c) : none, y = c < p.pre.n_ctas ? __ldcg(p.pre.rec + c) : none;
     if (x.z > 0 && x.y == s.q0 && x.w == h * p.G) first_sh[0] = c;
     if (y.z > 0 && y.y == pair0 * per_pair && y.w == h * p.G) first_sh[1] = c;
     if (y.z > 0 && y.y == pair1 * per_pair && y.w == h * p.G) first_sh[2] = c;
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
     there[1][c] = y.x;
   }
   __syncthreads();
-  for (int c = tid; c < p.n_ctas; c += kCombThreads)
+  for (int c = tid; c < most; c += kCombThreads)
     for (int k = 0; k < 3; ++k)
       if (first_sh[k] >= 0 && c > first_sh[k] && (there[k > 0][c] & kHeadEnds)) atomicMin(&last_sh[k], c);
   __syncthreads();
@@ -319,12 +322,11 @@ cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams&
   p.b = own.b;
   p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse, nullptr, nullptr, nullptr,
                    nullptr,      nullptr,            nullptr,             own.n_tok, own.Hk * own.G};
-  p.own = JoinSide{own.pre_o, own.pre_lse, own.part_o, own.part_lse, own.rec};
-  p.pre = JoinSide{pre.pre_o, pre.pre_lse, pre.part_o, pre.part_lse, pre.rec};
+  p.own = JoinSide{own.pre_o, own.pre_lse, own.part_o, own.part_lse, own.rec, own.n_ctas};
+  p.pre = JoinSide{pre.pre_o, pre.pre_lse, pre.part_o, pre.part_lse, pre.rec, pre.n_ctas};
   p.n_tok = own.n_tok;
   p.Hk = own.Hk;
   p.G = own.G;
-  p.n_ctas = own.n_ctas;
   if (head_dim == 64) return bf16 ? join_d<64, true>(p, s) : join_d<64, false>(p, s);
   return bf16 ? join_d<128, true>(p, s) : join_d<128, false>(p, s);
 }

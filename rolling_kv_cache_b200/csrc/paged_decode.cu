@@ -226,6 +226,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       int dummy = 0;
       for (int k = max(0, g - L::kStages); k < g; ++k)
         ptx::mbar_wait(&bar_full[k % L::kStages], (k / L::kStages) & 1, &dummy, p.status, RC_ETIMEOUT);
+      if (!is_v) ptx::grid_wait();  // in a chain, this grid ends after the one before it
     }
     return;
   }
@@ -458,7 +459,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 }  // namespace
 
 template <int D, bool BF16>
-static cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
+static cudaError_t launch_d(const PagedAttnParams& p, bool chained, cudaStream_t s) {
   static PerDevice attr_set;
   int done = 0;
   cudaError_t e = attr_set.get(&done, [](int, int* x) {
@@ -468,12 +469,12 @@ static cudaError_t launch_d(const PagedAttnParams& p, cudaStream_t s) {
   });
   if (e != cudaSuccess) return e;
   return launch_chained(paged_decode_kernel<D, BF16>, p, dim3(p.n_ctas), kDecThreads, DecLayout<D>::kDynSmem,
-                        false, s);
+                        chained, s);
 }
 
-cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s) {
-  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, s) : launch_d<64, false>(p, s);
-  return bf16 ? launch_d<128, true>(p, s) : launch_d<128, false>(p, s);
+cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s) {
+  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, chained, s) : launch_d<64, false>(p, chained, s);
+  return bf16 ? launch_d<128, true>(p, chained, s) : launch_d<128, false>(p, chained, s);
 }
 
 }  // namespace rc
