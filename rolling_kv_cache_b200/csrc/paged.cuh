@@ -102,6 +102,7 @@ struct alignas(64) PagedAttnParams {
   int box_rows;        // rows of a page per TMA box
   float scale_log2;    // log2(e) * scale
   int n_ctas;
+  int cluster;         // decode: CTAs that share a unit (1: the whole batch is cut evenly)
 };
 
 // part_o / part_lse rows of one unit in the two attention kernels

@@ -192,10 +192,13 @@ struct Work {
   bool two_pass;  // a prefix has a pass of its own
   int n_ctas, group;
   int x_ctas;     // of the prefix's own pass
+  int cluster;    // CTAs to a unit of the kernel for few rows; 1: cut evenly
   size_t part_o, part_lse, rec, total;
   size_t x_part_o, x_part_lse, x_rec, pre_o, pre_lse;  // two passes: the prefix's parts and its result
   size_t own_o, own_lse;                                // and that over the sequences' own tokens
 };
+
+constexpr int kClusterTiles = 16;
 
 rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_heads, Work* w) {
   rc::BatchView b;
@@ -244,6 +247,16 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   // the rest start without delay as the prefix's end: 48 continuations 62 us with
   // 147 CTAs (63 with 136 or 110), 68 with all 148
   w->x_ctas = w->two_pass && w->decode ? std::max(1, w->n_ctas - 1) : w->n_ctas;
+  // Few short units: a cluster of CTAs for each, which merges its parts in shared
+  // memory, one launch and no workspace.
+  w->cluster = 1;
+  if (w->decode && m->prefix_len == 0) {
+    int64_t keys = (int64_t)p->max_pages * p->page_size;
+    if (m->window_frames > 0)
+      keys = std::min(keys, ((int64_t)m->sink_frames + m->window_frames) * m->frame_seqlen + m->max_q + 64);
+    for (int c = 8; c > 1 && w->cluster == 1; c /= 2)
+      if ((int64_t)p->n_seqs * p->kv_heads * c <= w->n_ctas * 7 / 8 && keys <= (int64_t)c * kClusterTiles * 64) w->cluster = c;
+  }
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;
@@ -256,7 +269,8 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
     *pl = take(rows * 4);
     *rec = take((size_t)w->n_ctas * sizeof(int4));
   };
-  parts(w->decode ? rc::kDecodeRows : rc::kPrefillRows, &w->part_o, &w->part_lse, &w->rec);
+  if (w->cluster == 1)
+    parts(w->decode ? rc::kDecodeRows : rc::kPrefillRows, &w->part_o, &w->part_lse, &w->rec);
   if (w->two_pass) {
     // its own regions: the kernels of the call overlap at their ends
     parts(rc::kPrefillRows, &w->x_part_o, &w->x_part_lse, &w->x_rec);
@@ -360,7 +374,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
     Work w;
     if (rc_status st = plan_work(pg, m, n_tok, q->heads, &w)) return st;
     if (n_tok == 0 || pg->n_seqs == 0) return RC_OK;
-    if (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign)
+    if (w.total > 0 && (!workspace || reinterpret_cast<uintptr_t>(workspace) % kAlign))
       return invalid("the workspace must be 256-byte aligned");
     if (workspace_bytes < w.total) return SetLastError(RC_ENOMEM, "workspace smaller than rc_paged_workspace()");
     const bool bf16 = pg->dtype == RC_BF16;
@@ -379,6 +393,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
     p.Hk = pg->kv_heads;
     p.G = w.group;
     p.n_ctas = w.n_ctas;
+    p.cluster = w.cluster;
     const double scale = m->scale > 0.f ? (double)m->scale : 1.0 / std::sqrt((double)d);
     p.scale_log2 = (float)(1.4426950408889634 * scale);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -449,6 +464,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       if (cudaError_t e = rc::launch_paged_join(p, x, bf16, d, s)) return cuda_failed(e, "join launch");
       return RC_OK;
     }
+    if (w.cluster > 1) return RC_OK;
     if (cudaError_t e = rc::launch_paged_combine(p, bf16, d, true, s)) return cuda_failed(e, "combine launch");
     return RC_OK;
   });

@@ -109,17 +109,22 @@ __device__ __forceinline__ void block_prefix(T* pre, int n, T* warp_sums, Fn f) 
 // kernel calls grid_wait before it reads or overwrites what that one wrote, and before its last block ends.
 template <typename Params>
 inline cudaError_t launch_chained(void (*kernel)(const Params), const Params& p, dim3 grid, int threads, size_t smem,
-                                  bool chained, cudaStream_t s) {
+                                  bool chained, cudaStream_t s, int cluster = 1) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = chained ? 1 : 0;
+  cudaLaunchAttribute at[2]{};
+  if (chained) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[cfg.numAttrs++].val.programmaticStreamSerializationAllowed = 1;
+  }
+  if (cluster > 1) {
+    at[cfg.numAttrs].id = cudaLaunchAttributeClusterDimension;
+    at[cfg.numAttrs++].val.clusterDim = {(unsigned)cluster, 1, 1};
+  }
+  cfg.attrs = at;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 

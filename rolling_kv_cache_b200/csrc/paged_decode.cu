@@ -45,6 +45,7 @@ constexpr float kDecRescaleLog2 = 8.f;
 // What a unit costs beside its tiles, in tiles (its queries, its merge and its
 // writes: 4500 cycles to a tile's 1500)
 constexpr int kUnitCost = 3;
+constexpr int kMaxCluster = 8;
 
 template <int D>
 struct DecLayout {
@@ -110,7 +111,7 @@ struct DecWalk {
   }
 };
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool CLUSTER>
 __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __grid_constant__ PagedAttnParams p) {
   using L = DecLayout<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   __shared__ float wm[2][kConsumers][16], wl[2][kConsumers][16];
   __shared__ int warp_sums[kConsumers + 2];
   __shared__ int abort_sh, falls_sh;
+  __shared__ float own_lse[16];  // CLUSTER: of this CTA's tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* base = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
   const uint32_t base_u32 = ptx::smem_u32(base);
@@ -134,6 +136,26 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   }
   __syncthreads();
   ptx::grid_launch_dependents();
+  DecWalk walk;
+  DecUnit u, mine;
+  bool taken = false;
+  if constexpr (CLUSTER) {
+    // an equal share of one unit's tiles
+    const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
+    mine.b = unit / p.Hk;
+    mine.h = unit - mine.b * p.Hk;
+    const Seq s = load_seq(p.b, p.n_tok, mine.b);
+    if (s.n == 0) {  // the whole cluster returns
+      if (tid == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      return;
+    }
+    TileSpan<kTK> sp;
+    sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+    const int each = (sp.n + p.cluster - 1) / p.cluster;
+    mine.lo = min(rank * each, sp.n);
+    mine.hi = min(mine.lo + each, sp.n);
+    mine.total = sp.n;
+  } else {
   // tiles of each sequence, and this CTA's range of the batch's
   block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
     const Seq s = load_seq(p.b, p.n_tok, b);
@@ -147,10 +169,16 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   const int W = falls_sh ? 0 : p.Hk * pre[p.b.n_seqs];
   const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
   const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
-  volatile int* abort = &abort_sh;
-  DecWalk walk;
   walk.init(pre, p.b.n_seqs, p.Hk, pos, end);
-  DecUnit u;
+  }
+  auto next_unit = [&](DecUnit& v) {
+    if constexpr (!CLUSTER) return walk.next(v);
+    if (taken) return false;
+    taken = true;
+    v = mine;
+    return true;
+  };
+  volatile int* abort = &abort_sh;
 
   if (warp >= kConsumers) {
     // ----------------------------------------------------------- producers
@@ -179,11 +207,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     auto fetch = [&]() -> Batch {
       Batch t{0, 0, 0, -1, 0u};
       while (j >= n) {
-        if (!walk.next(u)) return t;
+        if (!next_unit(u)) return t;
         const Seq s = load_seq(p.b, p.n_tok, u.b);
         sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
         if (lane == 0 && s.bad && !is_v && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-        if (u.lo > 0) rec.x = kHasHead | (u.hi == u.total ? kHeadEnds : 0);
+        if (CLUSTER) {
+        } else if (u.lo > 0) rec.x = kHasHead | (u.hi == u.total ? kHeadEnds : 0);
         else if (u.hi < u.total) rec = make_int4(rec.x, s.q0, min(s.n, 16 / p.G), u.h * p.G);
         j = u.lo;
         n = min(u.hi, sp.n);
@@ -227,7 +256,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       now = next;
     }
     if (lane == 0) {
-      if (!is_v) p.rec[blockIdx.x] = rec;
+      if (!CLUSTER && !is_v) p.rec[blockIdx.x] = rec;
       // leave no copy in flight (bounded, whether or not the others gave up)
       int dummy = 0;
       for (int k = max(0, g - L::kStages); k < g; ++k)
@@ -264,7 +293,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       f[k][3] = r1 < rows ? __ldg(reinterpret_cast<const uint32_t*>(q1 + k * 32 + 16)) : 0u;
     }
   };
-  bool more = walk.next(u);
+  bool more = next_unit(u);
   if (more) {
     s = load_seq(p.b, p.n_tok, u.b);
     fetch(u, s, qf);
@@ -272,7 +301,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   while (more) {
     DecUnit un = u;
     Seq sn = s;
-    more = walk.next(un);
+    more = next_unit(un);
     if (more) sn = load_seq(p.b, p.n_tok, un.b);
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
@@ -448,7 +477,13 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       float lse2 = l == 0.f ? -INFINITY : gm * c + log2f(l);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] *= inv;
-      if (done.lo > 0 || done.hi < done.total) {
+      if constexpr (CLUSTER) {
+        // where this thread alone has read: the first buffer's place of the row
+        float4* dst = reinterpret_cast<float4*>(base + L::kMerge + (row * L::kOPad + col) * 4);
+        dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+        dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+        if (col == 0) own_lse[row] = lse2;
+      } else if (done.lo > 0 || done.hi < done.total) {
         const size_t at = (size_t)(2 * blockIdx.x + (done.lo > 0 ? 0 : 1)) * kDecodeRows + row;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
@@ -459,28 +494,66 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         store_row<D, BF16>(row_output(p), tok, head, col, acc, lse2);
       }
     }
+    if constexpr (CLUSTER) {
+      // O = sum_i 2^(lse_i - lse) O_i over the cluster's CTAs, by the first of them
+      ptx::cluster_sync();
+      if (row < R && (int)blockIdx.x % p.cluster == 0) {
+        const uint32_t at_lse = ptx::smem_u32(&own_lse[row]), at = base_u32 + L::kMerge + (row * L::kOPad + col) * 4;
+        float ls[kMaxCluster], m = -INFINITY, sum = 0.f, acc[8];
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          ls[r] = r < p.cluster ? ptx::cluster_ld(ptx::cluster_addr(at_lse, r)) : -INFINITY;
+          m = fmaxf(m, ls[r]);
+        }
+        if (m == -INFINITY) m = 0.f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          if (r >= p.cluster) continue;
+          const float w = exp2f(ls[r] - m);
+          const uint32_t src = ptx::cluster_addr(at, r);
+          const float4 x = ptx::cluster_ld4(src), y = ptx::cluster_ld4(src + 16);
+          const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+          sum += w;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], w, acc[k]);
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc[k] *= inv;
+        const int i = row / p.G;
+        store_row<D, BF16>(row_output(p), ds.q0 + i, done.h * p.G + row - i * p.G, col, acc,
+                           sum == 0.f ? -INFINITY : m + log2f(sum));
+      }
+      ptx::cluster_sync();  // no CTA's memory goes before it has been read
+    }
   }
 }
 
 }  // namespace
 
-template <int D, bool BF16>
+template <int D, bool BF16, bool CLUSTER>
 static cudaError_t launch_d(const PagedAttnParams& p, bool chained, cudaStream_t s) {
   static PerDevice attr_set;
   int done = 0;
   cudaError_t e = attr_set.get(&done, [](int, int* x) {
     *x = 1;
-    return cudaFuncSetAttribute(paged_decode_kernel<D, BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    return cudaFuncSetAttribute(paged_decode_kernel<D, BF16, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 (int)DecLayout<D>::kDynSmem);
   });
   if (e != cudaSuccess) return e;
-  return launch_chained(paged_decode_kernel<D, BF16>, p, dim3(p.n_ctas), kDecThreads, DecLayout<D>::kDynSmem,
-                        chained, s);
+  return launch_chained(paged_decode_kernel<D, BF16, CLUSTER>, p,
+                        dim3(CLUSTER ? p.b.n_seqs * p.Hk * p.cluster : p.n_ctas), kDecThreads, DecLayout<D>::kDynSmem,
+                        chained, s, CLUSTER ? p.cluster : 1);
 }
 
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s) {
-  if (head_dim == 64) return bf16 ? launch_d<64, true>(p, chained, s) : launch_d<64, false>(p, chained, s);
-  return bf16 ? launch_d<128, true>(p, chained, s) : launch_d<128, false>(p, chained, s);
+  const auto launch = p.cluster > 1 ? (head_dim == 64 ? (bf16 ? launch_d<64, true, true> : launch_d<64, false, true>)
+                                                      : (bf16 ? launch_d<128, true, true> : launch_d<128, false, true>))
+                                    : (head_dim == 64 ? (bf16 ? launch_d<64, true, false> : launch_d<64, false, false>)
+                                                      : (bf16 ? launch_d<128, true, false> : launch_d<128, false, false>));
+  return launch(p, chained, s);
 }
 
 }  // namespace rc

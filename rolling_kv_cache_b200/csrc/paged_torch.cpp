@@ -415,8 +415,9 @@ std::pair<Tensor, std::optional<Tensor>> attention(const Tensor& q, const Tensor
   size_t bytes = 0;
   check(rc_paged_workspace(&p, &m, n_tok, rq.heads, &bytes));
   // freed on return: the allocator hands it out again on this stream only
-  const Tensor work = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
-  check(rc_paged_attention(&p, &m, n_tok, &rq, &ro, lse ? lse->data_ptr<float>() : nullptr, work.data_ptr(), bytes,
+  Tensor work;
+  if (bytes) work = at::empty({static_cast<int64_t>(bytes)}, q.options().dtype(at::kByte));
+  check(rc_paged_attention(&p, &m, n_tok, &rq, &ro, lse ? lse->data_ptr<float>() : nullptr, bytes ? work.data_ptr() : nullptr, bytes,
                            status_word(dev.index), at::cuda::getCurrentCUDAStream(dev.index).stream()));
   if (out_) written(out);
   return {out, lse};

@@ -294,6 +294,31 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   else return pack_f16x2(lo, hi);
 }
 
+// All threads of the cluster that have not exited: what each wrote before, in its own
+// shared memory too, is seen by all behind it.
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release;\nbarrier.cluster.wait.acquire;" ::: "memory");
+}
+// The address of `addr` (this block's shared memory) in the memory of the cluster's block `rank`.
+__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ float cluster_ld(uint32_t addr) {
+  float r;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+  return r;
+}
+__device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {
+  float4 r;
+  asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+               : "r"(addr)
+               : "memory");
+  return r;
+}
+
 // Largest of three (max.f32 with three sources, sm_100 and later).
 __device__ __forceinline__ float fmax3(float a, float b, float c) {
   float r;

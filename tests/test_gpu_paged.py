@@ -236,6 +236,28 @@ def test_paged_attention_few_rows(case, dtype):
     assert_attend(got, bt, f=f, sinks=sinks, window=window)
 
 
+@pytest.mark.parametrize("case", DECODE)
+@pytest.mark.parametrize("dtype", [BF16, F16])
+def test_paged_attention_few_rows_in_a_wide_table(case, dtype):
+    """A table with room for long streams: the batch is cut evenly over the GPU, few short units too."""
+    lens, hq, hk, d, page, (f, sinks, window) = case
+    bt = Batch(22, lens, hq, hk, d, page, dtype, nhd=page == 32)
+    wide = torch.full((len(lens), 2 ** 18 // page), -7, dtype=torch.int32, device="cuda")
+    wide[:, :bt.page_table.shape[1]] = bt.page_table
+    bt.page_table = wide
+    got = paged.paged_attention(*bt.args(), max_q=max(a for a, _ in lens), frame_seqlen=f, sink_frames=sinks,
+                                window_frames=window, return_lse=True)
+    assert_attend(got, bt, f=f, sinks=sinks, window=window)
+
+
+@pytest.mark.parametrize("units", [1, 2, 16, 17, 32, 33, 64, 65])
+@pytest.mark.parametrize("n", [1, 64, 65, 449, 513, 1000])
+def test_single_tokens_by_the_number_of_units(units, n):
+    """Few short units are each shared by 8, 4 or 2 blocks, more are cut evenly: every count of tiles to a block."""
+    bt = Batch(23, [(1, n)] * units, 1, 1, 64, 16)
+    assert_attend(paged.paged_attention(*bt.args(), max_q=1, return_lse=True), bt)
+
+
 PREFILL = [
     ([(1, 1)], 1, 1, 64, 16, (1, 0, 0)),
     ([(17, 17)], 1, 1, 128, 16, (1, 0, 0)),
