@@ -10,7 +10,9 @@
 // the whole batch, in order, into one range per CTA (one CTA per SM), equal to
 // a tile, a unit's start and end counted as kUnitCost more: a ragged batch and a single long
 // sequence keep every SM reading alike. Each CTA finds its range from the lengths on the device. A unit cut
-// between CTAs leaves parts for the combine kernel.
+// between CTAs leaves parts for the combine kernel. Or, for few short units (CLUSTER), each unit's
+// tiles are shared equally by the CTAs of a cluster, whose first merges the others' results
+// out of their shared memory.
 //
 // Two warps (one for K, one for V) issue TMA copies of the tiles' pages (a box per page, its 64-dim
 // planes one after the other, 128-byte swizzle) into a ring of 128 KB, running ahead across units, so
@@ -25,8 +27,8 @@
 // Measured: 64 streams of 300 to 16384 tokens, 8 key heads of 128: 2.19 GB in 331 us,
 // 6.6 TB/s, the copy rate. A tile takes its group of warps 1500 cycles, a unit 5000
 // more (its place and lengths 1400, its queries 900, its merge and write 2700),
-// which the ring hides from HBM but not in units of a tile or two. 12 heads of one
-// stream of 777 tokens: 6.4 us.
+// which the ring hides from HBM but not in units of a tile or two. 12 heads of
+// one stream of 777 tokens, in clusters of 8: 6.6 us.
 //
 // Rows of a tile that no query of the unit sees (behind the sequence, before
 // the window, on a page that is not one) get weight 0 and their V fragments
@@ -156,20 +158,20 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     mine.hi = min(mine.lo + each, sp.n);
     mine.total = sp.n;
   } else {
-  // tiles of each sequence, and this CTA's range of the batch's
-  block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
-    const Seq s = load_seq(p.b, p.n_tok, b);
-    if (s.falls) falls_sh = 1;
-    if (s.n == 0) return 0;
-    TileSpan<kTK> sp;
-    sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-    return max(sp.n, 1) + kUnitCost;
-  });
-  if (falls_sh && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-  const int W = falls_sh ? 0 : p.Hk * pre[p.b.n_seqs];
-  const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
-  const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
-  walk.init(pre, p.b.n_seqs, p.Hk, pos, end);
+    // tiles of each sequence, and this CTA's range of the batch's
+    block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
+      const Seq s = load_seq(p.b, p.n_tok, b);
+      if (s.falls) falls_sh = 1;
+      if (s.n == 0) return 0;
+      TileSpan<kTK> sp;
+      sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
+      return max(sp.n, 1) + kUnitCost;
+    });
+    if (falls_sh && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+    const int W = falls_sh ? 0 : p.Hk * pre[p.b.n_seqs];
+    const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
+    const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
+    walk.init(pre, p.b.n_seqs, p.Hk, pos, end);
   }
   auto next_unit = [&](DecUnit& v) {
     if constexpr (!CLUSTER) return walk.next(v);
