@@ -89,6 +89,7 @@ struct Job {
   int tokens, at0;   // queries of the pair, position of the first
   int L, kv_lo, kv_hi, slot;
   bool has1, head, tail;  // head: begins inside the unit; tail: ends inside it
+  bool bad;               // of its sequence (Seq)
   int lead, total;        // tiles of the prefix that it walks first, and in all
   TileSpan<kTileRows> sp;
 };
@@ -212,6 +213,7 @@ struct PairWalk {
     j.h = h;
     j.q0 = s.q0 + pair * 2 * tpt;
     j.L = s.L;
+    j.bad = s.bad;
     j.kv_lo = lo;
     j.kv_hi = min(lo + len, j.total);
     j.has1 = j.tokens > tpt;
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           publish(-1);
           return false;
         }
-        if (lane == 0 && walk.s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+        if (lane == 0 && jb.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
         if (jb.head) rec.x = kHasHead | (jb.tail ? 0 : kHeadEnds);
         else if (jb.tail) rec = make_int4(rec.x, jb.q0, jb.tokens, jb.h * p.G);
         j = jb.kv_lo;

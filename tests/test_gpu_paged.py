@@ -294,8 +294,13 @@ PREFIX = [  # as above, and the prefix's length
     ([(300, 300), (513, 700), (260, 1000)], 2, 2, 128, 16, (1, 0, 0), 257),
     ([(640, 1280), (320, 320)], 4, 1, 64, 64, (160, 1, 3), 1000),
     ([(290, 290), (0, 5), (700, 900)], 4, 4, 64, 32, (1, 3, 40), 128),
-    # and those that do not, with the prefix in a pass of its own before a pass for many rows
+    # and so do short ones, where that is little work
     ([(30, 30)] * 12 + [(0, 9), (1, 77)], 6, 3, 128, 32, (1, 0, 0), 260),
+    # many short sequences: the prefix in a pass of its own before a pass for many rows
+    ([(20, 20)] * 70, 12, 12, 64, 16, (1, 0, 0), 500),
+    ([(5, 60)] * 60 + [(0, 3), (1, 1), (90, 300)], 32, 8, 128, 32, (1, 2, 30), 1000),
+    ([(16, 48)] * 50 + [(17, 20)], 24, 8, 64, 128, (16, 0, 2), 1111),
+    ([(30, 0)] * 40, 10, 10, 128, 64, (1, 0, 0), 700),
 ]
 
 
@@ -900,3 +905,23 @@ def test_cut_units_with_more_queries_than_max_q_says():
     for lens in ([(3, 9000)], [(4, 30), (3, 20000), (1, 5)]):
         bt = Batch(85, lens, 8, 2, 64, 16)
         assert_attend(paged.paged_attention(*bt.args(), max_q=1, return_lse=True), bt)
+
+
+def test_rows_before_the_first_of_many_short_sequences():
+    """As above, where two results are merged."""
+    lens, prefix = [(2, 2)] + [(20, 20)] * 70, 500
+    bt = Batch(86, lens, 12, 12, 64, 16, pad=3, spare=40)
+    table = torch.tensor(bt.free[:32], dtype=torch.int32, device="cuda")
+    j = torch.arange(prefix, device="cuda")
+    for pool in (bt.k_pages, bt.v_pages):
+        pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, prefix, 12, 64)
+    out = torch.full_like(bt.q, 7.0)
+    _, lse = paged.prefix_attention(bt.q, bt.k_pages, bt.v_pages, table, prefix, bt.cu_q[1:], bt.kv_len[1:],
+                                    bt.page_table[1:], max_q=20, out=out, return_lse=True)
+    assert bool((out[:2] == 7).all()) and bool((out[-3:] == 7).all())
+    bt.lens, bt.cu, bt.q, bt.page_table = bt.lens[1:], [n - 2 for n in bt.cu[1:]], bt.q[2:], bt.page_table[1:]
+    bt.n_tok -= 2
+    assert_attend((out[2:], lse[:, 2:]), bt, prefix=(table, prefix))
+    with pytest.raises(B.RcError) as e:
+        paged.device_status()
+    assert e.value.status == B.RC_ERANGE
