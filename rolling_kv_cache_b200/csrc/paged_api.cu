@@ -223,19 +223,7 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   // streams of up to 16384 keys, 4 query heads a key head, take 355 us there and 494
   // in the other kernel with one query each, 363 and 498 with four (16 rows).
   w->decode = (int64_t)std::max(1, m->max_q) * w->group <= rc::kDecodeRows;
-  // A prefix and many rows: where the sequences fill their query tiles on their
-  // own, each walks the prefix's tiles itself (the same products, the tiles from
-  // L2, no second pass and no merge); where they do not, the whole batch's rows
-  // are packed into tiles for a pass over the prefix. The line is a fill of 3/4 of
-  // an average sequence's tile pairs: 48 sequences of 64-token pairs over 7021
-  // prefix tokens take 381 us in two passes and 379 walked at 48 tokens each, 466
-  // and 382 at 63, 191 and 338 at 16; 16 of 256-token pairs over 9360, 279 and 256
-  // at 200, 177 and 231 at 100.
   const int per_pair = 2 * (128 / w->group);
-  const int64_t each = p->n_seqs > 0 ? ((int64_t)n_tok + p->n_seqs - 1) / p->n_seqs : 0;
-  const int64_t room = (each + per_pair - 1) / per_pair * per_pair;
-  w->lead = m->prefix_len > 0 && !w->decode && 4 * each >= 3 * room;
-  w->two_pass = m->prefix_len > 0 && !w->lead;
   // positions of the stream-K split are 32-bit: tiles of every unit, summed
   const int64_t tiles = ((int64_t)p->max_pages + (m->prefix_len > 0 ? m->prefix_pages : 0)) * p->page_size / 64 + 6;
   const int64_t pairs = (int64_t)n_tok / per_pair + p->n_seqs + 1;
@@ -244,6 +232,21 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   int sms = 0;
   if (cudaError_t e = sm_count(&sms)) return cuda_failed(e, "device attribute");
   w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
+  // A prefix and many rows: each sequence's units walk the prefix's tiles themselves
+  // (from L2; no second pass and no merge), or the whole batch's rows are packed into
+  // tiles for a pass over the prefix, and three kernels and the results in fp32 go on
+  // top. The first where what its units walk beside a packed pass's is no more than the second costs:
+  // per CTA 14 tiles and 20 bytes of traffic an element of q. In two passes and
+  // walked, us: 48 sequences, 64-token pairs, 7021 prefix tokens: 16 tokens each 191 and
+  // 338, 48 each 381 and 379, 63 each 466 and 382; 20 each over 300 prefix tokens 90 and 73, over
+  // 1500 115 and 120; 48 each over 30000 1112 and 1331. 256-token pairs: 6 sequences of 30
+  // over 5000 74 and 79; 16 of 100 over 3000 109 and 109, over 9360 177 and 231; 16 of 200
+  // over 9360 279 and 256, over 30000 621 and 683; 3 of 50 over 1000 61 and 35.
+  const int64_t each = p->n_seqs > 0 ? ((int64_t)n_tok + p->n_seqs - 1) / p->n_seqs : 0;
+  const int64_t walked = p->n_seqs * ((each + per_pair - 1) / per_pair), packed = ((int64_t)n_tok + per_pair - 1) / per_pair;
+  const double more = (double)(walked - packed) * p->kv_heads * ((m->prefix_len + 127) / 128);
+  w->lead = m->prefix_len > 0 && !w->decode && more <= w->n_ctas * (14 + 1.64e-6 * n_tok * q_heads * p->head_dim);
+  w->two_pass = m->prefix_len > 0 && !w->lead;
   // One SM is left to the pass that follows, whose first block is then in place and
   // the rest start without delay as the prefix's end: 48 continuations 62 us with
   // 147 CTAs (63 with 136 or 110), 68 with all 148
