@@ -202,6 +202,7 @@ struct Work {
 constexpr int kClusterTiles = 16;
 
 rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_heads, Work* w) {
+  *w = Work{};
   rc::BatchView b;
   if (rc_status st = check_paged(p, n_tok, &b)) return st;
   if (!m) return invalid("null mask");
@@ -464,10 +465,10 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
       return RC_OK;
     }
+    if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
     // the prefix first, its CTAs end together: 48 continuations 65 us the other way round, 62 so
     if (w.two_pass)
       if (cudaError_t e = rc::launch_paged_prefill(x, bf16, d, s)) return cuda_failed(e, "prefix launch");
-    if (rc_status st = maps(true, std::min(pg->page_size, 64))) return st;
     if (cudaError_t e = rc::launch_paged_decode(p, bf16, d, w.two_pass, s)) return cuda_failed(e, "paged attention launch");
     if (w.two_pass) {
       if (cudaError_t e = rc::launch_paged_join(p, x, bf16, d, s)) return cuda_failed(e, "join launch");
