@@ -85,8 +85,8 @@ struct alignas(64) PagedAttnParams {
   float* part_o;       // [2 * n_ctas][rows][d] fp32: parts of units cut between CTAs, each divided by its sum
   float* part_lse;     // [2 * n_ctas][rows], log2-sum-exp of each part
   int4* rec;           // [n_ctas] what of its range a CTA left in parts (PartRecord)
-  // A prefix that the whole batch sees. Prefill: lead_len > 0 tokens in the pages of lead_table, which
-  // every unit walks first.
+  // A prefix that the whole batch sees. Prefill, and decode in clusters: lead_len > 0 tokens in the pages of
+  // lead_table, which every unit walks first.
   const int32_t* lead_table;
   int lead_len;
   // Or in a pass of its own (batch_pass): one sequence of every query of the batch against keys [0, prefix_len) of

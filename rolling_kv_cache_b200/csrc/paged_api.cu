@@ -233,7 +233,23 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   int sms = 0;
   if (cudaError_t e = sm_count(&sms)) return cuda_failed(e, "device attribute");
   w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
-  // A prefix and many rows: each sequence's units walk the prefix's tiles themselves
+  // Few short units, by the table's width, the window and the prefix: a cluster of CTAs for each,
+  // which merges its parts in shared memory, in one launch and without a workspace. As
+  // many CTAs a unit as leave an eighth of the SMs spare (a cluster lies in one part of
+  // the GPU), and 16 tiles a CTA at most: 12 units of 777 keys take 10.2 us in
+  // clusters and 14.3 cut evenly, of 8000 18.4 and 20.4, of 16000 26.6 and 24.6; one unit
+  // of 4000 12.3 and 16.4, of 8000 16.8 and 16.7, of 12000 22.5 and 18.4; 60 units of
+  // 2000 18.4 and 22.5, of 8000 43.0 and 41.0.
+  w->cluster = 1;
+  if (w->decode) {
+    int64_t keys = (int64_t)p->max_pages * p->page_size;
+    if (m->window_frames > 0)
+      keys = std::min(keys, ((int64_t)m->sink_frames + m->window_frames) * m->frame_seqlen + m->max_q + 64);
+    keys += m->prefix_len;
+    for (int c = 8; c > 1 && w->cluster == 1; c /= 2)
+      if ((int64_t)p->n_seqs * p->kv_heads * c <= w->n_ctas * 7 / 8 && keys <= (int64_t)c * kClusterTiles * 64) w->cluster = c;
+  }
+  // A prefix and many rows (few rows: walked in clusters, else two passes): each sequence's units walk the prefix's tiles themselves
   // (from L2; no second pass and no merge), or the whole batch's rows are packed into
   // tiles for a pass over the prefix, and three kernels and the results in fp32 go on
   // top. The first where what its units walk beside a packed pass's is no more than the second costs:
@@ -246,27 +262,13 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   const int64_t each = p->n_seqs > 0 ? ((int64_t)n_tok + p->n_seqs - 1) / p->n_seqs : 0;
   const int64_t walked = p->n_seqs * ((each + per_pair - 1) / per_pair), packed = ((int64_t)n_tok + per_pair - 1) / per_pair;
   const double more = (double)(walked - packed) * p->kv_heads * ((m->prefix_len + 127) / 128);
-  w->lead = m->prefix_len > 0 && !w->decode && more <= w->n_ctas * (14 + 1.64e-6 * n_tok * q_heads * p->head_dim);
+  w->lead = m->prefix_len > 0 && (w->decode ? w->cluster > 1
+                                            : more <= w->n_ctas * (14 + 1.64e-6 * n_tok * q_heads * p->head_dim));
   w->two_pass = m->prefix_len > 0 && !w->lead;
   // One SM is left to the pass that follows, whose first block is then in place and
   // the rest start without delay as the prefix's end: 48 continuations 62 us with
   // 147 CTAs (63 with 136 or 110), 68 with all 148
   w->x_ctas = w->two_pass && w->decode ? std::max(1, w->n_ctas - 1) : w->n_ctas;
-  // Few short units, by the table's width and the window: a cluster of CTAs for each,
-  // which merges its parts in shared memory, in one launch and without a workspace. As
-  // many CTAs a unit as leave an eighth of the SMs spare (a cluster lies in one part of
-  // the GPU), and 16 tiles a CTA at most: 12 units of 777 keys take 10.2 us in
-  // clusters and 14.3 cut evenly, of 8000 18.4 and 20.4, of 16000 26.6 and 24.6; one unit
-  // of 4000 12.3 and 16.4, of 8000 16.8 and 16.7, of 12000 22.5 and 18.4; 60 units of
-  // 2000 18.4 and 22.5, of 8000 43.0 and 41.0.
-  w->cluster = 1;
-  if (w->decode && m->prefix_len == 0) {
-    int64_t keys = (int64_t)p->max_pages * p->page_size;
-    if (m->window_frames > 0)
-      keys = std::min(keys, ((int64_t)m->sink_frames + m->window_frames) * m->frame_seqlen + m->max_q + 64);
-    for (int c = 8; c > 1 && w->cluster == 1; c /= 2)
-      if ((int64_t)p->n_seqs * p->kv_heads * c <= w->n_ctas * 7 / 8 && keys <= (int64_t)c * kClusterTiles * 64) w->cluster = c;
-  }
   size_t o = 0;
   auto take = [&](size_t bytes) {
     const size_t at = o;

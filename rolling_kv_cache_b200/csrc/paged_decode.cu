@@ -141,8 +141,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   DecWalk walk;
   DecUnit u, mine;
   bool taken = false;
+  const int lead = CLUSTER ? (p.lead_len + kTK - 1) / kTK : 0;  // the prefix's tiles
   if constexpr (CLUSTER) {
-    // an equal share of one unit's tiles
+    // an equal share of one unit's tiles, a prefix's first
     const int unit = blockIdx.x / p.cluster, rank = blockIdx.x - unit * p.cluster;
     mine.b = unit / p.Hk;
     mine.h = unit - mine.b * p.Hk;
@@ -153,10 +154,10 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     }
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-    const int each = (sp.n + p.cluster - 1) / p.cluster;
-    mine.lo = min(rank * each, sp.n);
-    mine.hi = min(mine.lo + each, sp.n);
-    mine.total = sp.n;
+    mine.total = lead + sp.n;
+    const int each = (mine.total + p.cluster - 1) / p.cluster;
+    mine.lo = min(rank * each, mine.total);
+    mine.hi = min(mine.lo + each, mine.total);
   } else {
     // tiles of each sequence, and this CTA's range of the batch's
     block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
@@ -217,14 +218,18 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         } else if (u.lo > 0) rec.x = kHasHead | (u.hi == u.total ? kHeadEnds : 0);
         else if (u.hi < u.total) rec = make_int4(rec.x, s.q0, min(s.n, 16 / p.G), u.h * p.G);
         j = u.lo;
-        n = min(u.hi, sp.n);
+        n = min(u.hi, lead + sp.n);
       }
       t.tiles = min(in_batch, n - j);
       t.h = u.h;
-      t.k0 = sp.key(j + ahead) + box * p.box_rows;
-      const bool want = ahead < t.tiles && t.k0 < sp.hi_max &&
-                        (t.k0 + p.box_rows > sp.lo_min || (p.mask.window > 0 && t.k0 < p.mask.sink_tok));
-      if (want) t.page = __ldg(p.b.page_table + u.b * p.b.table_stride + (t.k0 >> p.b.page_log2));
+      const bool pre = CLUSTER && j + ahead < lead;
+      t.k0 = (pre ? (j + ahead) * kTK : sp.key(j + ahead - lead)) + box * p.box_rows;
+      const bool want = ahead < t.tiles &&
+                        (pre ? t.k0 < p.lead_len
+                             : t.k0 < sp.hi_max && (t.k0 + p.box_rows > sp.lo_min ||
+                                                    (p.mask.window > 0 && t.k0 < p.mask.sink_tok)));
+      const int32_t* table = pre ? p.lead_table : p.b.page_table + u.b * p.b.table_stride;
+      if (want) t.page = __ldg(table + (t.k0 >> p.b.page_log2));
       t.wanted = __ballot_sync(0xffffffffu, want);
       j += t.tiles;
       return t;
@@ -314,14 +319,15 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 #pragma unroll
     for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
     float mx0 = -INFINITY, mx1 = -INFINITY, l0 = 0.f, l1 = 0.f;
-    const int n = min(u.hi, sp.n);
+    const int n = min(u.hi, lead + sp.n);
     for (int j = u.lo; j < n && alive; ++j, ++g) {
       if ((g & 1) != grp) continue;
       const int st = g % L::kStages;
       alive = ptx::mbar_wait(&bar_full[st], (g / L::kStages) & 1, abort, p.status, RC_ETIMEOUT);
       alive = __all_sync(0xffffffffu, alive);
       if (!alive) break;
-      const int t0 = sp.key(j), w0 = t0 + kw;
+      const bool pre = CLUSTER && j < lead;
+      const int t0 = pre ? j * kTK : sp.key(j - lead), w0 = t0 + kw;
       const uint32_t sK = base_u32 + st * L::kStage, sV = sK + L::kTile;
       float x[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
       {
@@ -337,7 +343,9 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
       }
       // keep: bit pairs of this lane's 4 keys (w0 + cq, +1, +8, +9) that some row sees
       const uint32_t pages = readable[st];
-      const bool whole = w0 + 16 <= sp.hi_min && (w0 >= sp.lo_max || (p.mask.window > 0 && w0 + 16 <= p.mask.sink_tok)) &&
+      const bool whole = (pre ? w0 + 16 <= p.lead_len
+                              : w0 + 16 <= sp.hi_min &&
+                                    (w0 >= sp.lo_max || (p.mask.window > 0 && w0 + 16 <= p.mask.sink_tok))) &&
                          ((pages >> (kw / p.box_rows)) & 1u);
       uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
       if (!whole) {
@@ -349,11 +357,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             const int key = w0 + i * 8 + cq + e;
-            const bool v0 = page_ok && key < m0.hi && (key >= m0.lo || key < sink);
-            const bool v1 = page_ok && key < m1.hi && (key >= m1.lo || key < sink);
+            const bool v0 = page_ok && (pre ? key < p.lead_len : key < m0.hi && (key >= m0.lo || key < sink));
+            const bool v1 = page_ok && (pre ? key < p.lead_len : key < m1.hi && (key >= m1.lo || key < sink));
             if (!v0) x[i][e] = -INFINITY;
             if (!v1) x[i][2 + e] = -INFINITY;
-            if (page_ok && key < sp.hi_max && (key >= sp.lo_min || key < sink)) kb[i] |= 0xffffu << (16 * e);
+            if (page_ok && (pre ? key < p.lead_len : key < sp.hi_max && (key >= sp.lo_min || key < sink)))
+              kb[i] |= 0xffffu << (16 * e);
           }
         keep0 = kb[0];
         keep1 = kb[1];

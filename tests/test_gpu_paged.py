@@ -301,6 +301,13 @@ PREFIX = [  # as above, and the prefix's length
     ([(5, 60)] * 60 + [(0, 3), (1, 1), (90, 300)], 32, 8, 128, 32, (1, 2, 30), 1000),
     ([(16, 48)] * 50 + [(17, 20)], 24, 8, 64, 128, (16, 0, 2), 1111),
     ([(30, 0)] * 40, 10, 10, 128, 64, (1, 0, 0), 700),
+    # few single tokens, in clusters; and many, or a long prefix, in two passes
+    ([(1, 39)], 5, 1, 128, 32, (1, 0, 0), 6051),
+    ([(1, 259), (0, 7), (1, 0), (3, 90)], 4, 2, 64, 128, (1, 1, 40), 200),
+    ([(4, 25), (2, 8)], 16, 8, 128, 64, (1, 0, 0), 1030),
+    ([(1, 1000)], 3, 3, 64, 16, (16, 1, 5), 64),
+    ([(1, 7)] * 20, 12, 12, 128, 64, (1, 0, 0), 435),
+    ([(1, 30)], 1, 1, 64, 16, (1, 0, 0), 9000),
 ]
 
 

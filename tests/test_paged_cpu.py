@@ -204,7 +204,7 @@ def test_written_rows_that_overlap_are_refused():
 
 def test_written_rows_in_every_nesting_pass_the_checks():
     """Refused only for the workspace, which is looked at after the rows (or, without a GPU, for that)."""
-    m = B.rc_paged_mask(frame_seqlen=1, max_q=1, prefix_len=5, prefix_table=P, prefix_pages=1)
+    m = B.rc_paged_mask(frame_seqlen=1, max_q=100)  # many rows: a workspace is needed
     for tok, head in ((256, 64), (64, 192), (320, 72), (512, 128), (72, 256)):
         with pytest.raises(B.RcError, match="workspace|device attribute"):
             B.rc_paged_attention(_pool(), m, 3, _rows(), B.rc_rows(P, tok, head, 4), 0, 0, 0)
