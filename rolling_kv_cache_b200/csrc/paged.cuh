@@ -110,6 +110,8 @@ constexpr int kDecodeRows = 16;
 constexpr int kPrefillRows = 256;
 
 // chained: as a programmatic dependent of the kernel before it, whose results it does not read
+// How many clusters of 2^log2 CTAs of the decode kernel the current device runs at once.
+cudaError_t paged_decode_clusters(int log2, int* n);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 // out from a decode pass over the sequences' own tokens (`own`) and a pass of the batch over their prefix (`pre`),

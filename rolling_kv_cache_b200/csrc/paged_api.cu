@@ -235,19 +235,25 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   w->n_ctas = std::min(sms, rc::kMaxPersistentCtas);
   // Few short units, by the table's width, the window and the prefix: a cluster of CTAs for each,
   // which merges its parts in shared memory, in one launch and without a workspace. As
-  // many CTAs a unit as leave an eighth of the SMs spare (a cluster lies in one part of
-  // the GPU), and 16 tiles a CTA at most: 12 units of 777 keys take 10.2 us in
-  // clusters and 14.3 cut evenly, of 8000 18.4 and 20.4, of 16000 26.6 and 24.6; one unit
-  // of 4000 12.3 and 16.4, of 8000 16.8 and 16.7, of 12000 22.5 and 18.4; 60 units of
-  // 2000 18.4 and 22.5, of 8000 43.0 and 41.0.
+  // many CTAs a unit as run at once (a cluster lies in one part of the GPU: 15 of 8 CTAs fit; 16
+  // units take 17.1 us in clusters of 8 and 12.3 in clusters of 4), and 16 tiles a CTA at most:
+  // 12 units of 777 keys take 10.2 us in clusters and 14.3 cut evenly, of 8000 18.4 and
+  // 20.4, of 16000 26.6 and 24.6; one unit of 4000 12.3 and 16.4, of 8000 16.8 and 16.7, of
+  // 12000 22.5 and 18.4; 60 units of 2000 18.4 and 22.5, of 8000 43.0 and 41.0. With a
+  // prefix, whose other way is two passes and a join, 32 tiles: 8 units over 4000 prefix
+  // tokens 16.4 and 37, over 15000 28.7 and 53; 64 over 3300 27 and 39.
   w->cluster = 1;
   if (w->decode) {
     int64_t keys = (int64_t)p->max_pages * p->page_size;
     if (m->window_frames > 0)
       keys = std::min(keys, ((int64_t)m->sink_frames + m->window_frames) * m->frame_seqlen + m->max_q + 64);
     keys += m->prefix_len;
-    for (int c = 8; c > 1 && w->cluster == 1; c /= 2)
-      if ((int64_t)p->n_seqs * p->kv_heads * c <= w->n_ctas * 7 / 8 && keys <= (int64_t)c * kClusterTiles * 64) w->cluster = c;
+    const int64_t most = (m->prefix_len > 0 ? 2 : 1) * kClusterTiles * 64;
+    for (int log2 = 3; log2 > 0 && w->cluster == 1; --log2) {
+      int room = 0;
+      if (cudaError_t e = rc::paged_decode_clusters(log2, &room)) return cuda_failed(e, "cluster occupancy");
+      if ((int64_t)p->n_seqs * p->kv_heads <= room && keys <= (most << log2)) w->cluster = 1 << log2;
+    }
   }
   // A prefix and many rows (few rows: walked in clusters, else two passes): each sequence's units walk the prefix's tiles themselves
   // (from L2; no second pass and no merge), or the whole batch's rows are packed into

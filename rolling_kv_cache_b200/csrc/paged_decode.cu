@@ -559,6 +559,28 @@ static cudaError_t launch_d(const PagedAttnParams& p, bool chained, cudaStream_t
                         chained, s, CLUSTER ? p.cluster : 1);
 }
 
+cudaError_t paged_decode_clusters(int log2, int* n) {
+  static PerDevice cache[4];
+  if (log2 < 1 || log2 > 3) return cudaErrorInvalidValue;
+  auto query = [](int log2, int* x) {
+    const auto kernel = paged_decode_kernel<128, true, true>;
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)DecLayout<128>::kDynSmem);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(1u << log2);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.dynamicSmemBytes = DecLayout<128>::kDynSmem;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim = {1u << log2, 1, 1};
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    return cudaOccupancyMaxActiveClusters(x, kernel, &cfg);
+  };
+  return cache[log2].get(n, [&](int, int* x) { return query(log2, x); });
+}
+
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s) {
   const auto launch = p.cluster > 1 ? (head_dim == 64 ? (bf16 ? launch_d<64, true, true> : launch_d<64, false, true>)
                                                       : (bf16 ? launch_d<128, true, true> : launch_d<128, false, true>))

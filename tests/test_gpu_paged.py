@@ -308,6 +308,8 @@ PREFIX = [  # as above, and the prefix's length
     ([(1, 1000)], 3, 3, 64, 16, (16, 1, 5), 64),
     ([(1, 7)] * 20, 12, 12, 128, 64, (1, 0, 0), 435),
     ([(1, 30)], 1, 1, 64, 16, (1, 0, 0), 9000),
+    ([(1, 300), (3, 3)], 20, 5, 128, 32, (1, 0, 0), 40000),
+    ([(1, n) for n in range(1, 130, 2)], 8, 2, 64, 64, (1, 0, 0), 777),
 ]
 
 
@@ -790,12 +792,13 @@ def test_rows_listed_out_of_order_fault_nothing():
         pass
 
 
-def test_a_nan_in_the_prefix_reaches_every_row_and_reads_no_part_that_is_none():
+@pytest.mark.parametrize("pages", [190, 300])  # in clusters, in two passes
+def test_a_nan_in_the_prefix_reaches_every_row_and_reads_no_part_that_is_none(pages):
     """Rows whose sum is NaN, with parts of unequal number on both sides of a pair of query tiles."""
     lens = [(1, 70)] + [(2, 40)] * 31 + [(1, 0)]  # 8 heads a key head: 32 queries a pair, the 16th of the twos in both
-    bt = Batch(79, lens, 8, 1, 64, 16, spare=200)
-    n = 16 * 190 + 3
-    table = torch.tensor(bt.free[:191], dtype=torch.int32, device="cuda")
+    bt = Batch(79, lens, 8, 1, 64, 16, spare=pages + 10)
+    n = 16 * pages + 3
+    table = torch.tensor(bt.free[:pages + 1], dtype=torch.int32, device="cuda")
     j = torch.arange(n, device="cuda")
     for pool in (bt.k_pages, bt.v_pages):
         pool[table[j // 16].long(), :, j % 16] = randn(bt.gen, n, 1, 64)
