@@ -482,7 +482,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
 #pragma unroll
       for (int w = 0; w < kConsumers; ++w) gm = fmaxf(gm, um[w][row]);
 #pragma unroll
-      for (int w = 0; w < kConsumers; ++w) l += um[w][row] == -INFINITY ? 0.f : ul[w][row] * ptx::ex2((um[w][row] - gm) * c);
+      for (int w = 0; w < kConsumers; ++w)  // a warp without a maximum: 0, or NaN of NaN scores
+        l += um[w][row] == -INFINITY ? ul[w][row] : ul[w][row] * ptx::ex2((um[w][row] - gm) * c);
       // a row that sees nothing has l = 0: zeros and -inf; a NaN sum stays NaN
       const float inv = l == 0.f ? 0.f : 1.f / l;
       float lse2 = l == 0.f ? -INFINITY : gm * c + log2f(l);
