@@ -154,7 +154,7 @@ __device__ __forceinline__ void merge_prev(const RowOutput& p, int tok, int head
                                            float& lse2) {
   const float pl = __ldcg(p.prev_lse + (size_t)head * p.n_tok + tok);
   const float m = fmaxf(lse2, pl);
-  if (m == -INFINITY) return;  // neither side saw a key
+  if (m == -INFINITY && pl == m) return;  // the prefix's side saw no key (fmaxf passes over a NaN)
   const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.heads + head) * D + col);
   const float4 a = __ldcg(src), b = __ldcg(src + 1);
   const float w = exp2f(lse2 - m), wp = exp2f(pl - m), inv = 1.f / (w + wp);

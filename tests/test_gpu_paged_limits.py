@@ -83,3 +83,18 @@ def test_a_nan_key_of_a_sequence_behind_a_prefix(case):
     o, lse = _attend(bt, max_q, prefix)
     assert bool(o[hit].isnan().all()) and bool(lse.T[hit].isnan().all())
     assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse.T[~hit], wl.T[~hit])
+
+
+@pytest.mark.parametrize("case", PREFIXES, ids=["clusters", "join", "merge", "walked"])
+def test_a_nan_key_of_the_prefix_reaches_sequences_without_tokens(case):
+    hq, hk, d, page, rest, n, max_q = case
+    bt = Batch(103, [(1, 0)] + rest[:-1] + [(rest[-1][0], 0)], hq, hk, d, page, spare=(n + page - 1) // page + 1)
+    prefix = _prefix(bt, n)
+    want, wl = _attend(bt, max_q, prefix)
+    assert bool(torch.isfinite(want).all()) and bool(torch.isfinite(wl).all())
+    bt.k_pages[int(prefix[0][-1]), 1, (n - 1) % page, 3] = NAN
+    hit = torch.zeros(bt.n_tok, hq, dtype=torch.bool, device="cuda")
+    hit[:, hq // hk:2 * (hq // hk)] = True
+    o, lse = _attend(bt, max_q, prefix)
+    assert bool(o[hit].isnan().all()) and bool(lse.T[hit].isnan().all())
+    assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse.T[~hit], wl.T[~hit])
