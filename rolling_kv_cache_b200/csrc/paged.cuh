@@ -109,9 +109,10 @@ struct alignas(64) PagedAttnParams {
 constexpr int kDecodeRows = 16;
 constexpr int kPrefillRows = 256;
 
-// chained: as a programmatic dependent of the kernel before it, whose results it does not read
-// How many clusters of 2^log2 CTAs of the decode kernel the current device runs at once.
+// How many clusters of 2^log2 CTAs of the decode kernel the current device runs at once (asked of one of its
+// instantiations: every one has an SM to a CTA, by its shared memory).
 cudaError_t paged_decode_clusters(int log2, int* n);
+// chained: as a programmatic dependent of the kernel before it, whose results it does not read
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 // out from a decode pass over the sequences' own tokens (`own`) and a pass of the batch over their prefix (`pre`),

@@ -324,7 +324,7 @@ cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams&
                               cudaStream_t s) {
   JoinParams p{};
   p.b = own.b;
-  p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse, nullptr, nullptr, nullptr,
+  p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse,   nullptr,
                    nullptr,      nullptr,            nullptr,             own.n_tok, own.Hk * own.G};
   p.own = JoinSide{own.pre_o, own.pre_lse, own.part_o, own.part_lse, own.rec, own.n_ctas};
   p.pre = JoinSide{pre.pre_o, pre.pre_lse, pre.part_o, pre.part_lse, pre.rec, pre.n_ctas};

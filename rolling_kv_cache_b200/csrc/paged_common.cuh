@@ -137,14 +137,12 @@ struct RowOutput {
   const float* prev_lse;
   float* pre_o;
   float* pre_lse;
-  float* part_o;
-  float* part_lse;
   int n_tok, heads;
 };
 
 __device__ __forceinline__ RowOutput row_output(const PagedAttnParams& p) {
-  return RowOutput{p.out.data, p.out.tok_stride, p.out.head_stride, p.lse,    p.prev_o, p.prev_lse,
-                   p.pre_o,    p.pre_lse,        p.part_o,          p.part_lse, p.n_tok,  p.Hk * p.G};
+  return RowOutput{p.out.data, p.out.tok_stride, p.out.head_stride, p.lse,  p.prev_o,
+                   p.prev_lse, p.pre_o,          p.pre_lse,         p.n_tok, p.Hk * p.G};
 }
 
 // Merges 8 columns of a row (divided by its sum; lse2 its log2-sum-exp) with
