@@ -83,7 +83,7 @@ struct alignas(64) PagedAttnParams {
   float* lse;          // [q_heads][n_tok] or null
   int* status;
   float* part_o;       // [2 * n_ctas][rows][d] fp32: parts of units cut between CTAs, each divided by its sum
-  float* part_lse;     // [2 * n_ctas][rows], log2-sum-exp of each part
+  float2* part_sum;    // [2 * n_ctas][rows], each part's sum of exponentials (RowSum)
   int4* rec;           // [n_ctas] what of its range a CTA left in parts (PartRecord)
   // A prefix that the whole batch sees. Prefill, and decode in clusters: lead_len > 0 tokens in the pages of
   // lead_table, which every unit walks first.
@@ -92,12 +92,12 @@ struct alignas(64) PagedAttnParams {
   // Or in a pass of its own (batch_pass): one sequence of every query of the batch against keys [0, prefix_len) of
   // table row 0.
   int batch_pass, prefix_len;
-  // null, or where the result goes instead of out and lse: fp32 [n_tok][q_heads][d], log2 [q_heads][n_tok]
+  // null, or where the result goes instead of out and lse: fp32 [n_tok][q_heads][d], RowSum [q_heads][n_tok]
   float* pre_o;
-  float* pre_lse;
-  // the merge kernel's: such a result that it merges with pre_o, pre_lse
+  float2* pre_sum;
+  // the merge kernel's: such a result that it merges with pre_o, pre_sum
   const float* prev_o;
-  const float* prev_lse;
+  const float2* prev_sum;
   int n_tok, Hk, G;
   int box_rows;        // rows of a page per TMA box
   float scale_log2;    // log2(e) * scale
@@ -105,7 +105,7 @@ struct alignas(64) PagedAttnParams {
   int cluster;         // decode: CTAs that share a unit (1: the whole batch is cut evenly)
 };
 
-// part_o / part_lse rows of one unit in the two attention kernels
+// part_o / part_sum rows of one unit in the two attention kernels
 constexpr int kDecodeRows = 16;
 constexpr int kPrefillRows = 256;
 
@@ -116,10 +116,10 @@ cudaError_t paged_decode_clusters(int log2, int* n);
 cudaError_t launch_paged_decode(const PagedAttnParams& p, bool bf16, int head_dim, bool chained, cudaStream_t s);
 cudaError_t launch_paged_prefill(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 // out from a decode pass over the sequences' own tokens (`own`) and a pass of the batch over their prefix (`pre`),
-// from whole results (pre_o, pre_lse of each) and parts alike. Launched as a programmatic dependent.
+// from whole results (pre_o, pre_sum of each) and parts alike. Launched as a programmatic dependent.
 cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams& pre, bool bf16, int head_dim,
                               cudaStream_t s);
-// out = the merge of two results in fp32 (prev_o, prev_lse; pre_o, pre_lse), for the rows of sequences.
+// out = the merge of two results in fp32 (prev_o, prev_sum; pre_o, pre_sum), for the rows of sequences.
 cudaError_t launch_paged_merge(const PagedAttnParams& p, bool bf16, int head_dim, cudaStream_t s);
 cudaError_t launch_paged_combine(const PagedAttnParams& p, bool bf16, int head_dim, bool decode, cudaStream_t s);
 

@@ -193,9 +193,9 @@ struct Work {
   int n_ctas, group;
   int x_ctas;     // of the prefix's own pass
   int cluster;    // CTAs to a unit of the kernel for few rows; 1: cut evenly
-  size_t part_o, part_lse, rec, total;
-  size_t x_part_o, x_part_lse, x_rec, pre_o, pre_lse;  // two passes: the prefix's parts and its result
-  size_t own_o, own_lse;                                // and that over the sequences' own tokens
+  size_t part_o, part_sum, rec, total;
+  size_t x_part_o, x_part_sum, x_rec, pre_o, pre_sum;  // two passes: the prefix's parts and its result
+  size_t own_o, own_sum;                                // and that over the sequences' own tokens
 };
 
 // Tiles of 64 keys that a CTA of a cluster takes at most (plan_work)
@@ -213,7 +213,8 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
   if (m->sink_frames < 0 || m->window_frames < 0) return invalid("sink_frames and window_frames must not be negative");
   if (m->sink_frames > 0 && m->window_frames == 0) return invalid("sink_frames need a window");
   if (m->max_q < 0) return invalid("max_q must not be negative");
-  // within these bounds its product with the log2 of e, and what is divided by that, are finite and normal
+  // within these bounds its product with the log2 of e, and what is divided by that, are finite and normal; an
+  // exponential's argument is the product of that with a difference of scores, which is right at either end
   if (m->scale != 0.f && !(m->scale >= 1e-30f && m->scale <= 1e30f)) return invalid("scale must be 0 or in [1e-30, 1e30]");
   if (m->prefix_len < 0 || m->prefix_pages < 0) return invalid("prefix_len must not be negative");
   if (m->prefix_len > 0 &&
@@ -281,21 +282,21 @@ rc_status plan_work(const rc_paged* p, const rc_paged_mask* m, int n_tok, int q_
     o += align_up(bytes);
     return at;
   };
-  auto parts = [&](int unit_rows, size_t* po, size_t* pl, size_t* rec) {
+  auto parts = [&](int unit_rows, size_t* po, size_t* ps, size_t* rec) {
     const size_t rows = (size_t)2 * w->n_ctas * unit_rows;
     *po = take(rows * p->head_dim * 4);
-    *pl = take(rows * 4);
+    *ps = take(rows * sizeof(float2));
     *rec = take((size_t)w->n_ctas * sizeof(int4));
   };
   if (w->cluster == 1)
-    parts(w->decode ? rc::kDecodeRows : rc::kPrefillRows, &w->part_o, &w->part_lse, &w->rec);
+    parts(w->decode ? rc::kDecodeRows : rc::kPrefillRows, &w->part_o, &w->part_sum, &w->rec);
   if (w->two_pass) {
     // its own regions: the kernels of the call overlap at their ends
-    parts(rc::kPrefillRows, &w->x_part_o, &w->x_part_lse, &w->x_rec);
+    parts(rc::kPrefillRows, &w->x_part_o, &w->x_part_sum, &w->x_rec);
     w->pre_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
-    w->pre_lse = take((size_t)n_tok * q_heads * 4);
+    w->pre_sum = take((size_t)n_tok * q_heads * sizeof(float2));
     w->own_o = take((size_t)n_tok * q_heads * p->head_dim * 4);
-    w->own_lse = take((size_t)n_tok * q_heads * 4);
+    w->own_sum = take((size_t)n_tok * q_heads * sizeof(float2));
   }
   w->total = o;
   return RC_OK;
@@ -405,7 +406,7 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
     p.lse = lse;
     p.status = status;
     p.part_o = reinterpret_cast<float*>(ws + w.part_o);
-    p.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    p.part_sum = reinterpret_cast<float2*>(ws + w.part_sum);
     p.rec = reinterpret_cast<int4*>(ws + w.rec);
     p.n_tok = n_tok;
     p.Hk = pg->kv_heads;
@@ -458,18 +459,18 @@ rc_status rc_paged_attention(const rc_paged* pg, const rc_paged_mask* m, int n_t
       x.prefix_len = m->prefix_len;
       x.mask = rc::MaskView{1 << 30, 0, 0};
       x.part_o = reinterpret_cast<float*>(ws + w.x_part_o);
-      x.part_lse = reinterpret_cast<float*>(ws + w.x_part_lse);
+      x.part_sum = reinterpret_cast<float2*>(ws + w.x_part_sum);
       x.rec = reinterpret_cast<int4*>(ws + w.x_rec);
       x.pre_o = reinterpret_cast<float*>(ws + w.pre_o);
-      x.pre_lse = reinterpret_cast<float*>(ws + w.pre_lse);
+      x.pre_sum = reinterpret_cast<float2*>(ws + w.pre_sum);
       p.pre_o = reinterpret_cast<float*>(ws + w.own_o);
-      p.pre_lse = reinterpret_cast<float*>(ws + w.own_lse);
+      p.pre_sum = reinterpret_cast<float2*>(ws + w.own_sum);
     }
     if (!w.decode) {
       if (rc_status st = prefill(x)) return st;
       if (rc_status st = prefill(p)) return st;
       p.prev_o = x.pre_o;
-      p.prev_lse = x.pre_lse;
+      p.prev_sum = x.pre_sum;
       if (cudaError_t e = rc::launch_paged_merge(p, bf16, d, s)) return cuda_failed(e, "merge launch");
       return RC_OK;
     }

@@ -57,6 +57,9 @@ constexpr int kProducerWarp = 16;
 constexpr int kMmaWarp = 17;
 constexpr int kPreThreads = 18 * 32;
 constexpr float kRescaleLog2 = 8.0f;
+// A row's reference c m is rounded, to R. Below this its rounding is at most 1, and the row's sums
+// stand for what they are times 2^R; beyond, for that times 2^(c m), whose exponents take more steps (steep_scores).
+constexpr float kSteepLog2 = 16777216.f;
 constexpr int kMaxRounds = 64;
 // What a unit costs beside its tiles, in tiles (its queries, its first tile's
 // start and its last writes; ragged prompts 254 us with 1, 246 with 2, 3 or 4)
@@ -83,7 +86,7 @@ struct PreLayout {
 
 // KV tiles [kv_lo, kv_hi) of one pair of query tiles of key head h of
 // sequence b. slot >= 0: the job covers part of its unit and leaves
-// (O / l, log2-sum-exp) in that slot; slot < 0: it writes the output.
+// (O / l, its RowSum) in that slot; slot < 0: it writes the output.
 struct Job {
   int b, h, q0;      // q0: row of q of the pair's first query
   int tokens, at0;   // queries of the pair, position of the first
@@ -409,6 +412,32 @@ __device__ __noinline__ float mask_scores(uint32_t tS, int h0, RowMask rm, int s
   }
   ptx::tmem_st_wait();
   return mx;
+}
+
+// c m - R of a row's reference (see kSteepLog2)
+__device__ __forceinline__ float reference_gap(float m, float c) {
+  const float r = m * c;
+  return fabsf(r) < kSteepLog2 ? fmaf(m, c, -r) : 0.f;
+}
+
+// Writes the exponents of one row's 64 scores (TMEM columns tS ..) over them, where some row's of the warp
+// is steep: the difference first, so that the product's rounding is relative to the exponent.
+__device__ __noinline__ void steep_scores(uint32_t tS, float m, float c) {
+  const float r = m * c;
+  const bool steep = !(fabsf(r) < kSteepLog2);
+#pragma unroll 1
+  for (int cc = 0; cc < 64; cc += 16) {
+    uint32_t s[16];
+    ptx::tmem_ld16(tS + cc, s);
+    ptx::tmem_ld_wait();
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const float x = __uint_as_float(s[k]);
+      s[k] = __float_as_uint(steep ? (x - m) * c : fmaf(x, c, -r));
+    }
+    ptx::tmem_st16(tS + cc, s);
+  }
+  ptx::tmem_st_wait();
 }
 
 // Zeros the V rows of a tile (from key t0 on, one row to two threads) outside [lo, hi) and the sinks.
@@ -764,6 +793,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         continue;
       }
       float m = -INFINITY, l = 0.f;  // l: this half's share of the row sum
+      bool steep = false;            // some row of the warp is (kSteepLog2)
       for (int left = n_tiles; left > 0; --left) {
         if (!wait(&bar_s[grp], gs)) break;
         ptx::tc_fence_after();
@@ -798,39 +828,51 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         const float m_new = ptx::fmax3(m, mx, mo);
         const bool need = m_new > m + thresh;      // also true for the first visible tile
         const bool real = need && m != -INFINITY;  // O already holds weighted values
-        if (__any_sync(0xffffffffu, real)) {
-          // PV of the previous tile is complete: it was issued before this
-          // tile's S, which the wait above saw complete
-          const float alpha = real ? ptx::ex2((m - m_new) * c) : 1.f;
+        if (__any_sync(0xffffffffu, need)) {
+          if (__any_sync(0xffffffffu, real)) {
+            // PV of the previous tile is complete: it was issued before this
+            // tile's S, which the wait above saw complete
+            const float alpha = real ? ptx::ex2(fmaf(m - m_new, c, reference_gap(m_new, c) - reference_gap(m, c))) : 1.f;
 #pragma unroll
-          for (int cc = 0; cc < D / 64; ++cc) {
-            uint32_t o[32];
-            ptx::tmem_ld32(tO + cc * 32, o);
-            ptx::tmem_ld_wait();
+            for (int cc = 0; cc < D / 64; ++cc) {
+              uint32_t o[32];
+              ptx::tmem_ld32(tO + cc * 32, o);
+              ptx::tmem_ld_wait();
 #pragma unroll
-            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
-            ptx::tmem_st32(tO + cc * 32, o);
+              for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * alpha);
+              ptx::tmem_st32(tO + cc * 32, o);
+            }
+            ptx::tmem_st_wait();
+            l *= alpha;
           }
-          ptx::tmem_st_wait();
-          l *= alpha;
+          if (need) m = m_new;
+          // rows of no query hold anything: they do not count
+          steep = __any_sync(0xffffffffu, m != -INFINITY && !(fabsf(m * c) < kSteepLog2) && row < tpt * p.G);
         }
-        if (need) m = m_new;
-        const float mc = (m == -INFINITY ? 0.f : m) * c;
-        // P = 2^(s c - m c) as packed 16-bit pairs over the first 32 columns of
-        // this half of S (already read): keys h0 + 2i, h0 + 2i + 1 -> column i.
+        // P = 2^(s c - R), R = c m rounded, as packed 16-bit pairs over the first 32 columns of
+        // this half of S (already read): keys h0 + 2i, h0 + 2i + 1 -> column i. One
+        // rounding, relative to the exponent; what R is off by is the same for the row's sums, and
+        // put right where they meet others (with (s - m) c for all, video chunk 912 -> 930 us).
         // P is rounded to the values' type, the product's operand: off by at most
         // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it.
         // Every exponential is the SFU's: with one pair in eight or two on the FMA pipe the
         // video chunk takes 834 and 835 us instead of 819
+        const float ref = m == -INFINITY ? 0.f : m;
+        float ce = c, re = ref * c;
+        if (steep) {
+          steep_scores(tS, ref, c);
+          ce = 1.f;
+          re = 0.f;
+        }
         float sum = 0.f;
         auto emit = [&](const uint32_t (&r)[32], int k0) {
           uint32_t pk[16];
-          const float2 c2 = make_float2(c, c), nmc2 = make_float2(-mc, -mc);
+          const float2 c2 = make_float2(ce, ce), nr2 = make_float2(-re, -re);
           float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float2 x =
-                ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nmc2);
+                ptx::ffma2(make_float2(__uint_as_float(r[2 * k]), __uint_as_float(r[2 * k + 1])), c2, nr2);
             const float2 e = make_float2(ptx::ex2(x.x), ptx::ex2(x.y));
             s2 = ptx::fadd2(s2, e);
             pk[k] = ptx::pack16x2<BF16>(e.x, e.y);
@@ -864,7 +906,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         ++gs;
         ++gt;
       }
-      // epilogue: O / l to the output (or, fp32 with its log2-sum-exp, to the prefix
+      // epilogue: O / l to the output (or, fp32 with its RowSum, to the prefix
       // pass's result or to this CTA's partial slot); each warp writes its D/2 columns
       float l_other = 0.f;
       if (!alive || !swap(l, l_other)) break;
@@ -876,30 +918,32 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
       // a row that saw nothing has l = 0: zeros and -inf; a NaN sum stays NaN
       const bool none = lt == 0.f;
       const float inv_l = none ? 0.f : 1.f / lt;
-      const float lse2 = none ? -INFINITY : m * c + log2f(lt);
       const int qi = grp * tpt + row / p.G, tok = jb.q0 + qi, head = jb.head0 + row % p.G;
       const bool live = row < tpt * p.G && qi < jb.tokens;
       const float a = have_o ? inv_l : 0.f;
       uint8_t* dst;  // this warp's half of the row
-      float* dst_lse;
+      RowSum* dst_sum = nullptr;
       const bool f32 = jb.slot >= 0 || p.pre_o;
       if (jb.slot >= 0) {
         const size_t at = (size_t)jb.slot * kPrefillRows + grp * kTileRows + row;
         dst = reinterpret_cast<uint8_t*>(p.part_o + at * D) + ch * (D * 2);
-        dst_lse = p.part_lse + at;
+        dst_sum = p.part_sum + at;
       } else if (p.pre_o) {
         dst = reinterpret_cast<uint8_t*>(p.pre_o + ((size_t)tok * p.Hk * p.G + head) * D) + ch * (D * 2);
-        dst_lse = p.pre_lse + (size_t)head * p.n_tok + tok;
+        dst_sum = p.pre_sum + (size_t)head * p.n_tok + tok;
       } else {
         dst = p.out.data + tok * p.out.tok_stride + head * p.out.head_stride + ch * D;
-        dst_lse = p.lse ? p.lse + (size_t)head * p.n_tok + tok : nullptr;
       }
       const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31) == 0;  // fp32 rows always are
       // the job's words are read: its slot is free (before the stores, which an
       // arrive behind them would wait for)
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive(&bar_je[slot]);
-      if (live && ch == 0 && dst_lse) *dst_lse = f32 ? lse2 : lse2 * 0.69314718055994531f;
+      if (live && ch == 0) {
+        const RowSum sum = make_float2(m, lt * ptx::ex2(-reference_gap(m, c)));
+        if (f32) *dst_sum = sum;
+        else if (p.lse) p.lse[(size_t)head * p.n_tok + tok] = row_lse2(sum, c) * 0.69314718055994531f;
+      }
 #pragma unroll 4
       for (int cc = 0; cc < D / 2; cc += 16) {
         uint32_t o[16];

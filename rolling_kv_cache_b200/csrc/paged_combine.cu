@@ -1,5 +1,5 @@
 // Merges the parts of the units that the paged attention kernels cut between
-// CTAs: O = sum_i 2^(lse_i - lse) O_i, lse = log2 sum_i 2^(lse_i), in fp32 and
+// CTAs: O = sum_i w_i O_i, w_i = l_i 2^(c m_i) / sum_k l_k 2^(c m_k) with each part's sum l_i 2^(c m_i) (RowSum), in fp32 and
 // in a fixed order. Block (c, y) takes rows of the unit that begins in CTA
 // c's range and goes on in the next; the unit's parts are slot 2c + 1 and
 // slots 2(c + 1), 2(c + 2), ... up to the CTA whose record says that the unit
@@ -9,7 +9,7 @@
 //
 // Launched as a programmatic dependent of the attention kernel: its blocks are
 // resident when that grid ends. Bound by that start-up and two dependent reads
-// (records and log-sum-exps, then the parts), from L2: 4.3 us behind the attention
+// (records and sums, then the parts), from L2: 4.3 us behind the attention
 // kernel for 12 units of one row, 16 us for 148 units of 256 rows (39 MB of parts;
 // blocks of 64 threads that ask for the first parts along with the records: the same).
 #include "paged_common.cuh"
@@ -20,12 +20,12 @@ namespace {
 
 constexpr int kCombThreads = 256;
 
-// weight[i][r] from log2-sum-exps to the shares of the sum, for sources i < n
-// and rows r < rows, a warp a row; lse[r]: the log2 of the sum. A source with
-// -inf gets the weight 0 whatever the others hold (a NaN among them included): it
-// may not exist, and is not read.
+// weight[i][r], l[i][r] from the two halves of RowSums to the shares of their sum, in weight, for sources i < n
+// and rows r < rows, a warp a row; sum[r]: the sum. A source whose l is 0 gets the
+// weight 0 whatever the others hold (a NaN among them included): it may not exist, and is not read.
 template <int ROWS>
-__device__ __forceinline__ void normalise(float (*weight)[ROWS], int n, int rows, float* lse) {
+__device__ __forceinline__ void normalise(float (*weight)[ROWS], const float (*ls)[ROWS], int n, int rows, float c,
+                                          RowSum* sum) {
   const int lane = threadIdx.x & 31;
   for (int r = threadIdx.x >> 5; r < rows; r += kCombThreads / 32) {
     float m = -INFINITY, l = 0.f;
@@ -33,15 +33,19 @@ __device__ __forceinline__ void normalise(float (*weight)[ROWS], int n, int rows
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const float ref = m == -INFINITY ? 0.f : m;
-    for (int i = lane; i < n; i += 32) l += exp2f(weight[i][r] - ref);
+    for (int i = lane; i < n; i += 32) {
+      const float x = ls[i][r] == 0.f ? 0.f : ls[i][r] * ptx::ex2((weight[i][r] - ref) * c);
+      weight[i][r] = x;
+      l += x;
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
     const float inv = l == 0.f ? 0.f : 1.f / l;
     for (int i = lane; i < n; i += 32) {
       const float x = weight[i][r];
-      weight[i][r] = x == -INFINITY ? 0.f : exp2f(x - ref) * inv;
+      weight[i][r] = x == 0.f ? 0.f : x * inv;
     }
-    if (lane == 0) lse[r] = l == 0.f ? -INFINITY : ref + log2f(l);
+    if (lane == 0) sum[r] = make_float2(m, l);
   }
 }
 
@@ -56,19 +60,25 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
   __shared__ int last_sh, flags_sh[kCombThreads];
   __shared__ float weight[kMaxPersistentCtas][kRows];
   static_assert(kMaxPersistentCtas <= kCombThreads, "a thread a CTA");
-  __shared__ float lse_sh[kRows];
-  __shared__ float so[kCombThreads][9];
+  __shared__ RowSum sum_sh[kRows];
+  // the parts' second halves, and behind the weights the threads' sums: small enough that the block
+  // is resident beside the attention kernel's
+  constexpr int kScratch = kMaxPersistentCtas * kRows > kCombThreads * 9 ? kMaxPersistentCtas * kRows : kCombThreads * 9;
+  __shared__ float scratch[kScratch];
+  float(*ls)[kRows] = reinterpret_cast<float(*)[kRows]>(scratch);
+  float(*so)[9] = reinterpret_cast<float(*)[9]>(scratch);
   const int tid = threadIdx.x, c = blockIdx.x, row_lo = blockIdx.y * kRows;
   if (tid == 0) last_sh = p.n_ctas - 1;
   auto part_row = [&](int i) { return (size_t)(2 * (c + i) + (i == 0)) * kUnitRows + row_lo; };
   ptx::grid_wait();
   // records and parts come from L2 (ld.cg): this block's SM may have cached
   // their addresses before the attention kernel wrote them. The first parts'
-  // log-sum-exps are asked for along with the records, before it is known which of them exist
+  // sums are asked for along with the records, before it is known which of them exist
   const PartRecord rec = __ldcg(p.rec + c);
   const int ahead = c + 1 + tid < p.n_ctas ? __ldcg(&p.rec[c + 1 + tid].x) : 0;
-  float early = 0.f;
-  if (tid < kEarly * kRows && c + tid / kRows < p.n_ctas) early = __ldcg(p.part_lse + part_row(tid / kRows) + tid % kRows);
+  const RowSum none = make_float2(-INFINITY, 0.f);
+  RowSum early = none;
+  if (tid < kEarly * kRows && c + tid / kRows < p.n_ctas) early = __ldcg(p.part_sum + part_row(tid / kRows) + tid % kRows);
   if (rec.z <= 0) return;
   flags_sh[tid] = ahead;
   __syncthreads();
@@ -82,10 +92,12 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
     const int i = x / kRows, r = x % kRows;
     // a CTA whose range is empty left no part
     const bool there = r < rows && (i == 0 || (flags_sh[i - 1] & kHasHead));
-    weight[i][r] = !there ? -INFINITY : (x < kEarly * kRows ? early : __ldcg(p.part_lse + part_row(i) + r));
+    const RowSum s = !there ? none : (x < kEarly * kRows ? early : __ldcg(p.part_sum + part_row(i) + r));
+    weight[i][r] = s.x;
+    ls[i][r] = s.y;
   }
   __syncthreads();
-  normalise(weight, parts, rows, lse_sh);
+  normalise(weight, ls, parts, rows, p.scale_log2, sum_sh);
   __syncthreads();
   const RowOutput to = row_output(p);
   const int items = rows * kChunks, groups = max(1, kCombThreads / items);
@@ -129,16 +141,16 @@ __global__ void __launch_bounds__(kCombThreads) paged_combine_kernel(const __gri
       h = rr % p.G;
       if (rr >= tpt * p.G || i >= rec.z) continue;
     }
-    store_row<D, BF16>(to, rec.y + i, head0 + h, col, acc, lse_sh[r]);
+    store_row<D, BF16>(to, rec.y + i, head0 + h, col, acc, sum_sh[r]);
   }
 }
 
 // One result over some of the keys of a unit: where it lies whole, and where in parts.
 struct JoinSide {
   const float* o;
-  const float* lse;  // whole rows: [n_tok][q_heads][d] and [q_heads][n_tok]
+  const RowSum* sum;  // whole rows: [n_tok][q_heads][d] and [q_heads][n_tok]
   const float* part_o;
-  const float* part_lse;
+  const RowSum* part_sum;
   const int4* rec;
   int n_ctas;
 };
@@ -160,8 +172,9 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_constant__ JoinParams p) {
   constexpr int kChunks = D / 8;
   __shared__ int first_sh[3], last_sh[3];  // the decode unit's, and the first and last token's pair's
-  __shared__ float scratch[kJoinSources * kDecodeRows];  // small enough to be resident beside the attention kernels
-  __shared__ float lse_sh[kDecodeRows];
+  // small enough that two blocks are resident beside the decode kernel's (with the sums here too, twice as much, one: 0.7 us)
+  __shared__ float scratch[kJoinSources * kDecodeRows];
+  __shared__ float most_sh[kCombThreads / 32][kDecodeRows], l_sh[kCombThreads / 32][kDecodeRows];  // each warp's, of the rows
   __shared__ uint8_t there[2][kMaxPersistentCtas];  // the CTAs' records' flags
   float(*weight)[kDecodeRows] = reinterpret_cast<float(*)[kDecodeRows]>(scratch);
   float(*so)[9] = reinterpret_cast<float(*)[9]>(scratch);  // after the weights
@@ -198,11 +211,11 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
   const int n_pre0 = first_sh[1] < 0 ? 1 : last_sh[1] - first_sh[1] + 1;
   const int n_pre1 = first_sh[2] < 0 ? 1 : last_sh[2] - first_sh[2] + 1;
   const int n = n_own + max(n_pre0, n_pre1);
-  // Row r's values and log-sum-exp on one side: whole (c < 0), or in the parts
+  // Row r's values and sum on one side: whole (c < 0), or in the parts
   // from CTA c on, whose slots lie `unit` rows apart.
   struct Rows {
     const float* o;
-    const float* l;
+    const RowSum* l;
     int c, last, unit;
   };
   auto rows_of = [&](int r, bool own) {
@@ -218,24 +231,42 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
     const size_t at = x.c < 0 ? (size_t)tok * heads + head
                               : (size_t)(own ? r : tile * 128 + (in_pair - tile * tpt) * p.G + g);
     x.o = (x.c < 0 ? side.o : side.part_o) + at * D;
-    x.l = x.c < 0 ? side.lse + (size_t)head * p.n_tok + tok : side.part_lse + at;
+    x.l = x.c < 0 ? side.sum + (size_t)head * p.n_tok + tok : side.part_sum + at;
     return x;
   };
   auto slot = [](const Rows& x, int e) { return x.c < 0 ? (size_t)0 : (size_t)(2 * (x.c + e) + (e == 0)) * x.unit; };
+  // a row's largest m, then its sources' l 2^(c (m - that)) and their sum; a source that does not exist has the
+  // weight 0, whatever the others hold, and is not read
   {
-    const int r = tid % kDecodeRows;  // the same for all of a thread's sources
+    const int r = tid % kDecodeRows, warp = tid >> 5;  // the row of all of a thread's sources
+    const int e0 = tid / kDecodeRows, step = kCombThreads / kDecodeRows;
     const Rows own = rows_of(min(r, R - 1), true), pre = rows_of(min(r, R - 1), false);
-    for (int e = tid / kDecodeRows; e < n; e += kCombThreads / kDecodeRows) {
+    auto source = [&](int e) {
       const bool mine = e < n_own;
       const Rows& x = mine ? own : pre;
       const int i = mine ? e : e - n_own;
       // a CTA whose range is empty left no part
-      const bool is = r < R && (i == 0 || (x.c >= 0 && x.c + i <= x.last && (there[!mine][x.c + i] & kHasHead)));
-      weight[e][r] = is ? __ldcg(x.l + slot(x, i)) : -INFINITY;
+      const bool is = e < n && r < R && (i == 0 || (x.c >= 0 && x.c + i <= x.last && (there[!mine][x.c + i] & kHasHead)));
+      return is ? __ldcg(x.l + slot(x, i)) : make_float2(-INFINITY, 0.f);
+    };
+    const RowSum first = source(e0), second = source(e0 + step);  // kept; the rest is loaded twice
+    float m = fmaxf(first.x, second.x), l = 0.f;
+    for (int e = e0 + 2 * step; e < n; e += step) m = fmaxf(m, source(e).x);
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, kDecodeRows));
+    most_sh[warp][r] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kCombThreads / 32; ++w) m = fmaxf(m, most_sh[w][r]);
+    const float ref = m == -INFINITY ? 0.f : m;
+    for (int e = e0; e < n; e += step) {
+      const RowSum x = e == e0 ? first : (e == e0 + step ? second : source(e));
+      const float w = x.y == 0.f ? 0.f : x.y * ptx::ex2((x.x - ref) * p.to.c);
+      weight[e][r] = w;
+      l += w;
     }
+    l += __shfl_xor_sync(0xffffffffu, l, kDecodeRows);
+    l_sh[warp][r] = l;
   }
-  __syncthreads();
-  normalise(weight, n, R, lse_sh);
   __syncthreads();
   const int items = R * kChunks, groups = kCombThreads / items;
   const int item = tid % items, grp = tid / items;
@@ -258,6 +289,10 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
       for (int k = 0; k < 8; ++k) acc[k] = fmaf(x[k], w, acc[k]);
     }
   }
+  RowSum sum = make_float2(-INFINITY, 0.f);
+#pragma unroll
+  for (int w = 0; w < kCombThreads / 32; ++w) sum = make_float2(fmaxf(sum.x, most_sh[w][r]), sum.y + l_sh[w][r]);
+  const float inv = sum.y == 0.f ? 0.f : 1.f / sum.y;
   if (groups > 1) {
     __syncthreads();
 #pragma unroll
@@ -269,8 +304,10 @@ __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_c
         for (int k = 0; k < 8; ++k) acc[k] += so[g * items + item][k];
   }
   if (grp != 0) return;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) acc[k] *= inv;
   const int i = r / p.G;
-  store_row<D, BF16>(p.to, s.q0 + i, h * p.G + r - i * p.G, col, acc, lse_sh[r]);
+  store_row<D, BF16>(p.to, s.q0 + i, h * p.G + r - i * p.G, col, acc, sum);
 }
 
 template <int D, bool BF16>
@@ -278,7 +315,7 @@ cudaError_t join_d(const JoinParams& p, cudaStream_t s) {
   return launch_chained(paged_join_kernel<D, BF16>, p, dim3(p.b.n_seqs * p.Hk), kCombThreads, 0, true, s);
 }
 
-// out = the merge of the results in (pre_o, pre_lse) and (prev_o, prev_lse), 8
+// out = the merge of the results in (pre_o, pre_sum) and (prev_o, prev_sum), 8
 // columns of a row a thread, rows of no sequence left alone. Bound by HBM and L2: 768
 // rows of 32 heads of 128, 31 MB, 6.2 us.
 template <int D, bool BF16>
@@ -292,11 +329,11 @@ __global__ void __launch_bounds__(256) paged_merge_kernel(const __grid_constant_
   const float4* src = reinterpret_cast<const float4*>(p.pre_o + (size_t)row * D + col);
   const float4 a = src[0], b = src[1];
   float acc[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-  float lse2 = p.pre_lse[(size_t)head * p.n_tok + tok];
+  RowSum sum = p.pre_sum[(size_t)head * p.n_tok + tok];
   RowOutput to = row_output(p);
   to.pre_o = nullptr;
-  merge_prev<D>(to, tok, head, col, acc, lse2);
-  store_row<D, BF16>(to, tok, head, col, acc, lse2);
+  merge_prev<D>(to, tok, head, col, acc, sum);
+  store_row<D, BF16>(to, tok, head, col, acc, sum);
 }
 
 template <int D, bool BF16>
@@ -324,10 +361,10 @@ cudaError_t launch_paged_join(const PagedAttnParams& own, const PagedAttnParams&
                               cudaStream_t s) {
   JoinParams p{};
   p.b = own.b;
-  p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse,   nullptr,
-                   nullptr,      nullptr,            nullptr,             own.n_tok, own.Hk * own.G};
-  p.own = JoinSide{own.pre_o, own.pre_lse, own.part_o, own.part_lse, own.rec, own.n_ctas};
-  p.pre = JoinSide{pre.pre_o, pre.pre_lse, pre.part_o, pre.part_lse, pre.rec, pre.n_ctas};
+  p.to = RowOutput{own.out.data, own.out.tok_stride, own.out.head_stride, own.lse,        nullptr,       nullptr,
+                   nullptr,      nullptr,            own.n_tok,           own.Hk * own.G, own.scale_log2};
+  p.own = JoinSide{own.pre_o, own.pre_sum, own.part_o, own.part_sum, own.rec, own.n_ctas};
+  p.pre = JoinSide{pre.pre_o, pre.pre_sum, pre.part_o, pre.part_sum, pre.rec, pre.n_ctas};
   p.n_tok = own.n_tok;
   p.Hk = own.Hk;
   p.G = own.G;

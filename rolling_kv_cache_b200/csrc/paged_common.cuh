@@ -128,49 +128,57 @@ inline cudaError_t launch_chained(void (*kernel)(const Params), const Params& p,
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+// A row's sum of exponentials over some keys, sum_j 2^(c x_j) = y 2^(c x) with the raw score x of its running maximum
+// (-inf: it has none; y is then 0, or NaN of NaN scores) and c = scale_log2. Apart, because their one
+// logarithm c x + log2 y, in fp32, loses y and even the differences of scores where c x is large: two parts are
+// weighed by 2^(c (x1 - x2)), whose difference is taken between the scores themselves.
+using RowSum = float2;
+
+__device__ __forceinline__ float row_lse2(RowSum s, float c) { return s.y == 0.f ? -INFINITY : s.x * c + log2f(s.y); }
+
 // Where a row's result goes, and what it is merged with (PagedAttnParams' fields).
 struct RowOutput {
   uint8_t* out;
   long long tok_stride, head_stride;  // bytes
   float* lse;
   const float* prev_o;
-  const float* prev_lse;
+  const RowSum* prev_sum;
   float* pre_o;
-  float* pre_lse;
+  RowSum* pre_sum;
   int n_tok, heads;
+  float c;
 };
 
 __device__ __forceinline__ RowOutput row_output(const PagedAttnParams& p) {
-  return RowOutput{p.out.data, p.out.tok_stride, p.out.head_stride, p.lse,  p.prev_o,
-                   p.prev_lse, p.pre_o,          p.pre_lse,         p.n_tok, p.Hk * p.G};
+  return RowOutput{p.out.data, p.out.tok_stride, p.out.head_stride, p.lse,   p.prev_o,   p.prev_sum,
+                   p.pre_o,    p.pre_sum,        p.n_tok,           p.Hk * p.G, p.scale_log2};
 }
 
-// Merges 8 columns of a row (divided by its sum; lse2 its log2-sum-exp) with
-// the same row's result over the shared prefix.
+// Merges 8 columns of a row (divided by its sum) with the same row's result over the shared prefix.
 template <int D>
 __device__ __forceinline__ void merge_prev(const RowOutput& p, int tok, int head, int col, float (&acc)[8],
-                                           float& lse2) {
-  const float pl = __ldcg(p.prev_lse + (size_t)head * p.n_tok + tok);
-  const float m = fmaxf(lse2, pl);
-  if (m == -INFINITY && pl == m) return;  // the prefix's side saw no key (fmaxf passes over a NaN)
+                                           RowSum& sum) {
+  const RowSum ps = __ldcg(p.prev_sum + (size_t)head * p.n_tok + tok);
+  const float m = fmaxf(sum.x, ps.x), ref = m == -INFINITY ? 0.f : m;
   const float4* src = reinterpret_cast<const float4*>(p.prev_o + ((size_t)tok * p.heads + head) * D + col);
   const float4 a = __ldcg(src), b = __ldcg(src + 1);
-  const float w = exp2f(lse2 - m), wp = exp2f(pl - m), inv = 1.f / (w + wp);
+  const float w = sum.y * ptx::ex2((sum.x - ref) * p.c), wp = ps.y * ptx::ex2((ps.x - ref) * p.c), l = w + wp;
+  const float inv = l == 0.f ? 0.f : 1.f / l;  // neither side saw a key: both are zeros
   const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
   for (int k = 0; k < 8; ++k) acc[k] = (acc[k] * w + x[k] * wp) * inv;
-  lse2 = m + log2f(w + wp);
+  sum = make_float2(m, l);
 }
 
 // The last write of 8 columns of a row: the output, or the prefix pass's fp32 result.
 template <int D, bool BF16>
 __device__ __forceinline__ void store_row(const RowOutput& p, int tok, int head, int col, const float (&acc)[8],
-                                          float lse2) {
+                                          RowSum sum) {
   if (p.pre_o) {
     float4* dst = reinterpret_cast<float4*>(p.pre_o + ((size_t)tok * p.heads + head) * D + col);
     dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
     dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-    if (col == 0) p.pre_lse[(size_t)head * p.n_tok + tok] = lse2;
+    if (col == 0) p.pre_sum[(size_t)head * p.n_tok + tok] = sum;
     return;
   }
   uint4 u;
@@ -179,7 +187,7 @@ __device__ __forceinline__ void store_row(const RowOutput& p, int tok, int head,
   u.z = ptx::pack16x2<BF16>(acc[4], acc[5]);
   u.w = ptx::pack16x2<BF16>(acc[6], acc[7]);
   *reinterpret_cast<uint4*>(p.out + tok * p.tok_stride + head * p.head_stride + col * 2) = u;
-  if (p.lse && col == 0) p.lse[(size_t)head * p.n_tok + tok] = lse2 * 0.69314718055994531f;
+  if (p.lse && col == 0) p.lse[(size_t)head * p.n_tok + tok] = row_lse2(sum, p.c) * 0.69314718055994531f;
 }
 
 }  // namespace rc

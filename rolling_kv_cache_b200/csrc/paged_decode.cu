@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
   __shared__ float wm[2][kConsumers][16], wl[2][kConsumers][16];
   __shared__ int warp_sums[kConsumers + 2];
   __shared__ int abort_sh, falls_sh;
-  __shared__ float own_lse[16];  // CLUSTER: of this CTA's tiles
+  __shared__ RowSum own_sum[16];  // CLUSTER: of this CTA's tiles
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* base = smem_raw + (((ptx::smem_u32(smem_raw) + 1023u) & ~1023u) - ptx::smem_u32(smem_raw));
   const uint32_t base_u32 = ptx::smem_u32(base);
@@ -391,13 +391,14 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
           o[i][3] *= a1;
         }
       }
-      const float b0 = mx0 == -INFINITY ? 0.f : mx0 * c, b1 = mx1 == -INFINITY ? 0.f : mx1 * c;
+      // the difference first: the product's rounding is then relative to the exponent, whatever c is
+      const float b0 = mx0 == -INFINITY ? 0.f : mx0, b1 = mx1 == -INFINITY ? 0.f : mx1;
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        x[i][0] = ptx::ex2(fmaf(x[i][0], c, -b0));
-        x[i][1] = ptx::ex2(fmaf(x[i][1], c, -b0));
-        x[i][2] = ptx::ex2(fmaf(x[i][2], c, -b1));
-        x[i][3] = ptx::ex2(fmaf(x[i][3], c, -b1));
+        x[i][0] = ptx::ex2((x[i][0] - b0) * c);
+        x[i][1] = ptx::ex2((x[i][1] - b0) * c);
+        x[i][2] = ptx::ex2((x[i][2] - b1) * c);
+        x[i][3] = ptx::ex2((x[i][3] - b1) * c);
       }
       l0 += (x[0][0] + x[0][1]) + (x[1][0] + x[1][1]);
       l1 += (x[0][2] + x[0][3]) + (x[1][2] + x[1][3]);
@@ -486,7 +487,7 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         l += um[w][row] == -INFINITY ? ul[w][row] : ul[w][row] * ptx::ex2((um[w][row] - gm) * c);
       // a row that sees nothing has l = 0: zeros and -inf; a NaN sum stays NaN
       const float inv = l == 0.f ? 0.f : 1.f / l;
-      float lse2 = l == 0.f ? -INFINITY : gm * c + log2f(l);
+      const RowSum sum = make_float2(gm, l);
 #pragma unroll
       for (int k = 0; k < 8; ++k) acc[k] *= inv;
       if constexpr (CLUSTER) {
@@ -494,49 +495,53 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         float4* dst = reinterpret_cast<float4*>(base + L::kMerge + (row * L::kOPad + col) * 4);
         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (col == 0) own_lse[row] = lse2;
+        if (col == 0) own_sum[row] = sum;
       } else if (done.lo > 0 || done.hi < done.total) {
         const size_t at = (size_t)(2 * blockIdx.x + (done.lo > 0 ? 0 : 1)) * kDecodeRows + row;
         float4* dst = reinterpret_cast<float4*>(p.part_o + at * D + col);
         dst[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
         dst[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-        if (col == 0) p.part_lse[at] = lse2;
+        if (col == 0) p.part_sum[at] = sum;
       } else {
         const int i = row / p.G, head = done.h * p.G + row - i * p.G, tok = ds.q0 + i;
-        store_row<D, BF16>(row_output(p), tok, head, col, acc, lse2);
+        store_row<D, BF16>(row_output(p), tok, head, col, acc, sum);
       }
     }
     if constexpr (CLUSTER) {
-      // O = sum_i 2^(lse_i - lse) O_i over the cluster's CTAs, by the first of them
+      // O = sum_i w_i O_i over the cluster's CTAs, w_i each one's share of the sums, by the first of them
       ptx::cluster_sync();
       if (row < R && (int)blockIdx.x % p.cluster == 0) {
-        const uint32_t at_lse = ptx::smem_u32(&own_lse[row]), at = base_u32 + L::kMerge + (row * L::kOPad + col) * 4;
-        float ls[kMaxCluster], m = -INFINITY, sum = 0.f, acc[8];
+        const uint32_t at_sum = ptx::smem_u32(&own_sum[row]), at = base_u32 + L::kMerge + (row * L::kOPad + col) * 4;
+        float w[kMaxCluster], ls[kMaxCluster], m = -INFINITY, sum = 0.f, acc[8];
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
-          ls[r] = r < p.cluster ? ptx::cluster_ld(ptx::cluster_addr(at_lse, r)) : -INFINITY;
-          m = fmaxf(m, ls[r]);
+          const RowSum s = r < p.cluster ? ptx::cluster_ld2(ptx::cluster_addr(at_sum, r)) : make_float2(-INFINITY, 0.f);
+          w[r] = s.x;
+          ls[r] = s.y;
+          m = fmaxf(m, s.x);
         }
-        if (m == -INFINITY) m = 0.f;
+        const float ref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+        for (int r = 0; r < kMaxCluster; ++r) {
+          w[r] = ls[r] * ptx::ex2((w[r] - ref) * c);
+          sum += w[r];
+        }
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] = 0.f;
 #pragma unroll
         for (int r = 0; r < kMaxCluster; ++r) {
           if (r >= p.cluster) continue;
-          const float w = exp2f(ls[r] - m);
           const uint32_t src = ptx::cluster_addr(at, r);
           const float4 x = ptx::cluster_ld4(src), y = ptx::cluster_ld4(src + 16);
           const float v[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-          sum += w;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], w, acc[k]);
+          for (int k = 0; k < 8; ++k) acc[k] = fmaf(v[k], w[r], acc[k]);
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
         for (int k = 0; k < 8; ++k) acc[k] *= inv;
         const int i = row / p.G;
-        store_row<D, BF16>(row_output(p), ds.q0 + i, done.h * p.G + row - i * p.G, col, acc,
-                           sum == 0.f ? -INFINITY : m + log2f(sum));
+        store_row<D, BF16>(row_output(p), ds.q0 + i, done.h * p.G + row - i * p.G, col, acc, make_float2(m, sum));
       }
       ptx::cluster_sync();  // no CTA's memory goes before it has been read
     }

@@ -305,9 +305,9 @@ __device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, int rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ float cluster_ld(uint32_t addr) {
-  float r;
-  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+__device__ __forceinline__ float2 cluster_ld2(uint32_t addr) {
+  float2 r;
+  asm volatile("ld.shared::cluster.v2.f32 {%0,%1}, [%2];" : "=f"(r.x), "=f"(r.y) : "r"(addr) : "memory");
   return r;
 }
 __device__ __forceinline__ float4 cluster_ld4(uint32_t addr) {

@@ -1,14 +1,16 @@
 """Paged-cache operators at the ends of what their arguments allow: values that are no numbers, scales, rows
 and lengths out of range, modes of torch that a call has to notice."""
+import math
 
 import pytest
 import torch
 
 from rolling_kv_cache_b200 import paged
 
-from paged_util import Batch, randn
+from paged_util import F64, UNIT, Batch, generator, randn, visible
 
 pytestmark = pytest.mark.gpu
+BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
 NAN = float("nan")
 
 
@@ -98,3 +100,91 @@ def test_a_nan_key_of_the_prefix_reaches_sequences_without_tokens(case):
     o, lse = _attend(bt, max_q, prefix)
     assert bool(o[hit].isnan().all()) and bool(lse.T[hit].isnan().all())
     assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse.T[~hit], wl.T[~hit])
+
+
+def _one_axis(bt):
+    """Queries along the first axis, keys whose first element is a multiple of 1/16 below 8: every score is exact in
+    fp32, and the largest comes up several times."""
+    bt.q.zero_()
+    bt.q[..., 0] = torch.randint(1, 3, bt.q.shape[:2], generator=bt.gen, device="cuda").to(bt.dtype)
+    bt.q[..., 0] *= torch.randint(0, 2, bt.q.shape[:2], generator=bt.gen, device="cuda").to(bt.dtype) * 2 - 1
+    first = torch.randint(-127, 128, bt.k_pages.shape[:3], generator=bt.gen, device="cuda") / 16
+    bt.k_pages[..., 0] = torch.where(bt.k_pages[..., 0].isnan(), NAN, first.float()).to(bt.dtype)
+
+
+def _assert_exact_scores(got, bt, scale, prefix=None):
+    """Against the softmax in 64 bits. Scores and their differences are exact, so a weight's exponent, t nats below
+    the row's largest, is off by at most t 2^-22 (its factor and its product are rounded, once more where the stale maximum moved; the
+    sum of all the distances is at most t and 8 / log2(e) behind and before it). The exponential is allowed 2^-13, the weight's
+    rounding to the type UNIT (fp16: 2^-25 at least), sums of m terms in fp32 m 2^-23, the output's rounding UNIT."""
+    out, lse = got
+    u, dt = UNIT[bt.dtype], bt.dtype
+    sc = float(torch.tensor(scale, dtype=F32))
+    for b, (a, n) in enumerate(bt.lens):
+        if not a:
+            continue
+        seen = visible(n - a, a, n, 1, 0, 0)
+        j = torch.arange(n, device="cuda")
+        k, v = (bt.rows(x, bt.page_table[b], j) for x in (bt.k_pages, bt.v_pages))
+        if prefix is not None:
+            i = torch.arange(prefix[1], device="cuda")
+            k, v = (torch.cat((bt.rows(p, prefix[0], i), x)) for p, x in ((bt.k_pages, k), (bt.v_pages, v)))
+            seen = torch.cat((seen.new_ones(a, prefix[1]), seen), 1)
+        r = slice(bt.cu[b], bt.cu[b + 1])
+        for h in range(bt.hq):
+            kh, vh = k[:, h // (bt.hq // bt.hk)], v[:, h // (bt.hq // bt.hk)]
+            x = (bt.q[r, h].to(F64) @ kh.T * sc).masked_fill(~seen, -math.inf)
+            t = (x.amax(1, keepdim=True) - x).masked_fill(~seen, 0)
+            w = torch.softmax(x, -1)
+            m = seen.sum(1, keepdim=True)
+            rel = w * (u + 2.0 ** -13 + (m + 16) * 2.0 ** -23 + t * 2.0 ** -22)
+            rel = rel + (seen * 2.0 ** -25 if dt == F16 else 0)
+            o = w @ vh
+            tol = rel @ vh.abs() + rel.sum(1, keepdim=True) * o.abs()
+            tol = tol + u * (o.abs() + tol) + (2.0 ** -25 if dt == F16 else 0)
+            err = (out[r, h].to(F64) - o).abs()
+            assert bool((err <= tol).all()), (b, h, float(err.max()))
+            ls = torch.logsumexp(x, -1)
+            ltol = 2.0 ** -21 * (ls.abs() + 1) + rel.sum(1)
+            assert bool(((lse[h, r].to(F64) - ls).abs() <= ltol).all()), (b, h)
+
+
+@pytest.mark.parametrize("scale", [1e2, 1e4, 1e6, 1e7, 1e9, 1e30])
+@pytest.mark.parametrize("path", ["clusters", "cut", "many"])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_large_scales_leave_the_largest_scores_their_weight(scale, path, dtype, d):
+    a = 30 if path == "many" else 2
+    bt = Batch(104, [(a, 1000), (a, 300), (1, 5), (a, 2500)], 4, 2, d, 16, dtype)
+    if path == "cut":
+        bt.page_table = _wide(bt)
+    _one_axis(bt)
+    _assert_exact_scores(_attend(bt, a, scale=scale), bt, scale)
+
+
+@pytest.mark.parametrize("scale", [1e4, 1e9, 1e30])
+@pytest.mark.parametrize("case", PREFIXES, ids=["clusters", "join", "merge", "walked"])
+def test_large_scales_over_a_prefix(case, scale):
+    hq, hk, d, page, rest, n, max_q = case
+    bt = Batch(105, [(1, 9)] + rest, hq, hk, d, page, spare=(n + page - 1) // page + 1)
+    prefix = _prefix(bt, n)
+    _one_axis(bt)
+    _assert_exact_scores(_attend(bt, max_q, prefix, scale=scale), bt, scale, prefix)
+
+
+@pytest.mark.parametrize("path", ["clusters", "cut", "many"])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_maxima_that_grow_past_the_border_of_steep_rows(path, dtype, d):
+    """Scores of 90852 + i / 64, exact in fp32, i growing along the sequence: the largest passes 2^24 in units of the
+    exponential's base in steps of 2.9, so that sums from before and behind that border meet."""
+    a = 30 if path == "many" else 2
+    bt = Batch(116, [(a, 2500), (a, 700)], 4, 2, d, 16, dtype)
+    if path == "cut":
+        bt.page_table = _wide(bt)
+    bt.q.zero_()
+    bt.q[..., 0], bt.q[..., 1], bt.q[..., 2] = 256, 1, 1
+    for b, (_, n) in enumerate(bt.lens):
+        j = torch.arange(n, device="cuda")
+        page, row = bt.page_table[b][j // 16].long(), j % 16
+        for i, x in enumerate((354.0, 228.0, (j * 26 // n / 64)[:, None])):
+            bt.k_pages[page, :, row, i] = (torch.zeros(n, 2, device="cuda") + x).to(dtype)
+    _assert_exact_scores(_attend(bt, a, scale=128.0), bt, 128.0)
