@@ -92,7 +92,6 @@ struct Job {
   int tokens, at0;   // queries of the pair, position of the first
   int L, kv_lo, kv_hi, slot;
   bool has1, head, tail;  // head: begins inside the unit; tail: ends inside it
-  bool bad;               // of its sequence (Seq)
   int lead, total;        // tiles of the prefix that it walks first, and in all
   TileSpan<kTileRows> sp;
 };
@@ -107,8 +106,7 @@ __device__ __forceinline__ Seq pre_seq(const PagedAttnParams& p, int b) {
     s.q0 = 0;
     s.n = min(max(n, 0), p.n_tok);
     s.L = p.prefix_len;
-    s.falls = false;
-    s.bad = s.n != n;
+    s.falls = s.bad = false;  // the pass over the sequences' own tokens reports
     return s;
   }
   return load_seq(p.b, p.n_tok, b);
@@ -216,7 +214,6 @@ struct PairWalk {
     j.h = h;
     j.q0 = s.q0 + pair * 2 * tpt;
     j.L = s.L;
-    j.bad = s.bad;
     j.kv_lo = lo;
     j.kv_hi = min(lo + len, j.total);
     j.has1 = j.tokens > tpt;
@@ -296,6 +293,7 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
     if (lane == 0) {
       if (s.falls) sums[2] = 1;
+      if (s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);  // also where it is left without a unit
       before[b] = (unsigned long long)pairs << 32 | (uint32_t)sum;
       if (b < kPlanSeqs) seqs[b] = make_int4(s.q0, s.n, s.L, 0);
     }
@@ -303,7 +301,6 @@ __device__ __forceinline__ void make_plan(const PagedAttnParams& p, uint8_t* mem
   __syncthreads();
   block_prefix<kPreThreads>(before, n_seqs, warp_sums, [&](int b) { return before[b]; });
   const bool falls = sums[2];
-  if (falls && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
   const int W = falls ? 0 : p.Hk * tiles_of(before[n_seqs]), U = falls ? 0 : p.Hk * pairs_of(before[n_seqs]);
   const int r_max = min(U / G, kMaxRounds);
   int rounds = 0, own = 0;
@@ -560,7 +557,6 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
           publish(-1);
           return false;
         }
-        if (lane == 0 && jb.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
         if (jb.head) rec.x = kHasHead | (jb.tail ? 0 : kHeadEnds);
         else if (jb.tail) rec = make_int4(rec.x, jb.q0, jb.tokens, jb.h * p.G);
         j = jb.kv_lo;

@@ -148,10 +148,8 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     mine.b = unit / p.Hk;
     mine.h = unit - mine.b * p.Hk;
     const Seq s = load_seq(p.b, p.n_tok, mine.b);
-    if (s.n == 0) {  // the whole cluster returns
-      if (tid == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
-      return;
-    }
+    if (tid == 0 && s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
+    if (s.n == 0) return;  // the whole cluster
     TileSpan<kTK> sp;
     sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
     mine.total = lead + sp.n;
@@ -163,12 +161,12 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
     block_prefix<kDecThreads>(pre, p.b.n_seqs, warp_sums, [&](int b) {
       const Seq s = load_seq(p.b, p.n_tok, b);
       if (s.falls) falls_sh = 1;
+      if (s.bad && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);  // also where it is left without a unit
       if (s.n == 0) return 0;
       TileSpan<kTK> sp;
       sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
       return max(sp.n, 1) + kUnitCost;
     });
-    if (falls_sh && tid == 0 && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
     const int W = falls_sh ? 0 : p.Hk * pre[p.b.n_seqs];
     const int pos = (int)((long long)W * blockIdx.x / gridDim.x);
     const int end = (int)((long long)W * (blockIdx.x + 1) / gridDim.x);
@@ -213,7 +211,6 @@ __global__ void __launch_bounds__(kDecThreads, 1) paged_decode_kernel(const __gr
         if (!next_unit(u)) return t;
         const Seq s = load_seq(p.b, p.n_tok, u.b);
         sp.init(p.mask, s.L - s.n, s.L - 1, s.L);
-        if (lane == 0 && s.bad && !is_v && p.status) atomicCAS(p.status, 0, (int)RC_ERANGE);
         if (CLUSTER) {
         } else if (u.lo > 0) rec.x = kHasHead | (u.hi == u.total ? kHeadEnds : 0);
         else if (u.hi < u.total) rec = make_int4(rec.x, s.q0, min(s.n, 16 / p.G), u.h * p.G);

@@ -5,9 +5,10 @@ import math
 import pytest
 import torch
 
+from rolling_kv_cache_b200 import binding as B
 from rolling_kv_cache_b200 import paged
 
-from paged_util import F64, UNIT, Batch, generator, randn, visible
+from paged_util import F64, UNIT, Batch, assert_attend, generator, randn, visible
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -18,6 +19,12 @@ NAN = float("nan")
 def _status_stays_clear():
     yield
     paged.device_status()
+
+
+def _reported():
+    with pytest.raises(B.RcError) as e:
+        paged.device_status()
+    assert e.value.status == B.RC_ERANGE
 
 
 def _wide(bt):
@@ -188,3 +195,46 @@ def test_maxima_that_grow_past_the_border_of_steep_rows(path, dtype, d):
         for i, x in enumerate((354.0, 228.0, (j * 26 // n / 64)[:, None])):
             bt.k_pages[page, :, row, i] = (torch.zeros(n, 2, device="cuda") + x).to(dtype)
     _assert_exact_scores(_attend(bt, a, scale=128.0), bt, 128.0)
+
+
+PATHS = ["clusters", "cut", "many", "prefix clusters", "prefix join", "prefix walked", "prefix merge"]
+
+
+def _path(bt, path):
+    """(table, max_q, prefix) that take the path for a batch of two sequences of a few rows."""
+    prefix = None
+    if path.startswith("prefix"):
+        # a pass of its own from 2^18 tokens on, where few rows are many-row work: the same pages over and over
+        prefix = _prefix(bt, 2 ** 18 if path.endswith("merge") else 40, 3)
+    table = _wide(bt) if path in ("cut", "prefix join") else bt.page_table
+    return table, 3 if path in ("clusters", "cut", "prefix clusters", "prefix join") else 30, prefix
+
+
+@pytest.mark.parametrize("path", PATHS)
+@pytest.mark.parametrize("cu", [[0, 3, 7], [3, 3, 5], [0, 0, 5], [5, 5, 5]])
+def test_sequences_left_without_rows_by_what_is_out_of_range_are_reported(path, cu):
+    """Rows past the tokens, rows before the first sequence, a length past its table."""
+    n_tok = 3 if cu[-1] == 7 else 5
+    bt = Batch(106, [(max(0, e - s), 40) for s, e in zip(cu, cu[1:])], 4, 2, 64, 16, spare=8)
+    bt.page_table, max_q, prefix = _path(bt, path)
+    bt.q = randn(bt.gen, n_tok, 4, 64)
+    bt.cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    if cu[0] == 0 and cu[1] == 0:
+        bt.kv_len[0] = -1
+    out = torch.full_like(bt.q, 7.0)
+    got = _attend(bt, max_q, prefix, out=out)
+    _reported()
+    first, last = cu[0], min(cu[-1], n_tok)
+    assert bool((out[:first] == 7).all()) and bool((out[last:] == 7).all())
+    bt.cu, bt.lens, bt.n_tok = [min(c, n_tok) for c in cu], [(min(e, n_tok) - min(s, n_tok), n) for (s, e), (_, n) in
+                                                            zip(zip(cu, cu[1:]), bt.lens)], n_tok
+    if path == "prefix merge":
+        return  # 2^18 keys a row: the formula's bound says nothing
+    # rows of a sequence, in place
+    for b, (a, _) in enumerate(bt.lens):
+        if a:
+            one = Batch.__new__(Batch)
+            one.__dict__.update(bt.__dict__)
+            r = slice(bt.cu[b], bt.cu[b + 1])
+            one.lens, one.cu, one.n_tok, one.q, one.page_table = [bt.lens[b]], [0, a], a, bt.q[r], bt.page_table[b:b + 1]
+            assert_attend((got[0][r], got[1][:, r]), one, prefix=prefix)
