@@ -7,6 +7,7 @@
 #include <ATen/ATen.h>
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/CUDAGraphsUtils.cuh>
+#include <c10/core/InferenceMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/utils/pybind.h>
@@ -59,6 +60,8 @@ int32_t* status_word(int device) {
   if (!w.word[device].defined()) {
     if (at::cuda::currentStreamCaptureStatus() != at::cuda::CaptureStatus::None)
       throw std::runtime_error("run one paged call on this device before capturing one");
+    // a plain tensor whatever the mode of the first call: one made in inference mode could not be cleared outside it
+    const c10::InferenceMode plain(false);
     const at::NoGradGuard no_grad;
     Tensor t = at::zeros({1}, at::TensorOptions().dtype(at::kInt).device(at::kCUDA, device));
     at::cuda::getCurrentCUDAStream(device).synchronize();

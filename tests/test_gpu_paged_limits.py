@@ -1,6 +1,9 @@
 """Paged-cache operators at the ends of what their arguments allow: values that are no numbers, scales, rows
 and lengths out of range, modes of torch that a call has to notice."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -238,3 +241,24 @@ def test_sequences_left_without_rows_by_what_is_out_of_range_are_reported(path, 
             r = slice(bt.cu[b], bt.cu[b + 1])
             one.lens, one.cu, one.n_tok, one.q, one.page_table = [bt.lens[b]], [0, a], a, bt.q[r], bt.page_table[b:b + 1]
             assert_attend((got[0][r], got[1][:, r]), one, prefix=prefix)
+
+
+def test_a_first_call_under_inference_mode_leaves_a_status_that_can_be_cleared():
+    code = """
+import torch
+from rolling_kv_cache_b200 import binding as B, paged
+tables = paged.rope_tables((4,), (32,))
+x = torch.zeros(2, 1, 64, dtype=torch.bfloat16, device="cuda")
+with torch.inference_mode():
+    paged.rope_axes(x, torch.tensor([[9], [0]], dtype=torch.int32, device="cuda"), tables)
+for _ in range(2):
+    try:
+        paged.device_status()
+        print("clear")
+    except B.RcError as e:
+        print("status", e.status)
+"""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+    assert r.stdout.split("\n")[:2] == [f"status {B.RC_ERANGE}", "clear"], r.stdout
