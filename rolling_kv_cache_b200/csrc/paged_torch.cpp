@@ -5,9 +5,12 @@
 // the same marshalling in Python took 16 us of host time, and the rotation's
 // forward and backward 126 us. Every computation is the library's.
 #include <ATen/ATen.h>
+#include <ATen/TracerMode.h>
 #include <ATen/cuda/CUDAContext.h>
 #include <ATen/cuda/CUDAGraphsUtils.cuh>
+#include <c10/core/AutogradState.h>
 #include <c10/core/InferenceMode.h>
+#include <c10/core/impl/TorchDispatchModeTLS.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <torch/csrc/autograd/custom_function.h>
 #include <torch/csrc/utils/pybind.h>
@@ -78,11 +81,19 @@ std::optional<Tensor> existing_word(int device) {
   return w.word[device];
 }
 
-// The one CUDA device that every tensor is on, made current.
+// The one CUDA device that every tensor of a call is on. Refuses what torch would take for an answer although the
+// kernels are not part of it: tangents of forward mode, and recordings of a call.
 struct Device {
   int index = -1;
+  Device() {
+    using c10::impl::TorchDispatchModeKey;
+    if (at::tracer::impl::is_dispatch_enabled() || c10::impl::TorchDispatchModeTLS::get_mode(TorchDispatchModeKey::PROXY))
+      refuse("paged operators cannot be recorded by a trace");
+  }
   void add(const Tensor& t) {
     if (!t.defined()) return;
+    if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
+      refuse("paged operators have no forward-mode derivative");
     if (!t.is_cuda()) refuse("paged operators take CUDA tensors");
     const int i = t.get_device();
     if (index >= 0 && i != index) refuse("tensors on more than one device");

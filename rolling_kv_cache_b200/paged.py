@@ -16,7 +16,8 @@ Everything runs in librc.so's kernels on the current stream of the tensors'
 device; a call allocates its outputs and its workspace from torch's caching
 allocator, so that calls on several streams and captured graphs do not share scratch. Lengths, tables and
 positions are int32 device tensors read when the kernels run. What they hold out of range
-is never followed; ``device_status`` reports it.
+is never followed; ``device_status`` reports it. Tensors with a forward-mode tangent, and calls under
+torch.jit.trace or make_fx, are refused.
 """
 from __future__ import annotations
 
@@ -84,7 +85,7 @@ def rope_axes(x, pos: torch.Tensor, tables: Sequence[torch.Tensor], *, pairing: 
     int32; tables: one [positions, pairs, 2] table of (cos, sin) per axis (``rope_tables``), whose
     pairs sum to head_dim / 2. ``pairing``: pair m turns elements (2m, 2m + 1)
     ("adjacent") or (m, m + head_dim / 2) ("halves"). ``inverse`` turns back.
-    Differentiable in x (the gradient is the turn back). With ``out`` (a tensor
+    Differentiable in x by backward passes (the gradient is the turn back). With ``out`` (a tensor
     or a pair; x itself for in place) the result is written there, outside autograd.
     A leaf whose earlier graph, made on another stream, is alive is refused while
     a CUDA graph is captured.

@@ -262,3 +262,52 @@ for _ in range(2):
     r = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stderr[-2000:]
     assert r.stdout.split("\n")[:2] == [f"status {B.RC_ERANGE}", "clear"], r.stdout
+
+
+def _small(seed):
+    bt = Batch(seed, [(2, 30), (1, 9)], 4, 2, 64, 16)
+    return bt, paged.rope_tables((9,), (32,)), torch.zeros(3, 1, dtype=torch.int32, device="cuda")
+
+
+def test_tangents_of_forward_mode_are_refused():
+    """Also one that comes in by a gradient, forward over backward."""
+    import torch.autograd.forward_ad as fw
+    bt, tables, pos = _small(108)
+    q, k_pages, v_pages, *rest = bt.args()
+    k = randn(bt.gen, 3, 2, 64)
+    with fw.dual_level():
+        dual = lambda t: fw.make_dual(t, torch.ones_like(t))  # noqa: E731
+        calls = [lambda: paged.rope_axes(dual(q), pos, tables), lambda: paged.rope_axes((q, dual(k)), pos, tables),
+                 lambda: paged.rope_axes(dual(q), pos, tables, out=torch.empty_like(q)),
+                 lambda: paged.rope_axes(q, pos, (dual(tables[0]),)),
+                 lambda: paged.paged_append(dual(q), k, k, k_pages, v_pages, *rest),
+                 lambda: paged.paged_append(None, k, dual(k), k_pages, v_pages, *rest),
+                 lambda: paged.paged_attention(dual(q), k_pages, v_pages, *rest, max_q=2),
+                 lambda: paged.paged_attention(q, k_pages, dual(v_pages), *rest, max_q=2)]
+        for call in calls:
+            for mode in (torch.enable_grad, torch.no_grad):
+                with mode(), pytest.raises(ValueError, match="forward-mode"):
+                    call()
+        paged.rope_axes(q, pos, tables)  # plain tensors pass
+        x = q.float().requires_grad_(True)
+        y = paged.rope_axes(x, pos, tables)
+        with pytest.raises((ValueError, RuntimeError), match="forward-mode"):
+            torch.autograd.grad(y, (x,), dual(torch.ones_like(y)))
+        base = torch.zeros(3, 8, 64, dtype=BF16, device="cuda")
+        with pytest.raises(ValueError, match="forward-mode"):  # a view of such a tensor
+            paged.rope_axes(dual(base)[:, :4], pos, tables)
+
+
+def test_calls_under_a_trace_are_refused():
+    from torch.fx.experimental.proxy_tensor import make_fx
+    bt, tables, pos = _small(109)
+    q, k_pages, v_pages, *rest = bt.args()
+    k = randn(bt.gen, 3, 2, 64)
+    for f in (lambda x: paged.rope_axes(x, pos, tables),
+              lambda x: paged.paged_append(x, k, k, k_pages, v_pages, *rest),
+              lambda x: paged.paged_attention(x, k_pages, v_pages, *rest, max_q=2)):
+        with pytest.raises(ValueError, match="trace"):
+            torch.jit.trace(f, (q,), check_trace=False)
+        with pytest.raises(ValueError, match="trace"):
+            make_fx(f)(q)
+        f(q)

@@ -208,3 +208,20 @@ def test_written_rows_in_every_nesting_pass_the_checks():
     for tok, head in ((256, 64), (64, 192), (320, 72), (512, 128), (72, 256)):
         with pytest.raises(B.RcError, match="workspace|device attribute"):
             B.rc_paged_attention(_pool(), m, 3, _rows(), B.rc_rows(P, tok, head, 4), 0, 0, 0)
+
+
+def test_tangents_and_traces_are_refused_on_any_device():
+    import torch.autograd.forward_ad as fw
+
+    x = torch.zeros(3, 2, 64)
+    pos, tables = torch.zeros(3, 1, dtype=torch.int32), paged.rope_tables((4,), (32,), device="cpu")
+    pool, i, table = torch.zeros(4, 2, 16, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(1, 3, dtype=torch.int32)
+    calls = [lambda t: paged.rope_axes(t, pos, tables), lambda t: paged.paged_append(None, t, x, pool, pool, i, i[:1], table),
+             lambda t: paged.paged_attention(t, pool, pool, i, i[:1], table)]
+    for call in calls:
+        with fw.dual_level(), pytest.raises(ValueError, match="forward-mode"):
+            call(fw.make_dual(x, x))
+        with pytest.raises(ValueError, match="trace"):
+            torch.jit.trace(call, (x,), check_trace=False)
+        with pytest.raises(ValueError, match="CUDA"):
+            call(x)
