@@ -121,6 +121,13 @@ rc_rows rows_of(const Tensor& t, const char* what) {
 
 bool is_int32(const Tensor& t, int dim) { return t.scalar_type() == at::kInt && t.dim() == dim; }
 
+// The tables have no gradient: one that is asked for must not come out missing.
+void constant(const Tensors& tables) {
+  if (!at::GradMode::is_enabled()) return;
+  for (const Tensor& t : tables)
+    if (t.requires_grad()) refuse("the rotation tables have no gradient; detach them");
+}
+
 rc_rope rope_of(const Tensor& pos, const Tensors& tables, bool halves, int64_t n_tok, int64_t head_dim) {
   const int64_t n = static_cast<int64_t>(tables.size());
   if (n < 1 || n > 3) refuse("1 to 3 rotation tables");
@@ -289,6 +296,7 @@ Tensors turned(const Tensors& xs, const Tensor& pos, const Tensors& tables, bool
 Tensors rope_axes(const Tensors& xs, const Tensor& pos, const Tensors& tables, bool halves, bool inverse,
                   const std::optional<Tensors>& out) {
   if (xs.empty() || xs.size() > 2) refuse("one tensor or a pair");
+  constant(tables);
   if (!out) return turned(xs, pos, tables, halves, inverse);
   if (out->size() != xs.size()) refuse("one out for each x");
   if (at::GradMode::is_enabled())
@@ -351,6 +359,7 @@ std::optional<Tensor> append(const std::optional<Tensor>& q, const Tensor& k, co
                              const std::optional<Tensor>& q_out) {
   no_grad({q ? &*q : nullptr, &k, &v, &k_pages, &v_pages, q_out ? &*q_out : nullptr});
   if (pos.has_value() != tables.has_value()) refuse("pos and tables go together");
+  if (tables) constant(*tables);
   Device dev;
   for (const Tensor* t : {&k, &v, &k_pages, &v_pages, &cu_q, &kv_len, &page_table}) dev.add(*t);
   dev.add(q);

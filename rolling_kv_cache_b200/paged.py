@@ -85,7 +85,7 @@ def rope_axes(x, pos: torch.Tensor, tables: Sequence[torch.Tensor], *, pairing: 
     int32; tables: one [positions, pairs, 2] table of (cos, sin) per axis (``rope_tables``), whose
     pairs sum to head_dim / 2. ``pairing``: pair m turns elements (2m, 2m + 1)
     ("adjacent") or (m, m + head_dim / 2) ("halves"). ``inverse`` turns back.
-    Differentiable in x by backward passes (the gradient is the turn back). With ``out`` (a tensor
+    Differentiable in x by backward passes (the gradient is the turn back), not in the tables. With ``out`` (a tensor
     or a pair; x itself for in place) the result is written there, outside autograd.
     A leaf whose earlier graph, made on another stream, is alive is refused while
     a CUDA graph is captured.

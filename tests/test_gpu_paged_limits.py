@@ -11,7 +11,7 @@ import torch
 from rolling_kv_cache_b200 import binding as B
 from rolling_kv_cache_b200 import paged
 
-from paged_util import F64, UNIT, Batch, assert_attend, generator, randn, visible
+from paged_util import F64, UNIT, Batch, assert_attend, assert_turned, generator, randn, visible
 
 pytestmark = pytest.mark.gpu
 BF16, F16, F32 = torch.bfloat16, torch.float16, torch.float32
@@ -311,3 +311,18 @@ def test_calls_under_a_trace_are_refused():
         with pytest.raises(ValueError, match="trace"):
             make_fx(f)(q)
         f(q)
+
+
+def test_tables_that_ask_for_a_gradient_are_refused():
+    bt, tables, pos = _small(110)
+    q, k_pages, v_pages, *rest = bt.args()
+    learned = (tables[0].clone().requires_grad_(True),)
+    x = q.float().requires_grad_(True)
+    for t in (q, x):
+        with pytest.raises(ValueError, match="tables"):
+            paged.rope_axes(t, pos, learned)
+    with pytest.raises(ValueError):
+        paged.paged_append(q, q[:, :2], q[:, 2:], k_pages, v_pages, *rest, pos=pos, tables=learned)
+    with torch.no_grad():
+        y = paged.rope_axes(q, pos, learned)
+    assert_turned(y, q, pos, tables, False)

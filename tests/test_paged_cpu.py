@@ -225,3 +225,15 @@ def test_tangents_and_traces_are_refused_on_any_device():
             torch.jit.trace(call, (x,), check_trace=False)
         with pytest.raises(ValueError, match="CUDA"):
             call(x)
+
+
+def test_tables_that_ask_for_a_gradient_are_refused_on_any_device():
+    x, pos = torch.zeros(3, 2, 64), torch.zeros(3, 1, dtype=torch.int32)
+    learned = (paged.rope_tables((4,), (32,), device="cpu")[0].requires_grad_(True),)
+    pool, i, table = torch.zeros(4, 2, 16, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(1, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="tables"):
+        paged.rope_axes(x, pos, learned)
+    with pytest.raises(ValueError, match="tables"):
+        paged.paged_append(None, x, x, pool, pool, i, i[:1], table, pos=pos, tables=learned)
+    with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+        paged.rope_axes(x, pos, learned)
