@@ -82,7 +82,8 @@ std::optional<Tensor> existing_word(int device) {
 }
 
 // The one CUDA device that every tensor of a call is on. Refuses what torch would take for an answer although the
-// kernels are not part of it: tangents of forward mode, and recordings of a call.
+// kernels are not part of it: tangents of forward mode, recordings of a call, and views whose memory holds
+// the values negated.
 struct Device {
   int index = -1;
   Device() {
@@ -94,6 +95,7 @@ struct Device {
     if (!t.defined()) return;
     if (c10::AutogradState::get_tls_state().get_fw_grad_mode() && t._fw_grad(0).defined())
       refuse("paged operators have no forward-mode derivative");
+    if (t.is_neg()) refuse("paged operators do not take negated views (resolve_neg() makes a tensor of one)");
     if (!t.is_cuda()) refuse("paged operators take CUDA tensors");
     const int i = t.get_device();
     if (index >= 0 && i != index) refuse("tensors on more than one device");
@@ -191,15 +193,15 @@ void turn(const Tensors& xs, const Tensors& outs, const Tensor& pos, const Tenso
 }
 
 // The tensor itself where the kernels can read it, else a contiguous copy (a
-// gradient may come expanded, transposed or at any offset).
+// gradient may come expanded, transposed, negated or at any offset).
 Tensor readable(const Tensor& t) {
-  if (t.dim() == 3 && t.stride(2) == 1) {
+  if (t.dim() == 3 && t.stride(2) == 1 && !t.is_neg()) {
     const int64_t size = t.element_size();
     if (t.stride(0) >= 0 && t.stride(1) >= 0 && t.stride(0) * size % 16 == 0 && t.stride(1) * size % 16 == 0 &&
         reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0)
       return t;
   }
-  return t.clone(at::MemoryFormat::Contiguous);
+  return t.resolve_neg().clone(at::MemoryFormat::Contiguous);
 }
 
 Tensors turned(const Tensors& xs, const Tensor& pos, const Tensors& tables, bool halves, bool inverse);

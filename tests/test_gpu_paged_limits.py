@@ -326,3 +326,18 @@ def test_tables_that_ask_for_a_gradient_are_refused():
     with torch.no_grad():
         y = paged.rope_axes(q, pos, learned)
     assert_turned(y, q, pos, tables, False)
+
+
+def test_negated_views_are_refused_and_their_gradients_read():
+    bt, tables, pos = _small(111)
+    q, k_pages, v_pages, *rest = bt.args()
+    for call in (lambda: paged.rope_axes(torch._neg_view(q), pos, tables),
+                 lambda: paged.rope_axes(q, pos, tables, out=torch._neg_view(torch.empty_like(q))),
+                 lambda: paged.paged_append(None, torch._neg_view(q[:, :2]), q[:, 2:], k_pages, v_pages, *rest),
+                 lambda: paged.paged_attention(torch._neg_view(q), k_pages, v_pages, *rest, max_q=2)):
+        with pytest.raises(ValueError, match="negated"):
+            call()
+    x = q.float().requires_grad_(True)
+    gy = randn(bt.gen, 3, 4, 64, dtype=F32)
+    (dx,) = torch.autograd.grad(paged.rope_axes(x, pos, tables), (x,), torch._neg_view(gy))
+    assert_turned(dx, -gy, pos, tables, False, inverse=True)

@@ -237,3 +237,13 @@ def test_tables_that_ask_for_a_gradient_are_refused_on_any_device():
         paged.paged_append(None, x, x, pool, pool, i, i[:1], table, pos=pos, tables=learned)
     with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
         paged.rope_axes(x, pos, learned)
+
+
+def test_negated_views_are_refused_on_any_device():
+    x, pos = torch._neg_view(torch.zeros(3, 2, 64)), torch.zeros(3, 1, dtype=torch.int32)
+    pool, i, table = torch.zeros(4, 2, 16, 64), torch.zeros(2, dtype=torch.int32), torch.zeros(1, 3, dtype=torch.int32)
+    for call in (lambda: paged.rope_axes(x, pos, paged.rope_tables((4,), (32,), device="cpu")),
+                 lambda: paged.paged_append(None, x, x, pool, pool, i, i[:1], table),
+                 lambda: paged.paged_attention(x, pool, pool, i, i[:1], table)):
+        with pytest.raises(ValueError, match="negated"):
+            call()
