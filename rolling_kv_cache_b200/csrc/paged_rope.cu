@@ -202,8 +202,8 @@ __device__ __forceinline__ int seq_of(const BatchView& v, int tok) {
 
 // The append: head index hh walks the query heads (turned, to q_out), then
 // the key heads (turned, into the token's page row), then the value heads
-// (copied there). Tokens behind the last sequence are left alone; a token
-// whose place does not exist (a position before 0, past the table, or an
+// (copied there). Tokens behind the last sequence are left alone, those of no sequence before
+// that too, with RC_ERANGE; a token whose place does not exist (a position before 0, past the table, or an
 // entry that is no page) keeps its keys and values out of the pool and
 // records RC_ERANGE.
 template <int DT, int D, bool HALVES>
@@ -215,6 +215,9 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const __grid
   const long long g = idx / LN;
   if (g >= (long long)p.n_tok * p.splits) return;
   const int tok = (int)(g / p.splits), s0 = (int)(g - (long long)tok * p.splits);
+  // sequences that begin before the first row or end behind the last
+  if (idx == 0 && p.status && (__ldg(p.b.cu_q) != 0 || __ldg(p.b.cu_q + p.b.n_seqs) > p.n_tok))
+    atomicCAS(p.status, 0, (int)RC_ERANGE);
   const int Hq = p.q.heads, Hk = p.k.heads, NH = Hq + 2 * Hk;
   const bool rotate = p.ax.n_axes > 0;
   float c[E], s[E];
@@ -253,7 +256,10 @@ __global__ void __launch_bounds__(kRopeThreads) paged_append_kernel(const __grid
         if (rotate) load_angles<E, LN, HALVES>(p.ax, tok, lane, 1.f, p.status, c, s);
       }
     }
-    if (!inside) break;
+    if (!inside) {  // of no sequence, and before the last one's end
+      if (p.status && tok < __ldg(p.b.cu_q + p.b.n_seqs)) atomicCAS(p.status, 0, (int)RC_ERANGE);
+      break;
+    }
 #pragma unroll
     for (int i = 0; i < kUnroll; ++i) {
       const int hh = h0 + i * p.splits;

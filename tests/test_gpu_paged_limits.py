@@ -341,3 +341,19 @@ def test_negated_views_are_refused_and_their_gradients_read():
     gy = randn(bt.gen, 3, 4, 64, dtype=F32)
     (dx,) = torch.autograd.grad(paged.rope_axes(x, pos, tables), (x,), torch._neg_view(gy))
     assert_turned(dx, -gy, pos, tables, False, inverse=True)
+
+
+@pytest.mark.parametrize("cu,n_tok", [([0, 3, 7], 3), ([2, 3, 5], 5), ([3, 3, 5], 5), ([0, 3, 7], 6)])
+def test_an_append_reports_rows_of_no_sequence_and_rows_that_are_not_there(cu, n_tok):
+    bt = Batch(107, [(max(0, e - s), 40) for s, e in zip(cu, cu[1:])], 4, 2, 64, 16, fill=3.0)
+    k, v = randn(bt.gen, n_tok, 2, 64), randn(bt.gen, n_tok, 2, 64)
+    kp, vp = bt.k_pages.clone(), bt.v_pages.clone()
+    for b in range(2):
+        for tok in range(cu[b], min(cu[b + 1], n_tok)):
+            at = 40 - (cu[b + 1] - tok)
+            kp[int(bt.page_table[b, at // 16]), :, at % 16] = k[tok]
+            vp[int(bt.page_table[b, at // 16]), :, at % 16] = v[tok]
+    cu_q = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    paged.paged_append(None, k, v, bt.k_pages, bt.v_pages, cu_q, bt.kv_len, bt.page_table)
+    _reported()
+    assert torch.equal(bt.k_pages, kp) and torch.equal(bt.v_pages, vp)
