@@ -4,6 +4,7 @@ import math
 import os
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -357,3 +358,80 @@ def test_an_append_reports_rows_of_no_sequence_and_rows_that_are_not_there(cu, n
     paged.paged_append(None, k, v, bt.k_pages, bt.v_pages, cu_q, bt.kv_len, bt.page_table)
     _reported()
     assert torch.equal(bt.k_pages, kp) and torch.equal(bt.v_pages, vp)
+
+
+def test_threads_on_streams_of_their_own_finish_with_the_same_bits():
+    batches = [Batch(112, [(1, 900), (1, 40)] * 6, 8, 2, 128, 16), Batch(113, [(130, 400), (31, 31)], 8, 2, 128, 16)]
+    want = [_attend(b, max(a for a, _ in b.lens)) for b in batches]
+    torch.cuda.synchronize()
+    done, errors = [0, 0], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(20):
+                    got = _attend(batches[i], max(a for a, _ in batches[i].lens))
+                    torch.cuda.current_stream().synchronize()
+                    assert torch.equal(got[0], want[i][0]) and torch.equal(got[1], want[i][1])
+                    done[i] += 1
+        except BaseException as e:  # reported by the main thread
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,), daemon=True) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(timeout=300)
+        assert not t.is_alive()
+    assert not errors and done == [20, 20], errors
+
+
+def test_a_captured_append_reports_a_replay_without_a_page():
+    bt = Batch(114, [(1, 30), (1, 90)], 4, 2, 64, 16, fill=3.0)
+    k, v = randn(bt.gen, 2, 2, 64), randn(bt.gen, 2, 2, 64)
+    call = lambda: paged.paged_append(None, k, v, bt.k_pages, bt.v_pages, bt.cu_q, bt.kv_len, bt.page_table)  # noqa: E731
+    call()
+    paged.device_status()
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        call()
+    kp = bt.k_pages.clone()
+    bt.kv_len.fill_(55)  # the first sequence has two pages
+    k.fill_(1.0)
+    gr.replay()
+    kp[int(bt.page_table[1, 3]), :, 54 % 16] = 1.0
+    _reported()
+    assert torch.equal(bt.k_pages, kp)
+
+
+@pytest.mark.parametrize("cu", [[0, 5, 2, 6], [0, 2, 500, 6], [-3, 2, 5, 6], [4, 4, 4, 2 ** 31 - 1]])
+def test_an_append_of_rows_listed_out_of_order_writes_their_places_only(cu):
+    """A token goes to the sequence that a bisection for the last start at or before it finds, if it lies in that."""
+    bt = Batch(115, [(2, 40), (3, 30), (1, 9)], 4, 2, 64, 16, fill=3.0)
+    k, v = randn(bt.gen, 6, 2, 64), randn(bt.gen, 6, 2, 64)
+    kp, vp = bt.k_pages.clone(), bt.v_pages.clone()
+    places = set()
+    for tok in range(6):
+        lo, hi = 0, 2
+        while lo < hi:
+            mid = (lo + hi + 1) >> 1
+            lo, hi = (mid, hi) if cu[mid] <= tok else (lo, mid - 1)
+        at = bt.lens[lo][1] - (cu[lo + 1] - tok)
+        if not cu[lo] <= tok < cu[lo + 1] or at < 0:
+            continue
+        page = int(bt.page_table[lo, at // 16])
+        assert (page, at % 16) not in places
+        places.add((page, at % 16))
+        if page >= 0:
+            kp[page, :, at % 16], vp[page, :, at % 16] = k[tok], v[tok]
+    paged.paged_append(None, k, v, bt.k_pages, bt.v_pages, torch.tensor(cu, dtype=torch.int32, device="cuda"), bt.kv_len,
+                       bt.page_table)
+    torch.cuda.synchronize()
+    assert torch.equal(bt.k_pages, kp) and torch.equal(bt.v_pages, vp)
+    if cu[0] != 0 or cu[-1] > 6 or max(cu) > 6:
+        _reported()
+    else:
+        try:
+            paged.device_status()
+        except B.RcError as e:
+            assert e.status == B.RC_ERANGE
