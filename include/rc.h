@@ -470,16 +470,16 @@ typedef struct rc_paged {
 /* y = x turned by its positions, or back (inverse != 0: the transpose, which
  * is the gradient with respect to x). Up to two tensors (queries and keys) in
  * one launch: x[1].heads = 0 for one. y may be x with x's strides, else must not
- * overlap it. Positions out of their table are clamped to it. */
+ * overlap it, nor the other y. Positions out of their table are clamped to it. */
 rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, int inverse, const rc_rows x[2],
                        const rc_rows y[2], int32_t* status, void* stream);
 
 /* Appends a batch's new tokens: writes the turned keys and the values into
  * their page rows and the turned queries to q_out (q, q_out: heads = 0 for
- * none; q_out may be q). Without rotation (rope NULL or n_axes 0) all three are copied. A
+ * none; q_out may be q; what is written, q_out and both pools, overlaps nothing else). Without rotation (rope NULL or n_axes 0) all three are copied. A
  * token whose place is none (position below 0 or past the table row, an entry outside
- * [0, n_pages)) is kept out of the pool. Two tokens of one call with the same
- * place: one of them is kept. */
+ * [0, n_pages)) is kept out of the pool. Two tokens of one call must not have the same
+ * place: its rows would be a mix of theirs. */
 rc_status rc_paged_append(const rc_paged* p, const rc_rope* rope, int n_tok, const rc_rows* q, const rc_rows* k,
                           const rc_rows* v, const rc_rows* q_out, int32_t* status, void* stream);
 

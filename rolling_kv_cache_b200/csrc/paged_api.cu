@@ -325,6 +325,8 @@ rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, 
       p.x[i] = view(x[i], size);
       p.y[i] = view(y[i], size);
     }
+    if (n_tok > 0 && y[0].heads > 0 && y[1].heads > 0 && y[0].data == y[1].data)
+      return invalid("y: the two tensors are one");
     p.status = status;
     p.n_tok = n_tok;
     p.sign = inverse ? -1.f : 1.f;
@@ -352,6 +354,7 @@ rc_status rc_paged_append(const rc_paged* pg, const rc_rope* rope, int n_tok, co
       if (!apart({{st[0], pg->n_pages}, {st[1], pg->kv_heads}, {st[2], pg->page_size}}, pg->head_dim))
         return invalid("the pages' rows overlap");
     if (k->heads != pg->kv_heads || v->heads != pg->kv_heads) return invalid("k and v must have the pool's heads");
+    if (pg->k_pages == pg->v_pages) return invalid("k_pages and v_pages are one tensor");
     p.q = view(*q, 2);
     p.q_out = view(*q_out, 2);
     p.k = view(*k, 2);

@@ -86,7 +86,7 @@ def rope_axes(x, pos: torch.Tensor, tables: Sequence[torch.Tensor], *, pairing: 
     pairs sum to head_dim / 2. ``pairing``: pair m turns elements (2m, 2m + 1)
     ("adjacent") or (m, m + head_dim / 2) ("halves"). ``inverse`` turns back.
     Differentiable in x by backward passes (the gradient is the turn back), not in the tables. With ``out`` (a tensor
-    or a pair; x itself for in place) the result is written there, outside autograd.
+    or a pair that do not overlap; x itself for in place) the result is written there, outside autograd.
     A leaf whose earlier graph, made on another stream, is alive is refused while
     a CUDA graph is captured.
     """
@@ -111,7 +111,7 @@ def paged_append(q: Optional[torch.Tensor], k: torch.Tensor, v: torch.Tensor, k_
     q [tokens, q_heads, d] (or None), k, v [tokens, kv_heads, d], strided as they
     come from a fused projection; ``kv_len`` counts the new tokens already.
     Returns the turned queries (``q_out`` if given; q itself for in place). Two
-    tokens of one call must not share a place.
+    tokens of one call must not share a place: its rows would be a mix of theirs.
     """
     if pairing not in _HALVES:
         raise ValueError("pairing must be 'adjacent' or 'halves'")

@@ -247,3 +247,11 @@ def test_negated_views_are_refused_on_any_device():
                  lambda: paged.paged_attention(x, pool, pool, i, i[:1], table)):
         with pytest.raises(ValueError, match="negated"):
             call()
+
+
+def test_a_tensor_given_for_two_outputs_is_refused():
+    one, two = _rows(), _rows(2)
+    for fn, args in ((B.rc_rope_axes, (_rope(), B.RC_BF16, 3, 64, 0, (B.rc_rows * 2)(one, one), (B.rc_rows * 2)(one, one))),
+                     (B.rc_paged_append, (_pool(), None, 3, one, two, two, one))):
+        with pytest.raises(B.RcError, match="are one"):
+            fn(*args)
