@@ -513,7 +513,9 @@ rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n
  * windows, rows not written yet) do not reach the result whatever their bits;
  * a key that some query sees must be finite, or the NaN it makes reaches that
  * query and can reach queries of the same sequence that do not see it.
- *   lse: NULL or [q_heads][n_tok] fp32, natural log.
+ * A score of +inf makes NaN as well, one of -inf has the weight 0.
+ *   lse: NULL or [q_heads][n_tok] fp32, natural log; infinite where scale times the largest
+ *   score passes 2e38 (out is right there too: weights go by differences of scores).
  *   out may be q (same strides), else must not overlap it.
  * max_q * (q_heads / kv_heads) <= 16 takes the kernel for few rows; it
  * computes no more than that many, so max_q must not be below the longest

@@ -156,6 +156,8 @@ def _assert_exact_scores(got, bt, scale, prefix=None):
             err = (out[r, h].to(F64) - o).abs()
             assert bool((err <= tol).all()), (b, h, float(err.max()))
             ls = torch.logsumexp(x, -1)
+            if float(ls.abs().max()) > 2e38:
+                continue
             ltol = 2.0 ** -21 * (ls.abs() + 1) + rel.sum(1)
             assert bool(((lse[h, r].to(F64) - ls).abs() <= ltol).all()), (b, h)
 
@@ -180,6 +182,40 @@ def test_large_scales_over_a_prefix(case, scale):
     prefix = _prefix(bt, n)
     _one_axis(bt)
     _assert_exact_scores(_attend(bt, max_q, prefix, scale=scale), bt, scale, prefix)
+
+
+@pytest.mark.parametrize("path", ["clusters", "cut", "many"])
+@pytest.mark.parametrize("dtype,d", [(BF16, 128), (F16, 64)])
+def test_scores_that_pass_fp32_with_the_scale_still_weigh(path, dtype, d):
+    """Their log-sum-exp is infinite in fp32; the weights go by differences of the scores."""
+    a = 30 if path == "many" else 2
+    bt = Batch(117, [(a, 1000), (a, 300), (a, 40)], 4, 2, d, 16, dtype)
+    if path == "cut":
+        bt.page_table = _wide(bt)
+    _one_axis(bt)
+    bt.q[..., 0] *= 2 ** 13
+    bt.k_pages[..., 0] *= 2 ** 12
+    o, lse = _attend(bt, a, scale=1e30)
+    _assert_exact_scores((o, lse), bt, 1e30)
+    # 1000 keys of 255 values: a largest score above 7.5 2^25, with the scale 3.6e38 to the base 2
+    assert bool(torch.isinf(lse[:, a - 1]).all()) and not bool(lse.isnan().any())
+
+
+@pytest.mark.parametrize("path", ["clusters", "cut", "many"])
+def test_a_score_of_minus_infinity_has_no_weight(path):
+    a = 30 if path == "many" else 2
+    bt = Batch(118, [(a, 500), (a, 90)], 4, 2, 64, 16)
+    if path == "cut":
+        bt.page_table = _wide(bt)
+    bt.q[..., 0] = 1
+    at = [(int(bt.page_table[0, j // 16]), j % 16) for j in (0, 17, 63, 400)]
+    got = []
+    for value in (-3e38, -math.inf):
+        for page, row in at:
+            bt.k_pages[page, :, row, 0] = value
+        got.append(_attend(bt, a))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert bool(torch.isfinite(got[1][0]).all()) and bool(torch.isfinite(got[1][1]).all())
 
 
 @pytest.mark.parametrize("path", ["clusters", "cut", "many"])
