@@ -504,7 +504,8 @@ typedef struct rc_paged_mask {
 } rc_paged_mask;
 
 /* Bytes of workspace rc_paged_attention needs (256-byte aligned, contents not
- * kept or read from call to call; 0: none). It depends on the device only by its SMs. */
+ * kept or read from call to call; 0: none). It depends on the current device, by its SMs and by how many
+ * clusters of blocks it runs at once: ask on the device that runs the call. */
 rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n_tok, int q_heads, size_t* bytes);
 
 /* out = softmax(scale q k^T + mask) v over the batch's pages. Query head h

@@ -25,7 +25,7 @@
 // exponentials of the second do (video chunk 847 -> 818 us; a third step, 851).
 //
 // Measured: 4680 queries against 18 frames of 1560 keys, 12 heads of 128, 852 GFLOP:
-// 811 us, 1050 TFLOP/s; tensor pipe and exponentials are each 54 % busy, a tile's
+// 912 us, 934 TFLOP/s back to back (835 us the first times, before the power cap); tensor pipe and exponentials are each 54 % busy, a tile's
 // softmax (from S to P) being longer than the other tile's two products beside it.
 //
 // Schedule, found by every CTA from the lengths on the device: units in
@@ -852,7 +852,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) paged_prefill_kernel(const __g
         // P is rounded to the values' type, the product's operand: off by at most
         // 2^-8 (bf16) or 2^-11 (fp16) of each weight; the sum l is taken before it.
         // Every exponential is the SFU's: with one pair in eight or two on the FMA pipe the
-        // video chunk takes 834 and 835 us instead of 819
+        // video chunk takes 834 and 835 us instead of 819 (head_dim 128; 64, which has half the products
+        // to as many exponentials, was not measured)
         const float ref = m == -INFINITY ? 0.f : m;
         float ce = c, re = ref * c;
         if (steep) {

@@ -45,7 +45,7 @@ constexpr int kDecThreads = (kConsumers + 2) * 32;  // and two producers
 constexpr int kRingBytes = 128 * 1024;
 constexpr float kDecRescaleLog2 = 8.f;
 // What a unit costs beside its tiles, in tiles (its queries, its merge and its
-// writes: 4500 cycles to a tile's 1500)
+// writes: 5000 cycles to a tile's 1500)
 constexpr int kUnitCost = 3;
 constexpr int kMaxCluster = 8;
 
