@@ -454,10 +454,10 @@ typedef struct rc_paged {
   int64_t v_stride[3];
   int32_t n_pages;
   int32_t page_size;      /* 16, 32, 64 or 128 */
-  int32_t kv_heads;
+  int32_t kv_heads;       /* at most 1024; the attention's query heads: a multiple, up to 128 to each */
   int32_t head_dim;       /* 64 or 128 */
   int32_t dtype;          /* RC_BF16 or RC_F16 */
-  int32_t n_seqs;
+  int32_t n_seqs;         /* at most 4096 */
   const int32_t* cu_q;    /* [n_seqs + 1], ascending from 0 (where it descends, the attention's results
                              are undefined, with RC_ERANGE in *status; rows before
                              cu_q[0] are left as they are, with RC_ERANGE) */
@@ -476,8 +476,9 @@ rc_status rc_rope_axes(const rc_rope* rope, int dtype, int n_tok, int head_dim, 
 
 /* Appends a batch's new tokens: writes the turned keys and the values into
  * their page rows and the turned queries to q_out (q, q_out: heads = 0 for
- * none; q_out may be q; what is written, q_out and both pools, overlaps nothing else). Without rotation (rope NULL or n_axes 0) all three are copied. A
- * token whose place is none (position below 0 or past the table row, an entry outside
+ * none; q_out may be q, and otherwise what is written, q_out and both pools, overlaps
+ * nothing). Without rotation (rope NULL or n_axes 0) all three are copied. A token
+ * whose place is none (position below 0 or past the table row, an entry outside
  * [0, n_pages)) is kept out of the pool. Two tokens of one call must not have the same
  * place: its rows would be a mix of theirs. */
 rc_status rc_paged_append(const rc_paged* p, const rc_rope* rope, int n_tok, const rc_rows* q, const rc_rows* k,
@@ -515,8 +516,8 @@ rc_status rc_paged_workspace(const rc_paged* p, const rc_paged_mask* mask, int n
  * a key that some query sees must be finite, or the NaN it makes reaches that
  * query and can reach queries of the same sequence that do not see it.
  * A score of +inf makes NaN as well, one of -inf has the weight 0.
- *   lse: NULL or [q_heads][n_tok] fp32, natural log; infinite where scale times the largest
- *   score passes 2e38 (out is right there too: weights go by differences of scores).
+ *   lse: NULL or [q_heads][n_tok] fp32, natural log; infinite where scale times the largest score
+ *   passes 2e38 (out is right there too: weights go by differences of scores).
  *   out may be q (same strides), else must not overlap it.
  * max_q * (q_heads / kv_heads) <= 16 takes the kernel for few rows; it
  * computes no more than that many, so max_q must not be below the longest

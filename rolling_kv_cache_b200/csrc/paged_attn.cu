@@ -25,8 +25,9 @@
 // exponentials of the second do (video chunk 847 -> 818 us; a third step, 851).
 //
 // Measured: 4680 queries against 18 frames of 1560 keys, 12 heads of 128, 852 GFLOP:
-// 912 us, 934 TFLOP/s back to back (835 us the first times, before the power cap); tensor pipe and exponentials are each 54 % busy, a tile's
-// softmax (from S to P) being longer than the other tile's two products beside it.
+// 912 us, 934 TFLOP/s back to back (835 us the first times, before the power cap); tensor
+// pipe and exponentials are each 54 % busy, a tile's softmax (from S to P) being longer than
+// the other tile's two products beside it.
 //
 // Schedule, found by every CTA from the lengths on the device: units in
 // (sequence, key head, pair) order; CTA c of G first takes whole units c, c + G,

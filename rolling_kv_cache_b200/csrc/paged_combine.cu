@@ -1,6 +1,6 @@
 // Merges the parts of the units that the paged attention kernels cut between
-// CTAs: O = sum_i w_i O_i, w_i = l_i 2^(c m_i) / sum_k l_k 2^(c m_k) with each part's sum l_i 2^(c m_i) (RowSum), in fp32 and
-// in a fixed order. Block (c, y) takes rows of the unit that begins in CTA
+// CTAs: O = sum_i w_i O_i, w_i = l_i 2^(c m_i) / sum_k l_k 2^(c m_k) with each part's
+// sum l_i 2^(c m_i) (RowSum), in fp32 and in a fixed order. Block (c, y) takes rows of the unit that begins in CTA
 // c's range and goes on in the next; the unit's parts are slot 2c + 1 and
 // slots 2(c + 1), 2(c + 2), ... up to the CTA whose record says that the unit
 // ends there. First every part's weight for every row, in shared memory, then
@@ -172,7 +172,8 @@ template <int D, bool BF16>
 __global__ void __launch_bounds__(kCombThreads) paged_join_kernel(const __grid_constant__ JoinParams p) {
   constexpr int kChunks = D / 8;
   __shared__ int first_sh[3], last_sh[3];  // the decode unit's, and the first and last token's pair's
-  // small enough that two blocks are resident beside the decode kernel's (with the sums here too, twice as much, one: 0.7 us)
+  // small enough that two blocks are resident beside the decode kernel's (with the sums' other
+  // halves here too, one: 0.7 us more)
   __shared__ float scratch[kJoinSources * kDecodeRows];
   __shared__ float most_sh[kCombThreads / 32][kDecodeRows], l_sh[kCombThreads / 32][kDecodeRows];  // each warp's, of the rows
   __shared__ uint8_t there[2][kMaxPersistentCtas];  // the CTAs' records' flags

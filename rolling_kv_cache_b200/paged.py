@@ -7,7 +7,7 @@ batch of streams whose keys and values live in pages of one pool,
 strides with a contiguous last dimension). Token i of sequence b is row
 ``i % page_size`` of page ``page_table[b, i // page_size]``. Queries are packed:
 sequence b owns rows ``cu_q[b]:cu_q[b + 1]``, its last tokens, and ``kv_len[b]``
-counts its tokens in the pages, those among them. A decoding step is::
+counts its tokens in the pages, those among them. A call takes up to 4096 sequences. A decoding step is::
 
     q = paged_append(q, k, v, k_pages, v_pages, cu_q, kv_len, page_table, pos=pos, tables=tables)
     out = paged_attention(q, k_pages, v_pages, cu_q, kv_len, page_table, max_q=1)
